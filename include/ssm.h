@@ -375,6 +375,137 @@ int selective_state_update(const ssm_scan_desc *desc, float *s, const void *x, c
                            const float *conv_w, float *conv_state, void *y, uint32_t *err,
                            ssm_stream_t stream);
 
+/* ---- around the scan in a block -------------------------------------------
+ * The operators that stand next to the scan in a Mamba block: the norm
+ * between two blocks, the gated norm after the scan, activation checkpoints
+ * in 8 bits, and a projection's weight gradient from such a checkpoint.
+ * The pages define none of them; their formulas are those given here.
+ *
+ * They work on [n_rows][width] matrices, a row a token.  A row stride (ld, in
+ * elements, >= the width; 0: the width) lets a matrix be a slice of a wider
+ * one, as z, x, B, C and dt are of the projection's output.  Elements need
+ * their own alignment only; checkpoints need 16 bytes.  n_rows may be 0:
+ * column sums are then written as zero.  A NaN or an infinity in a row stays
+ * in that row's outputs and in the column sums.  Statistics and sums are f32;
+ * a result is rounded once, to nearest even, when it is stored.  Sums over
+ * rows have a fixed order: results repeat bitwise. */
+
+enum { SSM_NORM_GATE_AFTER = 1u }; /* gated norm: the gate multiplies the normalised value */
+
+typedef struct ssm_norm_desc {
+    int64_t n_rows;     /* rows (>= 0); n_rows * n_group <= 2^31 - 1              */
+    int64_t width;      /* columns (>= 1)                                         */
+    int64_t n_group;    /* gated norm: groups of width / n_group columns (at most
+                           32768), each with its own rms; residual norm: 1        */
+    int64_t ld_x;       /* row stride of y and d_y, or of b and d_b               */
+    int64_t ld_z;       /* row stride of z and d_z                                */
+    int64_t ld_res;     /* row stride of r, r_out, dr_out and d_r                 */
+    int64_t ld_out;     /* row stride of out and dout, or of h and dh             */
+    int32_t io_dtype;   /* ssm_dtype of every matrix but the residual stream      */
+    int32_t res_dtype;  /* ssm_dtype of r, r_out, dr_out, d_r: io's, or f32       */
+    float eps;          /* > 0                                                    */
+    float res_scale;    /* constant factor of the branch (residual norm); else 1  */
+    uint32_t flags;     /* SSM_NORM_GATE_AFTER (gated norm)                       */
+    uint32_t reserved;  /* must be 0                                              */
+} ssm_norm_desc;
+
+/* The 8-bit checkpoint of an [n_rows][width] matrix: e4m3 codes in blocks of
+ * 32 along the row, each block with one scale byte k + 127 where k >= -127 is
+ * the smallest integer with max|x| <= 448 * 2^k over the block's finite
+ * values; code = e4m3(x / 2^k) rounded to nearest even, so a value is off by
+ * at most 2^-4 of itself, or by 2^(k - 10) below 2^(k - 6).  A NaN or an
+ * infinity is kept as NaN; with k = 120 a magnitude is at most 240 * 2^k, so
+ * that it reads back finite.  In memory: codes [n_rows][W32], W32 = width
+ * rounded up to 32 (zeros past width), then scale bytes [n_rows][W32 / 32].
+ * Returns its size in bytes; *scale_offset (may be NULL) receives the offset
+ * of the scale bytes.  0 for bad dimensions (or no rows). */
+size_t ssm_ckpt8_bytes(int64_t n_rows, int64_t width, size_t *scale_offset);
+
+/* ckpt8_pack writes the checkpoint of x (dtype: ssm_dtype, row stride ld);
+ * ckpt8_unpack writes code * 2^k to x: exact in f32 and in bf16 (below 2^-126
+ * as far as the type's subnormals go). */
+int ssm_ckpt8_pack(const void *x, int64_t ld, int64_t n_rows, int64_t width, int32_t dtype,
+                   void *ckpt, ssm_stream_t stream);
+int ssm_ckpt8_unpack(const void *ckpt, void *x, int64_t ld, int64_t n_rows, int64_t width,
+                     int32_t dtype, ssm_stream_t stream);
+
+/* ssm_ckpt8_wgrad: the weight gradient of out = x W^T from dy = d out
+ * [n_rows][n_out] (dtype, row stride ld) and the checkpoint of x
+ * [n_rows][width]:
+ *   dw[o][c] = sum_m dy[m][o] x[m][c]   (+ dw[o][c] when accumulate != 0)
+ * dw [n_out][width] f32, dense.  Products are exact and summed in f32.
+ * width and n_out are at most 2^22.  workspace:
+ * ssm_ckpt8_wgrad_workspace_bytes bytes, 256-byte aligned, no initial
+ * contents (may be NULL when that is 0). */
+size_t ssm_ckpt8_wgrad_workspace_bytes(int64_t n_rows, int64_t width, int64_t n_out, int32_t dtype);
+int ssm_ckpt8_wgrad(const void *dy, int64_t ld, const void *ckpt, float *dw, int64_t n_rows,
+                    int64_t width, int64_t n_out, int32_t dtype, int32_t accumulate,
+                    void *workspace, size_t workspace_bytes, ssm_stream_t stream);
+
+/* ssm_norm_gated_fwd: the gated norm after the scan, per row and group
+ *   u = y SiLU(z),  out = u rstd w                    (default)
+ *   out = y rstd w SiLU(z),  rstd of y                (SSM_NORM_GATE_AFTER)
+ * with rstd = 1 / sqrt(mean(u^2) + eps) over the group's columns.
+ *  - y, z, out [n_rows][width] io (z may be NULL: no gate), w [width] f32.
+ *  - rstd [n_rows][n_group] f32 (may be NULL): the backward's input.
+ *  - y8, z8, out8 (each may be NULL): receive the 8-bit checkpoints of y, z
+ *    and out, as ssm_ckpt8_pack writes them; with groups, width / n_group
+ *    must then be a multiple of 32, else SSM_ERR_UNSUPPORTED. */
+int ssm_norm_gated_fwd(const ssm_norm_desc *desc, const void *y, const void *z, const float *w,
+                       void *out, float *rstd, void *y8, void *z8, void *out8, ssm_stream_t stream);
+
+/* Workspace of the two norms' backwards (bytes; 256-byte aligned, no initial
+ * contents; it may be NULL when no column sum is asked for). */
+size_t ssm_norm_bwd_workspace_bytes(const ssm_norm_desc *desc);
+
+/* ssm_norm_gated_bwd: its backward.  With x = u rstd (or y rstd), mean over
+ * the group, s = sigmoid(z), G = SiLU(z) and G' = s (1 + z (1 - s)):
+ *   default:  dn = dout w;    du = rstd (dn - x mean(dn x));
+ *             d_y = du G;  d_z = du y G';  d_w = sum_rows dout x
+ *   after:    dn = dout G w;  d_y = rstd (dn - x mean(dn x));
+ *             d_z = dout x w G';  d_w = sum_rows dout G x
+ *  - y or its checkpoint y8 is given, not both; the same for z (neither: no
+ *    gate).  rstd is the forward's, also with checkpoints.
+ *  - d_y, d_z io, d_w [width] f32: each may be NULL.  A gradient has the row
+ *    stride of its tensor. */
+int ssm_norm_gated_bwd(const ssm_norm_desc *desc, const void *dout, const void *y, const void *z,
+                       const void *y8, const void *z8, const float *w, const float *rstd, void *d_y,
+                       void *d_z, float *d_w, void *workspace, size_t workspace_bytes,
+                       ssm_stream_t stream);
+
+/* ssm_norm_residual_fwd: between two blocks, per row
+ *   t = b,  or  b rstd_post w_post                    (w_post: norm after the block)
+ *   r_out = r + res_scale * scale * t                 (scale [width] f32, or NULL: 1)
+ *   h = r_out rstd w                                  (norm before the next block)
+ * with rstd = 1 / sqrt(mean(r_out^2) + eps), from r_out before it is rounded,
+ * and rstd_post the same of b.
+ *  - b, h io; r, r_out in res_dtype; b may be NULL (h is then the norm of r)
+ *    and r may be NULL (zeros), not both.  r_out may be NULL, or r itself.
+ *  - rstd [n_rows], rstd_post [n_rows] f32: may be NULL.
+ *  - r8, b8, h8 (each may be NULL): the 8-bit checkpoints of r_out and h as
+ *    they are stored, and of b.
+ *  - io f32 with res bf16 is SSM_ERR_UNSUPPORTED. */
+int ssm_norm_residual_fwd(const ssm_norm_desc *desc, const void *b, const void *r, const float *w_post,
+                          const float *scale, const float *w, void *r_out, void *h, float *rstd,
+                          float *rstd_post, void *r8, void *b8, void *h8, ssm_stream_t stream);
+
+/* ssm_norm_residual_bwd: its backward, from dh and dr_out (NULL: zeros).  With
+ * x = r_out rstd, v = b rstd_post and means over the row:
+ *   dn = dh w;  d_r = rstd (dn - x mean(dn x)) + dr_out;  d_w = sum_rows dh x
+ *   dt = res_scale scale d_r;  d_scale = sum_rows res_scale d_r t
+ *   d_b = dt,  or  rstd_post (dm - v mean(dm v)), dm = dt w_post, and
+ *   d_w_post = sum_rows dt v
+ *  - r_out or its checkpoint r8 is given, not both; with w_post or d_scale
+ *    also b or its checkpoint b8.  rstd and rstd_post are the forward's.
+ *  - d_r in res_dtype (it may be dr_out itself), d_b io, d_w, d_w_post,
+ *    d_scale [width] f32: each may be NULL. */
+int ssm_norm_residual_bwd(const ssm_norm_desc *desc, const void *dh, const void *dr_out,
+                          const void *r_out, const void *r8, const void *b, const void *b8,
+                          const float *w_post, const float *scale, const float *w, const float *rstd,
+                          const float *rstd_post, void *d_r, void *d_b, float *d_w, float *d_w_post,
+                          float *d_scale, void *workspace, size_t workspace_bytes,
+                          ssm_stream_t stream);
+
 /* Copies the device-error word of a workspace to *bits (synchronises the
  * stream; for tests and debugging, not for the hot path). */
 int ssm_get_device_error(const void *workspace, ssm_stream_t stream, uint32_t *bits);

@@ -12,4 +12,7 @@ from ._binding import (  # noqa: F401
     ssm_conv_bwd, ssm_conv_bwd_workspace_bytes, ssm_conv_fwd, ssm_get_device_error,
     ssm_scan_dgrad_layout, ssm_scan_fwd_plan, ssm_scan_out_bytes,
     ssm_scan_state_offset_bytes, ssm_scan_workspace_bytes, ssm_status_str, ssm_version,
+    SSM_NORM_GATE_AFTER, SsmNormDesc, ssm_ckpt8_bytes, ssm_ckpt8_pack, ssm_ckpt8_unpack,
+    ssm_ckpt8_wgrad, ssm_ckpt8_wgrad_workspace_bytes, ssm_norm_bwd_workspace_bytes,
+    ssm_norm_gated_bwd, ssm_norm_gated_fwd, ssm_norm_residual_bwd, ssm_norm_residual_fwd,
 )

@@ -17,6 +17,7 @@ SSM_OK, SSM_ERR_NULL, SSM_ERR_SHAPE, SSM_ERR_DTYPE, SSM_ERR_UNSUPPORTED, \
     SSM_ERR_WORKSPACE, SSM_ERR_ALIGN, SSM_ERR_HIP = range(8)
 SSM_F32, SSM_BF16 = 0, 1
 SSM_HAS_D, SSM_DT_SOFTPLUS = 1, 2
+SSM_NORM_GATE_AFTER = 1
 SSM_DEVERR_IDS, SSM_DEVERR_SEQLENS, SSM_DEVERR_RELAY = 1, 2, 4
 
 EXPORTS = ("ssm_status_str", "ssm_version", "ssm_scan_out_bytes", "ssm_scan_state_offset_bytes",
@@ -24,7 +25,10 @@ EXPORTS = ("ssm_status_str", "ssm_version", "ssm_scan_out_bytes", "ssm_scan_stat
            "ssm_conv_bwd_workspace_bytes", "ssm_conv_bwd", "selective_scan_fwd",
            "selective_scan_bwd", "selective_state_update", "ssm_get_device_error",
            "ssm_scan_ext_out_bytes", "selective_scan_fwd_ext", "ssm_scan_fwd_plan",
-           "selective_scan_fwd_static", "selective_scan_bwd_conv")
+           "selective_scan_fwd_static", "selective_scan_bwd_conv", "ssm_ckpt8_bytes",
+           "ssm_ckpt8_pack", "ssm_ckpt8_unpack", "ssm_ckpt8_wgrad_workspace_bytes",
+           "ssm_ckpt8_wgrad", "ssm_norm_gated_fwd", "ssm_norm_bwd_workspace_bytes",
+           "ssm_norm_gated_bwd", "ssm_norm_residual_fwd", "ssm_norm_residual_bwd")
 
 
 class SsmError(RuntimeError):
@@ -46,6 +50,16 @@ class SsmScanDesc(ctypes.Structure):
 class SsmScanExt(ctypes.Structure):
     _fields_ = [("dt_bias", ctypes.c_void_p), ("z", ctypes.c_void_p),
                 ("cu_seqlens", ctypes.c_void_p), ("total_tokens", ctypes.c_int64)]
+
+
+class SsmNormDesc(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("n_group", ctypes.c_int64), ("ld_x", ctypes.c_int64),
+                ("ld_z", ctypes.c_int64), ("ld_res", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
 
 
 _lib = None
@@ -98,6 +112,23 @@ def load():
         lib.ssm_scan_fwd_plan.restype = ctypes.c_char_p
         lib.ssm_get_device_error.argtypes = [P, P, ctypes.POINTER(ctypes.c_uint32)]
         lib.ssm_get_device_error.restype = ctypes.c_int
+        lib.ssm_ckpt8_bytes.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+        lib.ssm_ckpt8_bytes.restype = SZ
+        lib.ssm_ckpt8_pack.argtypes = [P, I64, I64, I64, I32, P, P]
+        lib.ssm_ckpt8_unpack.argtypes = [P, P, I64, I64, I64, I32, P]
+        lib.ssm_ckpt8_wgrad_workspace_bytes.argtypes = [I64, I64, I64, I32]
+        lib.ssm_ckpt8_wgrad_workspace_bytes.restype = SZ
+        lib.ssm_ckpt8_wgrad.argtypes = [P, I64, P, P, I64, I64, I64, I32, I32, P, SZ, P]
+        N = ctypes.POINTER(SsmNormDesc)
+        lib.ssm_norm_bwd_workspace_bytes.argtypes = [N]
+        lib.ssm_norm_bwd_workspace_bytes.restype = SZ
+        lib.ssm_norm_gated_fwd.argtypes = [N] + [P] * 9
+        lib.ssm_norm_gated_bwd.argtypes = [N] + [P] * 11 + [SZ, P]
+        lib.ssm_norm_residual_fwd.argtypes = [N] + [P] * 13
+        lib.ssm_norm_residual_bwd.argtypes = [N] + [P] * 17 + [SZ, P]
+        for fn in ("ssm_ckpt8_pack", "ssm_ckpt8_unpack", "ssm_ckpt8_wgrad", "ssm_norm_gated_fwd",
+                   "ssm_norm_gated_bwd", "ssm_norm_residual_fwd", "ssm_norm_residual_bwd"):
+            getattr(lib, fn).restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -241,6 +272,75 @@ def selective_state_update(desc, s, x, dt, dt_bias, A, B, C, D, z, ids, conv_w, 
                                        _ptr(ids), _ptr(conv_w), _ptr(conv_state), _ptr(y),
                                        _ptr(err), _stream(stream))
     return _check(rc, "selective_state_update")
+
+
+def ssm_ckpt8_bytes(n_rows, width):
+    """(size in bytes, offset of the scale bytes); (0, 0) for bad dimensions."""
+    off = ctypes.c_size_t(0)
+    n = load().ssm_ckpt8_bytes(int(n_rows), int(width), ctypes.byref(off))
+    return int(n), int(off.value)
+
+
+def ssm_ckpt8_pack(x, ld, n_rows, width, dtype, ckpt, stream=None):
+    rc = load().ssm_ckpt8_pack(_ptr(x), int(ld), int(n_rows), int(width), int(dtype), _ptr(ckpt),
+                               _stream(stream))
+    return _check(rc, "ssm_ckpt8_pack")
+
+
+def ssm_ckpt8_unpack(ckpt, x, ld, n_rows, width, dtype, stream=None):
+    rc = load().ssm_ckpt8_unpack(_ptr(ckpt), _ptr(x), int(ld), int(n_rows), int(width), int(dtype),
+                                 _stream(stream))
+    return _check(rc, "ssm_ckpt8_unpack")
+
+
+def ssm_ckpt8_wgrad_workspace_bytes(n_rows, width, n_out, dtype) -> int:
+    return load().ssm_ckpt8_wgrad_workspace_bytes(int(n_rows), int(width), int(n_out), int(dtype))
+
+
+def ssm_ckpt8_wgrad(dy, ld, ckpt, dw, n_rows, width, n_out, dtype, accumulate, workspace,
+                    workspace_bytes, stream=None):
+    rc = load().ssm_ckpt8_wgrad(_ptr(dy), int(ld), _ptr(ckpt), _ptr(dw), int(n_rows), int(width),
+                                int(n_out), int(dtype), int(accumulate), _ptr(workspace),
+                                int(workspace_bytes), _stream(stream))
+    return _check(rc, "ssm_ckpt8_wgrad")
+
+
+def ssm_norm_bwd_workspace_bytes(desc: SsmNormDesc) -> int:
+    return load().ssm_norm_bwd_workspace_bytes(ctypes.byref(desc))
+
+
+def ssm_norm_gated_fwd(desc, y, z, w, out, rstd, y8, z8, out8, stream=None):
+    rc = load().ssm_norm_gated_fwd(ctypes.byref(desc), _ptr(y), _ptr(z), _ptr(w), _ptr(out),
+                                   _ptr(rstd), _ptr(y8), _ptr(z8), _ptr(out8), _stream(stream))
+    return _check(rc, "ssm_norm_gated_fwd")
+
+
+def ssm_norm_gated_bwd(desc, dout, y, z, y8, z8, w, rstd, d_y, d_z, d_w, workspace,
+                       workspace_bytes, stream=None):
+    rc = load().ssm_norm_gated_bwd(ctypes.byref(desc), _ptr(dout), _ptr(y), _ptr(z), _ptr(y8),
+                                   _ptr(z8), _ptr(w), _ptr(rstd), _ptr(d_y), _ptr(d_z), _ptr(d_w),
+                                   _ptr(workspace), int(workspace_bytes), _stream(stream))
+    return _check(rc, "ssm_norm_gated_bwd")
+
+
+def ssm_norm_residual_fwd(desc, b, r, w_post, scale, w, r_out, h, rstd, rstd_post, r8, b8, h8,
+                          stream=None):
+    rc = load().ssm_norm_residual_fwd(ctypes.byref(desc), _ptr(b), _ptr(r), _ptr(w_post),
+                                      _ptr(scale), _ptr(w), _ptr(r_out), _ptr(h), _ptr(rstd),
+                                      _ptr(rstd_post), _ptr(r8), _ptr(b8), _ptr(h8),
+                                      _stream(stream))
+    return _check(rc, "ssm_norm_residual_fwd")
+
+
+def ssm_norm_residual_bwd(desc, dh, dr_out, r_out, r8, b, b8, w_post, scale, w, rstd, rstd_post,
+                          d_r, d_b, d_w, d_w_post, d_scale, workspace, workspace_bytes,
+                          stream=None):
+    rc = load().ssm_norm_residual_bwd(ctypes.byref(desc), _ptr(dh), _ptr(dr_out), _ptr(r_out),
+                                      _ptr(r8), _ptr(b), _ptr(b8), _ptr(w_post), _ptr(scale),
+                                      _ptr(w), _ptr(rstd), _ptr(rstd_post), _ptr(d_r), _ptr(d_b),
+                                      _ptr(d_w), _ptr(d_w_post), _ptr(d_scale), _ptr(workspace),
+                                      int(workspace_bytes), _stream(stream))
+    return _check(rc, "ssm_norm_residual_bwd")
 
 
 def ssm_get_device_error(workspace, stream=None) -> int:

@@ -189,3 +189,332 @@ def state_update(desc, s, x, dt, A, Bm, Cm, D, ids, *, dt_bias=None, z=None, con
     B.selective_state_update(desc, s, x, dt, dt_bias, A, Bm, Cm, D, z, ids, conv_w, conv_state, y,
                              err, stream)
     return y
+
+
+# ---- around the scan in a block: norms, 8-bit checkpoints, weight gradient ----
+#
+# These take [n_rows][width] tensors whose last axis is contiguous; the row
+# stride may be larger (a slice of the projection's output).  What the C ABI
+# cannot see of a tensor -- its shape, strides, type and device -- is checked
+# here, with the ABI's status codes.
+
+
+def _refuse(status, where, name, t):
+    raise B.SsmError(status, f"{where}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, "
+                             f"strides {t.stride()}")
+
+
+def _matrix(where, name, t, rows, width, ld, dtype):
+    """t is None or [rows][width] in dtype with row stride ld."""
+    if t is None:
+        return
+    if t.dtype is not dtype:
+        _refuse(B.SSM_ERR_DTYPE, where, name, t)
+    if t.shape != (rows, width) or (rows > 1 and t.stride(0) != ld) or \
+            (width > 1 and rows > 0 and t.stride(1) != 1):
+        _refuse(B.SSM_ERR_SHAPE, where, name, t)
+    if not t.is_cuda:
+        _refuse(B.SSM_ERR_UNSUPPORTED, where, name, t)
+
+
+def _dense(where, name, t, numel, dtype):
+    """t is None or a contiguous tensor of at least numel elements."""
+    if t is None:
+        return
+    if t.dtype is not dtype:
+        _refuse(B.SSM_ERR_DTYPE, where, name, t)
+    if t.numel() < numel or not t.is_contiguous():
+        _refuse(B.SSM_ERR_SHAPE, where, name, t)
+    if not t.is_cuda:
+        _refuse(B.SSM_ERR_UNSUPPORTED, where, name, t)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor in the memory of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _matrix_like(rows, width, ld, dtype, device, stream):
+    if ld == width or rows < 2:
+        return _empty((rows, width), dtype, device, stream)
+    return _empty((rows, ld), dtype, device, stream)[:, :width]
+
+
+def _io_of(t, where):
+    if t.dtype is torch.bfloat16:
+        return B.SSM_BF16
+    if t.dtype is torch.float32:
+        return B.SSM_F32
+    _refuse(B.SSM_ERR_DTYPE, where, "the tensor", t)
+
+
+def ckpt8_bytes(n_rows, width) -> int:
+    return B.ssm_ckpt8_bytes(n_rows, width)[0]
+
+
+def ckpt8_empty(n_rows, width, device="cuda", stream=None) -> torch.Tensor:
+    """Memory for the 8-bit checkpoint of an [n_rows][width] tensor."""
+    return _empty((ckpt8_bytes(n_rows, width),), torch.uint8, device, stream)
+
+
+def ckpt8_pack(x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """The 8-bit checkpoint of x [n_rows][width] (f32 or bf16)."""
+    where = "ckpt8_pack"
+    io, (rows, width) = _io_of(x, where), x.shape
+    ld = x.stride(0) if rows > 1 else width
+    _matrix(where, "x", x, rows, width, ld, x.dtype)
+    if out is None:
+        out = ckpt8_empty(rows, width, x.device, stream)
+    _dense(where, "out", out, ckpt8_bytes(rows, width), torch.uint8)
+    B.ssm_ckpt8_pack(x, ld, rows, width, io, out, stream)
+    return out
+
+
+def ckpt8_unpack(ckpt: torch.Tensor, n_rows, width, io="bf16", out=None, stream=None) -> torch.Tensor:
+    """The values an 8-bit checkpoint holds, [n_rows][width] in out's type (io
+    without out)."""
+    where = "ckpt8_unpack"
+    _dense(where, "ckpt", ckpt, ckpt8_bytes(n_rows, width), torch.uint8)
+    if out is None:
+        out = _empty((n_rows, width), TORCH_IO[IO_DTYPES[io]], ckpt.device, stream)
+    ld = out.stride(0) if n_rows > 1 else width
+    _matrix(where, "out", out, n_rows, width, ld, out.dtype)
+    B.ssm_ckpt8_unpack(ckpt, out, ld, n_rows, width, _io_of(out, where), stream)
+    return out
+
+
+def ckpt8_wgrad_workspace(n_rows, width, n_out, io="bf16", device="cuda", stream=None) -> torch.Tensor:
+    n = B.ssm_ckpt8_wgrad_workspace_bytes(n_rows, width, n_out, IO_DTYPES[io])
+    return _empty((max(n, 4),), torch.uint8, device, stream)
+
+
+def ckpt8_wgrad(dy: torch.Tensor, ckpt: torch.Tensor, width, *, dw=None, accumulate=False, ws=None,
+                stream=None) -> torch.Tensor:
+    """Weight gradient dw [n_out][width] (f32) of out = x W^T from dy
+    [n_rows][n_out] and the 8-bit checkpoint of x [n_rows][width]; added to dw
+    with accumulate."""
+    where = "ckpt8_wgrad"
+    io, (rows, n_out) = _io_of(dy, where), dy.shape
+    ld = dy.stride(0) if rows > 1 else n_out
+    _matrix(where, "dy", dy, rows, n_out, ld, dy.dtype)
+    _dense(where, "ckpt", ckpt, ckpt8_bytes(rows, width), torch.uint8)
+    if dw is None:
+        if accumulate:
+            raise B.SsmError(B.SSM_ERR_NULL, f"{where}: accumulate without dw")
+        dw = _empty((n_out, width), torch.float32, dy.device, stream)
+    _dense(where, "dw", dw, n_out * width, torch.float32)
+    if ws is None:
+        n = B.ssm_ckpt8_wgrad_workspace_bytes(rows, width, n_out, io)
+        ws = _empty((n,), torch.uint8, dy.device, stream)
+    B.ssm_ckpt8_wgrad(dy, ld, ckpt, dw, rows, width, n_out, io, bool(accumulate), ws,
+                      ws.numel(), stream)
+    return dw
+
+
+def norm_desc(*, n_rows, width, n_group=1, io="bf16", res="f32", eps=1e-5, res_scale=1.0,
+              gate_after=False, ld_x=0, ld_z=0, ld_res=0, ld_out=0) -> B.SsmNormDesc:
+    """Descriptor of the two norms.  ld_x, ld_z, ld_res, ld_out: row strides in
+    elements (0: width) of y or b, of z, of the residual stream, and of out or
+    h; a gradient has its tensor's."""
+    def dtype(v):
+        return IO_DTYPES[v] if isinstance(v, str) else int(v)
+
+    return B.SsmNormDesc(int(n_rows), int(width), int(n_group), int(ld_x) or int(width),
+                         int(ld_z) or int(width), int(ld_res) or int(width),
+                         int(ld_out) or int(width), dtype(io), dtype(res), float(eps),
+                         float(res_scale), B.SSM_NORM_GATE_AFTER if gate_after else 0, 0)
+
+
+def norm_bwd_workspace(desc: B.SsmNormDesc, device="cuda", stream=None) -> torch.Tensor:
+    n = B.ssm_norm_bwd_workspace_bytes(desc)
+    if n == 0:
+        raise B.SsmError(B.SSM_ERR_SHAPE, "ssm_norm_bwd_workspace_bytes")
+    return _empty((n,), torch.uint8, device, stream)
+
+
+@dataclass
+class NormGatedResult:
+    out: torch.Tensor              # [n_rows][width] io
+    rstd: Optional[torch.Tensor]   # [n_rows][n_group] f32
+    y8: Optional[torch.Tensor]     # 8-bit checkpoints of y, z and out
+    z8: Optional[torch.Tensor]
+    out8: Optional[torch.Tensor]
+
+
+def norm_gated_fwd(desc, y, z, w, *, train=False, out=None, rstd=None, y8=None, z8=None, out8=None,
+                   stream=None) -> NormGatedResult:
+    """The gated norm after the scan (ssm_norm_gated_fwd).  train: also what
+    the backward needs, rstd and the 8-bit checkpoints y8 and z8, in new
+    tensors where none is given."""
+    where, M, W, io = "norm_gated_fwd", desc.n_rows, desc.width, TORCH_IO[desc.io_dtype]
+    _matrix(where, "y", y, M, W, desc.ld_x, io)
+    _matrix(where, "z", z, M, W, desc.ld_z, io)
+    _dense(where, "w", w, W, torch.float32)
+    if out is None:
+        out = _matrix_like(M, W, desc.ld_out, io, y.device, stream)
+    else:
+        _matrix(where, "out", out, M, W, desc.ld_out, io)
+    if train:
+        rstd = _empty((M, desc.n_group), torch.float32, y.device, stream) if rstd is None else rstd
+        y8 = ckpt8_empty(M, W, y.device, stream) if y8 is None else y8
+        if z is not None:
+            z8 = ckpt8_empty(M, W, y.device, stream) if z8 is None else z8
+    _dense(where, "rstd", rstd, M * desc.n_group, torch.float32)
+    if y8 is not None or z8 is not None or out8 is not None:
+        n = ckpt8_bytes(M, W)
+        _dense(where, "y8", y8, n, torch.uint8)
+        _dense(where, "z8", z8, n, torch.uint8)
+        _dense(where, "out8", out8, n, torch.uint8)
+    B.ssm_norm_gated_fwd(desc, y, z, w, out, rstd, y8, z8, out8, stream)
+    return NormGatedResult(out, rstd, y8, z8, out8)
+
+
+@dataclass
+class NormGatedGrad:
+    d_y: torch.Tensor
+    d_z: Optional[torch.Tensor]
+    d_w: torch.Tensor
+
+
+def norm_gated_bwd(desc, dout, w, rstd, *, y=None, z=None, y8=None, z8=None, d_y=None, d_z=None,
+                   d_w=None, ws=None, stream=None) -> NormGatedGrad:
+    """Backward of ``norm_gated_fwd`` from y and z or their 8-bit checkpoints."""
+    where, M, W, io = "norm_gated_bwd", desc.n_rows, desc.width, TORCH_IO[desc.io_dtype]
+    _matrix(where, "dout", dout, M, W, desc.ld_out, io)
+    _matrix(where, "y", y, M, W, desc.ld_x, io)
+    _matrix(where, "z", z, M, W, desc.ld_z, io)
+    _dense(where, "w", w, W, torch.float32)
+    _dense(where, "rstd", rstd, M * desc.n_group, torch.float32)
+    if y8 is not None or z8 is not None:
+        n = ckpt8_bytes(M, W)
+        _dense(where, "y8", y8, n, torch.uint8)
+        _dense(where, "z8", z8, n, torch.uint8)
+    if d_y is None:
+        d_y = _matrix_like(M, W, desc.ld_x, io, dout.device, stream)
+    else:
+        _matrix(where, "d_y", d_y, M, W, desc.ld_x, io)
+    if d_z is not None:
+        _matrix(where, "d_z", d_z, M, W, desc.ld_z, io)
+    elif z is not None or z8 is not None:
+        d_z = _matrix_like(M, W, desc.ld_z, io, dout.device, stream)
+    if d_w is None:
+        d_w = _empty((W,), torch.float32, dout.device, stream)
+    else:
+        _dense(where, "d_w", d_w, W, torch.float32)
+    if ws is None:
+        ws = norm_bwd_workspace(desc, dout.device, stream)
+    B.ssm_norm_gated_bwd(desc, dout, y, z, y8, z8, w, rstd, d_y, d_z, d_w, ws, ws.numel(), stream)
+    return NormGatedGrad(d_y, d_z, d_w)
+
+
+@dataclass
+class NormResidualResult:
+    r_out: torch.Tensor                # [n_rows][width] residual stream
+    h: torch.Tensor                    # [n_rows][width] io
+    rstd: Optional[torch.Tensor]       # [n_rows] f32
+    rstd_post: Optional[torch.Tensor]  # [n_rows] f32, with w_post
+    r8: Optional[torch.Tensor]         # 8-bit checkpoints of r_out, b and h
+    b8: Optional[torch.Tensor]
+    h8: Optional[torch.Tensor]
+
+
+def norm_residual_fwd(desc, b, r, w, *, w_post=None, scale=None, train=False, r_out=None, h=None,
+                      rstd=None, rstd_post=None, r8=None, b8=None, h8=None,
+                      stream=None) -> NormResidualResult:
+    """The norm between two blocks (ssm_norm_residual_fwd): the branch b into
+    the residual stream r, and the stream's norm for the next block.  train:
+    also what the backward needs, rstd, rstd_post and the 8-bit checkpoints r8
+    and (with w_post or scale) b8, and h8 for the next projection's weight
+    gradient, in new tensors where none is given.  r_out may be r."""
+    where, M, W = "norm_residual_fwd", desc.n_rows, desc.width
+    io, res = TORCH_IO[desc.io_dtype], TORCH_IO[desc.res_dtype]
+    _matrix(where, "b", b, M, W, desc.ld_x, io)
+    _matrix(where, "r", r, M, W, desc.ld_res, res)
+    _dense(where, "w", w, W, torch.float32)
+    _dense(where, "w_post", w_post, W, torch.float32)
+    _dense(where, "scale", scale, W, torch.float32)
+    if r_out is None:
+        r_out = _matrix_like(M, W, desc.ld_res, res, w.device, stream)
+    else:
+        _matrix(where, "r_out", r_out, M, W, desc.ld_res, res)
+    if h is None:
+        h = _matrix_like(M, W, desc.ld_out, io, w.device, stream)
+    else:
+        _matrix(where, "h", h, M, W, desc.ld_out, io)
+    if train:
+        rstd = _empty((M,), torch.float32, w.device, stream) if rstd is None else rstd
+        if w_post is not None and rstd_post is None:
+            rstd_post = _empty((M,), torch.float32, w.device, stream)
+        r8 = ckpt8_empty(M, W, w.device, stream) if r8 is None else r8
+        h8 = ckpt8_empty(M, W, w.device, stream) if h8 is None else h8
+        if (w_post is not None or scale is not None) and b8 is None:
+            b8 = ckpt8_empty(M, W, w.device, stream)
+    _dense(where, "rstd", rstd, M, torch.float32)
+    _dense(where, "rstd_post", rstd_post, M, torch.float32)
+    if r8 is not None or b8 is not None or h8 is not None:
+        n = ckpt8_bytes(M, W)
+        _dense(where, "r8", r8, n, torch.uint8)
+        _dense(where, "b8", b8, n, torch.uint8)
+        _dense(where, "h8", h8, n, torch.uint8)
+    B.ssm_norm_residual_fwd(desc, b, r, w_post, scale, w, r_out, h, rstd, rstd_post, r8, b8, h8,
+                            stream)
+    return NormResidualResult(r_out, h, rstd, rstd_post, r8, b8, h8)
+
+
+@dataclass
+class NormResidualGrad:
+    d_r: torch.Tensor
+    d_b: torch.Tensor
+    d_w: torch.Tensor
+    d_w_post: Optional[torch.Tensor]
+    d_scale: Optional[torch.Tensor]
+
+
+def norm_residual_bwd(desc, dh, w, rstd, *, dr_out=None, r_out=None, r8=None, b=None, b8=None,
+                      rstd_post=None, w_post=None, scale=None, d_r=None, d_b=None, d_w=None,
+                      d_w_post=None, d_scale=None, ws=None, stream=None) -> NormResidualGrad:
+    """Backward of ``norm_residual_fwd`` from r_out or its 8-bit checkpoint
+    (and b or its, with w_post or scale).  d_r may be dr_out."""
+    where, M, W = "norm_residual_bwd", desc.n_rows, desc.width
+    io, res = TORCH_IO[desc.io_dtype], TORCH_IO[desc.res_dtype]
+    _matrix(where, "dh", dh, M, W, desc.ld_out, io)
+    _matrix(where, "dr_out", dr_out, M, W, desc.ld_res, res)
+    _matrix(where, "r_out", r_out, M, W, desc.ld_res, res)
+    _matrix(where, "b", b, M, W, desc.ld_x, io)
+    _dense(where, "w", w, W, torch.float32)
+    _dense(where, "w_post", w_post, W, torch.float32)
+    _dense(where, "scale", scale, W, torch.float32)
+    _dense(where, "rstd", rstd, M, torch.float32)
+    _dense(where, "rstd_post", rstd_post, M, torch.float32)
+    if r8 is not None or b8 is not None:
+        n = ckpt8_bytes(M, W)
+        _dense(where, "r8", r8, n, torch.uint8)
+        _dense(where, "b8", b8, n, torch.uint8)
+    if d_r is None:
+        d_r = _matrix_like(M, W, desc.ld_res, res, dh.device, stream)
+    else:
+        _matrix(where, "d_r", d_r, M, W, desc.ld_res, res)
+    if d_b is None:
+        d_b = _matrix_like(M, W, desc.ld_x, io, dh.device, stream)
+    else:
+        _matrix(where, "d_b", d_b, M, W, desc.ld_x, io)
+    if d_w is None:
+        d_w = _empty((W,), torch.float32, dh.device, stream)
+    if w_post is not None and d_w_post is None:
+        d_w_post = _empty((W,), torch.float32, dh.device, stream)
+    if scale is not None and d_scale is None:
+        d_scale = _empty((W,), torch.float32, dh.device, stream)
+    _dense(where, "d_w", d_w, W, torch.float32)
+    _dense(where, "d_w_post", d_w_post, W, torch.float32)
+    _dense(where, "d_scale", d_scale, W, torch.float32)
+    if ws is None:
+        ws = norm_bwd_workspace(desc, dh.device, stream)
+    B.ssm_norm_residual_bwd(desc, dh, dr_out, r_out, r8, b, b8, w_post, scale, w, rstd, rstd_post,
+                            d_r, d_b, d_w, d_w_post, d_scale, ws, ws.numel(), stream)
+    return NormResidualGrad(d_r, d_b, d_w, d_w_post, d_scale)
