@@ -104,7 +104,7 @@ static int check_wgrad(int64_t n_rows, int64_t width, int64_t n_out, int32_t dty
     int64_t t;
     if (!known(dtype)) return SSM_ERR_DTYPE;
     if (check_ckpt(n_rows, width) || n_rows > INT_MAX - 1024 || n_out < 1 || n_out > 1 << 22 ||
-        width > 1 << 22 || !mul_ok(n_out, width, &t) || !mul_ok(t, 8, &t))
+        width > 1 << 22 || !mul_ok(n_out, width, &t) || t > (int64_t)1 << 37)
         return SSM_ERR_SHAPE;
     return SSM_OK;
 }
@@ -119,7 +119,7 @@ int ssm_ckpt8_wgrad(const void* dy, int64_t ld, const void* ckpt, float* dw, int
                     void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
     const int rc = check_wgrad(n_rows, width, n_out, dtype);
     if (rc) return rc;
-    if (!stride_ok(n_rows, n_out, &ld)) return SSM_ERR_SHAPE;
+    if (!stride_ok(n_rows, n_out, &ld) || ld > 1 << 26) return SSM_ERR_SHAPE;
     const size_t need = ssm_ckpt8_wgrad_workspace_bytes(n_rows, width, n_out, dtype);
     if (!dw || (n_rows > 0 && (!dy || !ckpt)) || (need && !workspace)) return SSM_ERR_NULL;
     if (workspace_bytes < need) return SSM_ERR_WORKSPACE;

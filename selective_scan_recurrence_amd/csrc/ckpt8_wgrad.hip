@@ -1,68 +1,306 @@
 // Weight gradient of a projection whose input was kept as an 8-bit checkpoint:
 //   dw[o][c] = sum_m dy[m][o] x[m][c] (+ dw[o][c]),  x = code * 2^k.
-// A workgroup owns a 64 x 64 tile of dw and walks the rows 16 at a time.
+// Both operands run along the summed axis m with their slow axis, so both
+// have to be transposed for the MFMA, whose lanes want 8 consecutive m of one
+// column.  A code times its scale fits bf16, so the products are exact; an f32
+// dy enters as three bf16 terms (24 bits), with three MFMAs.
+//
+// A workgroup (4 waves) owns 256 (o) x 128 (c) of dw, wave w the rows 64w ..
+// 64w + 63, and walks m in steps of 64:
+//   dy: a wave's 64 columns are its own, so they go from memory to its
+//     registers past LDS: lane 16g + i loads columns 4i .. 4i + 3 of the rows
+//     8g .. 8g + 7 of a 32-row half step and pairs rows with one byte permute
+//     a register.  Its four columns belong to four MFMA tiles: tile t takes
+//     columns 4i + t, i = 0 .. 15.
+//   x: all four waves need all 128 columns: a thread converts 8 rows of 4
+//     columns, pairs them the same way and writes a column's 8 rows as one
+//     16-byte piece to LDS, which the waves read as MFMA operands.  Column c's
+//     piece q sits at c' * 128 + 16 (q ^ (c / 4 % 8)) bytes, c' = c ^ (c / 32
+//     % 2): the 8 lanes of a write (c = 4 l + t) and of a read (tile j, lane
+//     i: c = 4i + j % 4 + 64 (j / 4)) then meet 8 different 16-byte columns.
+// With few tiles the rows are split over workgroups, each of which leaves an
+// f32 partial in the workspace, and a second kernel adds them in order.
 #include "block_internal.h"
 #include "norm_rows.h"
 
 namespace ssm {
 namespace {
 
-constexpr int kT = 64, kK = 16;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTO = 256, kTC = 128, kTM = 64;
+
+struct WgradP {
+    const void* dy;
+    const uint8_t* x8;
+    float* out;        // dw, or the partials [splits][O][W]
+    int64_t ld, scale_off;
+    int M, W, W32, O;
+    int tiles_c, tiles;   // tiles along c, tiles in all
+    int rows;             // rows a split, a multiple of kTM
+    bool accumulate;
+};
+
+// dword with row a's 16-bit half h below row b's
+__device__ __forceinline__ uint32_t pair_rows(uint32_t a, uint32_t b, int h) {
+    return __builtin_amdgcn_perm(b, a, h ? 0x07060302u : 0x05040100u);
+}
+
+// A half step's dy of a lane: rows 8g .. 8g + 7, 4 columns.
+template <typename T>
+struct DyRaw;
+template <>
+struct DyRaw<bf16_t> {
+    static constexpr int kTerms = 1;
+    u32x2 r[8];
+    __device__ __forceinline__ void zero(int j) { r[j] = u32x2{0, 0}; }
+    __device__ __forceinline__ void frags(u32x4 f[1][4]) const {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) f[0][t][p] = pair_rows(r[2 * p][t / 2], r[2 * p + 1][t / 2], t & 1);
+    }
+};
+template <>
+struct DyRaw<float> {
+    static constexpr int kTerms = 3;
+    u32x4 r[8];
+    __device__ __forceinline__ void zero(int j) { r[j] = u32x4{0, 0, 0, 0}; }
+    // v = hi + mid + lo, each the bf16 nearest to what is left; an infinity or
+    // a NaN is all in hi
+    __device__ __forceinline__ void frags(u32x4 f[3][4]) const {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                uint32_t w[3][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v = __uint_as_float(r[2 * p + h][t]);
+                    const bool finite = fabsf(v) < __builtin_inff();
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) {
+                        w[n][h] = bf16_rne(v);
+                        v = finite ? v - to_f32((bf16_t)w[n][h]) : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 3; ++n) f[n][t][p] = w[n][0] | w[n][1] << 16;
+            }
+    }
+};
 
 template <typename T>
-__global__ __launch_bounds__(256) void wgrad_tile(const T* __restrict__ dy, int64_t ld, const uint8_t* __restrict__ x8,
-                                                  float* dw, int64_t M, int W, int W32, int O, int64_t scale_off,
-                                                  bool accumulate) {
-    __shared__ float a[kK][kT], b[kK][kT];
-    const int o0 = blockIdx.y * kT, c0 = blockIdx.x * kT, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int64_t m0 = 0; m0 < M; m0 += kK) {
-        for (int i = threadIdx.x; i < kK * kT; i += 256) {
-            const int r = i / kT, e = i % kT;
-            const int64_t m = m0 + r;
-            a[r][e] = m < M && o0 + e < O ? to_f32(dy[m * ld + o0 + e]) : 0.0f;
-            float v = 0.0f;
-            if (m < M && c0 + e < W) {
-                const uint8_t code = x8[m * W32 + c0 + e];
-                const uint8_t s = x8[scale_off + m * (W32 / 32) + (c0 + e) / 32];
-                v = __builtin_amdgcn_cvt_pk_f32_fp8((int)code, false)[0] * ckpt8_scale(s);
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP p) {
+    constexpr int NT = DyRaw<T>::kTerms;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][kTC * kTM * 2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int i16 = lane & 15, g = lane >> 4;
+    // XCD-ordered numbering (workgroups are dealt to the 8 XCDs in turn): an
+    // XCD's workgroups are neighbouring tiles, c fastest, that share dy and x
+    const uint32_t n_wg = gridDim.x, pid = blockIdx.x;
+    const uint32_t per = n_wg / 8, extra = n_wg % 8, xcd = pid % 8;
+    const uint32_t id = xcd * per + min(xcd, extra) + pid / 8;
+    const int split = id / p.tiles, tile = id % p.tiles;
+    const int o0 = tile / p.tiles_c * kTO + 64 * wave, c0 = tile % p.tiles_c * kTC;
+    const int m_begin = split * p.rows, m_end = min(p.M, m_begin + p.rows);
+
+    // dy: columns past O are never stored, so a lane past the end takes the
+    // last four columns; with fewer than four columns in all, column by column
+    const bool narrow = p.O < 4;
+    const int col = narrow ? 0 : min(o0 + 4 * i16, p.O - 4);
+    const T* dy = static_cast<const T*>(p.dy);
+    DyRaw<T> raw[2];
+    auto load_dy = [&](DyRaw<T>& d, int m0, bool tail) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int m = m0 + 8 * g + j;
+            if (narrow) {
+                T v[4];
+                for (int t = 0; t < 4; ++t) v[t] = dy[(int64_t)min(m, p.M - 1) * p.ld + min(t, p.O - 1)];
+                __builtin_memcpy(&d.r[j], v, sizeof v);
+            } else if (tail) {
+                __builtin_memcpy(&d.r[j], dy + (int64_t)min(m, p.M - 1) * p.ld + col, sizeof d.r[j]);
+            } else {
+                const T* base = dy + (int64_t)(m0 + j) * p.ld;
+                __builtin_memcpy(&d.r[j], base + (uint32_t)(8 * g * (int)p.ld + col), sizeof d.r[j]);
             }
-            b[r][e] = v;
+            if (tail && m >= m_end) d.zero(j);
         }
-        __syncthreads();
-        for (int r = 0; r < kK; ++r)
+    };
+    // x: thread (octet of rows, 4 columns)
+    const int cl = tid & 31, octet = tid >> 5;
+    const int xc = min(c0 + 4 * cl, p.W32 - 4);  // columns past W32 are never stored
+    const int blocks = p.W32 / 32;
+    uint32_t xr[8], xs[8];
+    auto load_x = [&](int m0, bool tail) {
+        const uint8_t* codes = p.x8 + (int64_t)m0 * p.W32;
+        const uint8_t* scales = p.x8 + p.scale_off + (int64_t)m0 * blocks;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 8; ++j) {
+            int r = 8 * octet + j;
+            const bool past = tail && m0 + r >= m_end;
+            if (past) r = m_end - 1 - m0;
+            __builtin_memcpy(&xr[j], codes + (uint32_t)(r * p.W32 + xc), 4);
+            xs[j] = scales[(uint32_t)(r * blocks + xc / 32)];
+            if (past) xr[j] = 0;
+        }
+    };
+    auto store_x = [&](uint8_t* buf) {
+        uint32_t v[8][2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += a[r][ty + 16 * i] * b[r][tx + 16 * j];
+        for (int j = 0; j < 8; ++j) {
+            const float s = ckpt8_scale(xs[j]);
+            v[j][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)xr[j], s, false));
+            v[j][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)xr[j], s, true));
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            u32x4 w;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = pair_rows(v[2 * q][t / 2], v[2 * q + 1][t / 2], t & 1);
+            const int c = 4 * cl + t;
+            *reinterpret_cast<u32x4*>(buf + (c ^ (c >> 5 & 1)) * 128 + 16 * (octet ^ (cl & 7))) = w;
+        }
+    };
+
+    f32x4 acc[4][8];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
+
+    // one half step: rows 32 ks .. 32 ks + 31 of the buffer
+    auto multiply = [&](const DyRaw<T>& d, const uint8_t* buf, int ks) {
+        u32x4 a[NT][4];
+        d.frags(a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = 4 * i16 + (j & 3) + 64 * (j >> 2);
+            const u32x4 b = *reinterpret_cast<const u32x4*>(
+                buf + (c ^ (c >> 5 & 1)) * 128 + 16 * ((g + 4 * ks) ^ (i16 & 7)));
+#pragma unroll
+            for (int n = NT - 1; n >= 0; --n)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, a[n][t]), __builtin_bit_cast(bf16x8, b), acc[t][j], 0, 0, 0);
+        }
+    };
+
+    if (m_begin < m_end) {
+        int m = m_begin, cur = 0;
+        bool tail = m + kTM > m_end;
+        load_x(m, tail);
+        load_dy(raw[0], m, tail);
+        load_dy(raw[1], m + 32, tail);
+        store_x(lds[0]);
         __syncthreads();
+        for (;;) {
+            const int next = m + kTM;
+            const bool more = next < m_end;
+            DyRaw<T> now[2] = {raw[0], raw[1]};
+            if (more) {
+                tail = next + kTM > m_end;
+                load_x(next, tail);
+                load_dy(raw[0], next, tail);
+                load_dy(raw[1], next + 32, tail);
+            }
+            multiply(now[0], lds[cur], 0);
+            multiply(now[1], lds[cur], 1);
+            if (!more) break;
+            store_x(lds[cur ^ 1]);
+            __syncthreads();
+            cur ^= 1;
+            m = next;
+        }
     }
+
+    // lane 16g + i holds rows 16g + 4r + t (r = 0 .. 3) and, over j % 4, four
+    // neighbouring columns
+    float* out = p.out + (int64_t)split * p.O * p.W;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int o = o0 + ty + 16 * i, c = c0 + tx + 16 * j;
-            if (o < O && c < W) {
-                float* p = dw + (int64_t)o * W + c;
-                *p = accumulate ? *p + acc[i][j] : acc[i][j];
+        for (int r = 0; r < 4; ++r) {
+            const int want = o0 + 16 * g + 4 * r;  // the columns of dy that lane 4g + r stands for
+            const int o = (narrow ? want : min(want, p.O - 4)) + t;
+            if (o < want || o >= p.O) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = c0 + 64 * h + 4 * i16, n = p.W - c;
+                if (n <= 0) continue;
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = acc[t][4 * h + q][r];
+                float* at = out + (int64_t)o * p.W + c;
+                if (n >= 4) {
+                    float4 s = make_float4(v[0], v[1], v[2], v[3]);
+                    if (p.accumulate) {
+                        float4 u;
+                        __builtin_memcpy(&u, at, 16);
+                        s = make_float4(s.x + u.x, s.y + u.y, s.z + u.z, s.w + u.w);
+                    }
+                    __builtin_memcpy(at, &s, 16);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (q < n) at[q] = p.accumulate ? at[q] + v[q] : v[q];
+                }
             }
         }
 }
 
+// dw[e] = sum_s part[s][e] (+ dw[e])
+__global__ __launch_bounds__(256) void wgrad_join(const float* __restrict__ part, float* dw, int64_t n, int S,
+                                                  bool accumulate) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= n) return;
+    float v = 0.0f;
+    for (int s = 0; s < S; ++s) v += part[s * n + e];
+    dw[e] = accumulate ? dw[e] + v : v;
+}
+
+struct Split {
+    int count, rows;
+};
+// Splits of the rows: 512 workgroups fill the chip (two on each of 256 compute
+// units); a split keeps at least two steps.
+Split split_rows(int64_t M, int64_t W, int64_t O) {
+    const int64_t tiles = ((W + kTC - 1) / kTC) * ((O + kTO - 1) / kTO), steps = (M + kTM - 1) / kTM;
+    int64_t n = 512 / tiles;
+    n = n < steps / 2 ? n : steps / 2;
+    n = n < 1 ? 1 : n;
+    const int64_t each = steps ? (steps + n - 1) / n : 1;
+    return Split{(int)(steps ? (steps + each - 1) / each : 1), (int)(each * kTM)};
+}
+
 }  // namespace
 
-size_t ckpt8_wgrad_workspace_bytes(int64_t, int64_t, int64_t, int) { return 0; }
+size_t ckpt8_wgrad_workspace_bytes(int64_t M, int64_t W, int64_t O, int) {
+    const Split s = split_rows(M, W, O);
+    return s.count > 1 ? (size_t)s.count * W * O * 4 : 0;
+}
 
 int launch_ckpt8_wgrad(const void* dy, int64_t ld, const uint8_t* x8, float* dw, int64_t M, int64_t W,
-                       int64_t O, int dtype, bool accumulate, void*, hipStream_t stream) {
-    const dim3 grid((unsigned)((W + kT - 1) / kT), (unsigned)((O + kT - 1) / kT));
+                       int64_t O, int dtype, bool accumulate, void* ws, hipStream_t stream) {
+    const Split s = split_rows(M, W, O);
     const int64_t W32 = ckpt8_width(W);
-    if (dtype == SSM_BF16)
-        wgrad_tile<bf16_t><<<grid, 256, 0, stream>>>(static_cast<const bf16_t*>(dy), ld, x8, dw, M, (int)W,
-                                                     (int)W32, (int)O, M * W32, accumulate);
-    else
-        wgrad_tile<float><<<grid, 256, 0, stream>>>(static_cast<const float*>(dy), ld, x8, dw, M, (int)W,
-                                                    (int)W32, (int)O, M * W32, accumulate);
+    const int tiles_c = (int)((W + kTC - 1) / kTC);
+    const int64_t tiles = tiles_c * ((O + kTO - 1) / kTO);
+    const bool joined = s.count > 1;
+    WgradP p = {dy, x8, joined ? static_cast<float*>(ws) : dw, ld, M * W32, (int)M, (int)W, (int)W32, (int)O,
+                tiles_c, (int)tiles, s.rows, !joined && accumulate};
+    const unsigned grid = (unsigned)(tiles * s.count);
+    if (dtype == SSM_BF16) wgrad_tile<bf16_t><<<grid, 256, 0, stream>>>(p);
+    else wgrad_tile<float><<<grid, 256, 0, stream>>>(p);
+    if (joined) {
+        const int64_t n = W * O;
+        wgrad_join<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(static_cast<float*>(ws), dw, n, s.count, accumulate);
+    }
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
