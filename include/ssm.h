@@ -434,7 +434,7 @@ int ssm_ckpt8_unpack(const void *ckpt, void *x, int64_t ld, int64_t n_rows, int6
  * [n_rows][width]:
  *   dw[o][c] = sum_m dy[m][o] x[m][c]   (+ dw[o][c] when accumulate != 0)
  * dw [n_out][width] f32, dense.  Products are exact and summed in f32.
- * width and n_out are at most 2^22, their product 2^37, ld 2^26.  workspace:
+ * width, n_out and ld are at most 2^22, width * n_out 2^37.  workspace:
  * ssm_ckpt8_wgrad_workspace_bytes bytes, 256-byte aligned, no initial
  * contents (may be NULL when that is 0). */
 size_t ssm_ckpt8_wgrad_workspace_bytes(int64_t n_rows, int64_t width, int64_t n_out, int32_t dtype);

@@ -119,7 +119,7 @@ int ssm_ckpt8_wgrad(const void* dy, int64_t ld, const void* ckpt, float* dw, int
                     void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
     const int rc = check_wgrad(n_rows, width, n_out, dtype);
     if (rc) return rc;
-    if (!stride_ok(n_rows, n_out, &ld) || ld > 1 << 26) return SSM_ERR_SHAPE;
+    if (!stride_ok(n_rows, n_out, &ld) || ld > 1 << 22) return SSM_ERR_SHAPE;
     const size_t need = ssm_ckpt8_wgrad_workspace_bytes(n_rows, width, n_out, dtype);
     if (!dw || (n_rows > 0 && (!dy || !ckpt)) || (need && !workspace)) return SSM_ERR_NULL;
     if (workspace_bytes < need) return SSM_ERR_WORKSPACE;

@@ -20,6 +20,8 @@
 //     i: c = 4i + j % 4 + 64 (j / 4)) then meet 8 different 16-byte columns.
 // With few tiles the rows are split over workgroups, each of which leaves an
 // f32 partial in the workspace, and a second kernel adds them in order.
+#include <type_traits>
+
 #include "block_internal.h"
 #include "norm_rows.h"
 
@@ -49,6 +51,11 @@ __device__ __forceinline__ uint32_t pair_rows(uint32_t a, uint32_t b, int h) {
     return __builtin_amdgcn_perm(b, a, h ? 0x07060302u : 0x05040100u);
 }
 
+// A descriptor without a bound: whole steps only load what is there.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000);
+}
+
 // A half step's dy of a lane: rows 8g .. 8g + 7, 4 columns.
 template <typename T>
 struct DyRaw;
@@ -56,6 +63,9 @@ template <>
 struct DyRaw<bf16_t> {
     static constexpr int kTerms = 1;
     u32x2 r[8];
+    __device__ __forceinline__ void load(int j, __amdgpu_buffer_rsrc_t b, int at, int row) {
+        r[j] = __builtin_amdgcn_raw_buffer_load_b64(b, at, row, 0);
+    }
     __device__ __forceinline__ void zero(int j) { r[j] = u32x2{0, 0}; }
     __device__ __forceinline__ void frags(u32x4 f[1][4]) const {
 #pragma unroll
@@ -68,6 +78,9 @@ template <>
 struct DyRaw<float> {
     static constexpr int kTerms = 3;
     u32x4 r[8];
+    __device__ __forceinline__ void load(int j, __amdgpu_buffer_rsrc_t b, int at, int row) {
+        r[j] = __builtin_amdgcn_raw_buffer_load_b128(b, at, row, 0);
+    }
     __device__ __forceinline__ void zero(int j) { r[j] = u32x4{0, 0, 0, 0}; }
     // v = hi + mid + lo, each the bf16 nearest to what is left; an infinity or
     // a NaN is all in hi
@@ -93,7 +106,8 @@ struct DyRaw<float> {
     }
 };
 
-template <typename T>
+// NARROW: fewer than 4 columns of dy in all, loaded one by one.
+template <typename T, bool NARROW>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP p) {
     constexpr int NT = DyRaw<T>::kTerms;
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][kTC * kTM * 2];
@@ -109,51 +123,55 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP
     const int m_begin = split * p.rows, m_end = min(p.M, m_begin + p.rows);
 
     // dy: columns past O are never stored, so a lane past the end takes the
-    // last four columns; with fewer than four columns in all, column by column
-    const bool narrow = p.O < 4;
-    const int col = narrow ? 0 : min(o0 + 4 * i16, p.O - 4);
+    // last four.  A step's rows past the end (LAST) are loaded from the last
+    // row and zeroed, so that nothing of them reaches a sum.  Whole steps load
+    // from a scalar base that moves with the step, a scalar row offset and a
+    // lane offset that stays.
+    const int col = NARROW ? 0 : min(o0 + 4 * i16, p.O - 4);
     const T* dy = static_cast<const T*>(p.dy);
-    DyRaw<T> raw[2];
-    auto load_dy = [&](DyRaw<T>& d, int m0, bool tail) {
+    const int dy_row = (int)p.ld * (int)sizeof(T), dy_at = 8 * g * dy_row + col * (int)sizeof(T);
+    auto load_dy = [&](DyRaw<T>& d, int m0, int ks, auto rsrc, auto last) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int m = m0 + 8 * g + j;
-            if (narrow) {
+            if constexpr (NARROW) {
                 T v[4];
-                for (int t = 0; t < 4; ++t) v[t] = dy[(int64_t)min(m, p.M - 1) * p.ld + min(t, p.O - 1)];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    v[t] = dy[(int64_t)min(m0 + 32 * ks + 8 * g + j, p.M - 1) * p.ld + min(t, p.O - 1)];
                 __builtin_memcpy(&d.r[j], v, sizeof v);
-            } else if (tail) {
-                __builtin_memcpy(&d.r[j], dy + (int64_t)min(m, p.M - 1) * p.ld + col, sizeof d.r[j]);
+            } else if constexpr (last.value) {
+                __builtin_memcpy(&d.r[j], dy + (int64_t)min(m0 + 32 * ks + 8 * g + j, m_end - 1) * p.ld + col,
+                                 sizeof d.r[j]);
             } else {
-                const T* base = dy + (int64_t)(m0 + j) * p.ld;
-                __builtin_memcpy(&d.r[j], base + (uint32_t)(8 * g * (int)p.ld + col), sizeof d.r[j]);
+                d.load(j, rsrc, dy_at, (32 * ks + j) * dy_row);
             }
-            if (tail && m >= m_end) d.zero(j);
+            if (last.value && m0 + 32 * ks + 8 * g + j >= m_end) d.zero(j);
         }
     };
-    // x: thread (octet of rows, 4 columns)
+    // x: thread (octet of rows, 4 columns); columns past W32 are never stored
     const int cl = tid & 31, octet = tid >> 5;
-    const int xc = min(c0 + 4 * cl, p.W32 - 4);  // columns past W32 are never stored
-    const int blocks = p.W32 / 32;
+    const int xc = min(c0 + 4 * cl, p.W32 - 4), blocks = p.W32 / 32;
+    const int x_at = 8 * octet * p.W32 + xc, s_at = 8 * octet * blocks + xc / 32;
     uint32_t xr[8], xs[8];
-    auto load_x = [&](int m0, bool tail) {
-        const uint8_t* codes = p.x8 + (int64_t)m0 * p.W32;
-        const uint8_t* scales = p.x8 + p.scale_off + (int64_t)m0 * blocks;
+    auto load_x = [&](int m0, auto codes, auto scales, auto last) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            int r = 8 * octet + j;
-            const bool past = tail && m0 + r >= m_end;
-            if (past) r = m_end - 1 - m0;
-            __builtin_memcpy(&xr[j], codes + (uint32_t)(r * p.W32 + xc), 4);
-            xs[j] = scales[(uint32_t)(r * blocks + xc / 32)];
-            if (past) xr[j] = 0;
+            if constexpr (last.value) {
+                const int m = m0 + 8 * octet + j, r = min(m, m_end - 1);
+                __builtin_memcpy(&xr[j], p.x8 + (int64_t)r * p.W32 + xc, 4);
+                xs[j] = p.x8[p.scale_off + (int64_t)r * blocks + xc / 32];
+                if (m >= m_end) xr[j] = 0;
+            } else {
+                xr[j] = __builtin_amdgcn_raw_buffer_load_b32(codes, x_at, j * p.W32, 0);
+                xs[j] = __builtin_amdgcn_raw_buffer_load_b8(scales, s_at, j * blocks, 0);
+            }
         }
     };
     auto store_x = [&](uint8_t* buf) {
         uint32_t v[8][2];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float s = ckpt8_scale(xs[j]);
+            const float s = __uint_as_float(xs[j] << 23);
             v[j][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)xr[j], s, false));
             v[j][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)xr[j], s, true));
         }
@@ -167,6 +185,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP
         }
     };
 
+    DyRaw<T> raw[2];
     f32x4 acc[4][8];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -191,32 +210,39 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP
         }
     };
 
+    // buffers alternate: step n + 1 is loaded while step n is multiplied, and
+    // written to the other buffer after it, with one barrier a step
+    auto load = [&](int m0, auto last) {
+        const auto codes = rsrc_of(p.x8 + (int64_t)m0 * p.W32);
+        const auto scales = rsrc_of(p.x8 + p.scale_off + (int64_t)m0 * blocks);
+        const auto rows = rsrc_of(dy + (int64_t)m0 * p.ld);
+        load_x(m0, codes, scales, last);
+        load_dy(raw[0], m0, 0, rows, last);
+        load_dy(raw[1], m0, 1, rows, last);
+    };
+    auto step = [&](int m0, int cur, auto last) {  // multiplies buffer cur, loads the step at m0
+        const DyRaw<T> now[2] = {raw[0], raw[1]};
+        load(m0, last);
+        multiply(now[0], lds[cur], 0);
+        multiply(now[1], lds[cur], 1);
+        store_x(lds[cur ^ 1]);
+        __syncthreads();
+    };
+    constexpr std::false_type whole{};
+    constexpr std::true_type partial{};
     if (m_begin < m_end) {
         int m = m_begin, cur = 0;
-        bool tail = m + kTM > m_end;
-        load_x(m, tail);
-        load_dy(raw[0], m, tail);
-        load_dy(raw[1], m + 32, tail);
+        if (m + kTM <= m_end) load(m, whole);
+        else load(m, partial);
         store_x(lds[0]);
         __syncthreads();
-        for (;;) {
-            const int next = m + kTM;
-            const bool more = next < m_end;
-            DyRaw<T> now[2] = {raw[0], raw[1]};
-            if (more) {
-                tail = next + kTM > m_end;
-                load_x(next, tail);
-                load_dy(raw[0], next, tail);
-                load_dy(raw[1], next + 32, tail);
-            }
-            multiply(now[0], lds[cur], 0);
-            multiply(now[1], lds[cur], 1);
-            if (!more) break;
-            store_x(lds[cur ^ 1]);
-            __syncthreads();
+        for (; m + 2 * kTM <= m_end; m += kTM, cur ^= 1) step(m + kTM, cur, whole);
+        if (m + kTM < m_end) {
+            step(m + kTM, cur, partial);
             cur ^= 1;
-            m = next;
         }
+        multiply(raw[0], lds[cur], 0);
+        multiply(raw[1], lds[cur], 1);
     }
 
     // lane 16g + i holds rows 16g + 4r + t (r = 0 .. 3) and, over j % 4, four
@@ -227,7 +253,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int want = o0 + 16 * g + 4 * r;  // the columns of dy that lane 4g + r stands for
-            const int o = (narrow ? want : min(want, p.O - 4)) + t;
+            const int o = (NARROW ? want : min(want, p.O - 4)) + t;
             if (o < want || o >= p.O) continue;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -295,8 +321,13 @@ int launch_ckpt8_wgrad(const void* dy, int64_t ld, const uint8_t* x8, float* dw,
     WgradP p = {dy, x8, joined ? static_cast<float*>(ws) : dw, ld, M * W32, (int)M, (int)W, (int)W32, (int)O,
                 tiles_c, (int)tiles, s.rows, !joined && accumulate};
     const unsigned grid = (unsigned)(tiles * s.count);
-    if (dtype == SSM_BF16) wgrad_tile<bf16_t><<<grid, 256, 0, stream>>>(p);
-    else wgrad_tile<float><<<grid, 256, 0, stream>>>(p);
+    if (dtype == SSM_BF16) {
+        if (O < 4) wgrad_tile<bf16_t, true><<<grid, 256, 0, stream>>>(p);
+        else wgrad_tile<bf16_t, false><<<grid, 256, 0, stream>>>(p);
+    } else {
+        if (O < 4) wgrad_tile<float, true><<<grid, 256, 0, stream>>>(p);
+        else wgrad_tile<float, false><<<grid, 256, 0, stream>>>(p);
+    }
     if (joined) {
         const int64_t n = W * O;
         wgrad_join<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(static_cast<float*>(ws), dw, n, s.count, accumulate);
