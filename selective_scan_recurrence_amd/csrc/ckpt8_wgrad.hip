@@ -293,27 +293,39 @@ __global__ __launch_bounds__(256) void wgrad_join(const float* __restrict__ part
 struct Split {
     int count, rows;
 };
-// Splits of the rows: 512 workgroups fill the chip (two on each of 256 compute
-// units); a split keeps at least two steps.
-Split split_rows(int64_t M, int64_t W, int64_t O) {
+// Parts of the rows, each of at least two steps: the count with the least
+// modelled time.  A step takes 1.25 us with one workgroup on a compute unit
+// and 2.0 with two (bf16), 3.9 with the one that f32 has room for; the join
+// costs a launch and moves each partial twice at 5 TB/s.  (8192 x 1024 x 512
+// in bf16, 16 tiles: 36 us with the 32 parts that fill the chip, 24 with 10.)
+Split split_rows(int64_t M, int64_t W, int64_t O, int dtype) {
     const int64_t tiles = ((W + kTC - 1) / kTC) * ((O + kTO - 1) / kTO), steps = (M + kTM - 1) / kTM;
-    int64_t n = 512 / tiles;
-    n = n < steps / 2 ? n : steps / 2;
-    n = n < 1 ? 1 : n;
-    const int64_t each = steps ? (steps + n - 1) / n : 1;
-    return Split{(int)(steps ? (steps + each - 1) / each : 1), (int)(each * kTM)};
+    Split best{1, (int)((steps ? steps : 1) * kTM)};
+    double best_us = 0;
+    for (int64_t n = 1; n == 1 || (n <= steps / 2 && n * tiles <= 512); ++n) {
+        const int64_t each = steps ? (steps + n - 1) / n : 1, count = steps ? (steps + each - 1) / each : 1;
+        const int64_t wgs = tiles * count, left = wgs % 512;
+        const double step_us = dtype == SSM_BF16 ? (double)(wgs / 512) * 2.0 + (left == 0 ? 0.0 : left <= 256 ? 1.25 : 2.0)
+                                                 : (double)((wgs + 255) / 256) * 3.9;
+        const double us = step_us * (double)each + (count > 1 ? 4.0 + (double)count * W * O * 8.0 / 5e6 : 0.0);
+        if (n == 1 || us < best_us) {
+            best = Split{(int)count, (int)(each * kTM)};
+            best_us = us;
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
-size_t ckpt8_wgrad_workspace_bytes(int64_t M, int64_t W, int64_t O, int) {
-    const Split s = split_rows(M, W, O);
+size_t ckpt8_wgrad_workspace_bytes(int64_t M, int64_t W, int64_t O, int dtype) {
+    const Split s = split_rows(M, W, O, dtype);
     return s.count > 1 ? (size_t)s.count * W * O * 4 : 0;
 }
 
 int launch_ckpt8_wgrad(const void* dy, int64_t ld, const uint8_t* x8, float* dw, int64_t M, int64_t W,
                        int64_t O, int dtype, bool accumulate, void* ws, hipStream_t stream) {
-    const Split s = split_rows(M, W, O);
+    const Split s = split_rows(M, W, O, dtype);
     const int64_t W32 = ckpt8_width(W);
     const int tiles_c = (int)((W + kTC - 1) / kTC);
     const int64_t tiles = tiles_c * ((O + kTO - 1) / kTO);
