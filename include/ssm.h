@@ -403,7 +403,7 @@ typedef struct ssm_norm_desc {
     int64_t ld_out;     /* row stride of out and dout, or of h and dh             */
     int32_t io_dtype;   /* ssm_dtype of every matrix but the residual stream      */
     int32_t res_dtype;  /* ssm_dtype of r, r_out, dr_out, d_r: io's, or f32       */
-    float eps;          /* > 0                                                    */
+    float eps;          /* >= 2^-126                                              */
     float res_scale;    /* constant factor of the branch (residual norm); else 1  */
     uint32_t flags;     /* SSM_NORM_GATE_AFTER (gated norm)                       */
     uint32_t reserved;  /* must be 0                                              */

@@ -30,7 +30,7 @@ int check_norm(const ssm_norm_desc* d, NormShape* out) {
         return SSM_ERR_SHAPE;
     int64_t t;
     if (!mul_ok(d->n_rows, d->n_group, &t) || t > INT_MAX) return SSM_ERR_SHAPE;
-    if (!(d->eps > 0.0f) || !isfinite(d->eps) || !isfinite(d->res_scale)) return SSM_ERR_SHAPE;
+    if (!(d->eps >= 0x1p-126f) || !isfinite(d->eps) || !isfinite(d->res_scale)) return SSM_ERR_SHAPE;
     NormShape s;
     s.M = d->n_rows; s.W = (int)d->width; s.G = (int)d->n_group; s.Wg = s.W / s.G;
     s.io = d->io_dtype; s.res = d->res_dtype; s.eps = d->eps; s.alpha = d->res_scale;
@@ -54,7 +54,7 @@ int check_residual(const ssm_norm_desc* d, NormShape* out) {
 }
 
 size_t norm_bwd_workspace(const NormShape& s) {
-    const size_t n = (size_t)norm_bwd_slices(s) * s.W * 4 * 3;
+    const size_t n = (size_t)norm_bwd_slices(s) * s.W * 4 * 2;
     return (n + 255) / 256 * 256;
 }
 

@@ -68,14 +68,19 @@ struct ResidualBwdArgs {
     const float *w_post, *scale, *w, *rstd, *rstd_post;
     void *d_r, *d_b;
     float *d_w, *d_w_post, *d_scale;
-    float* part;  // partial sums [3][slices][W]: w, w_post, scale
+    float* part;  // partial sums [2][slices][W]
 };
 int launch_norm_residual_bwd(const ResidualBwdArgs& a, hipStream_t stream);
 
-// Sums n_arr arrays of S partial rows of W columns in a fixed order:
-// out[a][c] = sum_s part[a][s][c].  Null outputs are skipped.
-int launch_column_sums(const float* part, int S, int W, float* const out[3], int n_arr,
-                       hipStream_t stream);
+// Sums S partial rows of W columns in a fixed order: d_w[c] = sum_s
+// part[0][s][c] and, with T the same of part[1], d_w_post = alpha scale T and
+// d_scale = alpha w_post T.  Null outputs are skipped, null factors are 1.
+struct ColumnSums {
+    float *d_w, *d_w_post = nullptr, *d_scale = nullptr;
+    const float *scale = nullptr, *w_post = nullptr;
+    float alpha = 1.0f;
+};
+int launch_column_sums(const float* part, int S, int W, const ColumnSums& out, hipStream_t stream);
 
 int launch_ckpt8_pack(const void* x, int64_t ld, int64_t M, int64_t W, int dtype, uint8_t* out,
                       hipStream_t stream);

@@ -47,23 +47,32 @@ __device__ __forceinline__ float ckpt8_scale(uint32_t b) {
 // Codes of this lane's 8 values; the four lanes of a quad call it together.
 // byte receives the block's scale byte.
 __device__ __forceinline__ uint2 ckpt8_encode(const float v[8], uint32_t* byte) {
-    float m = 0.0f, x[8];
+    float x[8], m = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float a = fabsf(v[j]);
-        const bool finite = a < __builtin_inff();
-        m = fmaxf(m, finite ? a : 0.0f);
-        x[j] = finite ? v[j] : __builtin_nanf("");
+        x[j] = v[j];
+        m = fmaxf(m, fabsf(v[j]));  // a quiet NaN drops out here and converts to NaN below
     }
     m = fmax_quad(m);
+    // a block that holds an infinity or a signalling NaN: find amax again
+    if (__builtin_amdgcn_ballot_w64(!(m < __builtin_inff()))) {
+        m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool finite = __builtin_isfinite(v[j]);
+            x[j] = finite ? v[j] : __builtin_nanf("");
+            m = fmaxf(m, finite ? fabsf(v[j]) : 0.0f);
+        }
+        m = fmax_quad(m);
+    }
     const uint32_t b = ckpt8_scale_byte(m);
-    const float inv = __uint_as_float((254u - b) << 23);
-    if (b == 247u) {
-        const float top = __uint_as_float((247u + 7u) << 23 | 0x700000u);  // 240 * 2^120
+    if (__builtin_amdgcn_ballot_w64(b == 247u)) {
+        const float top = b == 247u ? __uint_as_float((247u + 7u) << 23 | 0x700000u) : __builtin_inff();  // 240 * 2^120
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (fabsf(x[j]) > top) x[j] = copysignf(top, x[j]);
     }
+    const float inv = __uint_as_float((254u - b) << 23);
     int lo = 0, hi = 0;
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * inv, x[1] * inv, lo, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * inv, x[3] * inv, lo, true);

@@ -14,14 +14,13 @@ __global__ __launch_bounds__(256) void ckpt8_pack(const T* __restrict__ x, int64
     const int64_t i = block_id() * 256 + threadIdx.x;
     if (i >= pieces) return;  // pieces is a multiple of 4: a block's lanes go together
     const int64_t row = i / P;
-    const int c = (int)(i % P), n = W - 8 * c;
-    float v[8] = {};
-    if (n > 0) {
-        const Piece<T> t = load8(x + row * ld + 8 * c, n);
+    const int at = 8 * (int)(i % P);
+    Piece<T> t = {};
+    load8<true>(t, x + row * ld, at, W);
+    float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = t[j];
-    }
-    ckpt_store(ckpt_row(out, scale_off, W32, row, 0), c, v);
+    for (int j = 0; j < 8; ++j) v[j] = t[j];
+    Ckpt(out, scale_off, W32, 0).store(row, at, v);
 }
 
 template <typename T>
@@ -30,11 +29,11 @@ __global__ __launch_bounds__(256) void ckpt8_unpack(uint8_t* x8, T* __restrict__
     const int64_t i = block_id() * 256 + threadIdx.x;
     if (i >= pieces) return;
     const int64_t row = i / P;
-    const int c = (int)(i % P), n = W - 8 * c;
-    if (n <= 0) return;
+    const int at = 8 * (int)(i % P);
+    if (at >= W) return;
     float v[8];
-    ckpt_load(ckpt_row(x8, scale_off, W32, row, 0), c, v);
-    store8(x + row * ld + 8 * c, n, v);
+    Ckpt(x8, scale_off, W32, 0).load(row, at).values(v);
+    store8<true>(x + row * ld, at, W, v);
 }
 
 }  // namespace

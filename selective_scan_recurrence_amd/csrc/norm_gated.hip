@@ -16,79 +16,91 @@
 namespace ssm {
 namespace {
 
+enum Gate { kNone, kBefore, kAfter };
+
 struct FwdP {
     const void *y, *z;
     const float* w;
     void* out;
     float* rstd;
     uint8_t *y8, *z8, *out8;
-    int64_t ld_y, ld_z, ld_out, units, scale_off;
-    int G, Wg, W32;
+    int64_t ld_y, ld_z, ld_out, M, scale_off;
+    int G, Wg, W32, slices;
     float eps, inv_n;
 };
 
-template <typename T, int L, int NC, bool AFTER>
+// Workgroup (slice, group) takes every slices-th row (or set of rows), and
+// loads the next one while it works on the present one.  w stays in registers:
+// a load between the next row's and their use would have to wait for them.
+template <typename T, int L, int NC, bool RAGGED, Gate GATE>
 __global__ __launch_bounds__(L ? kRowThreads : 1024) void gated_fwd(FwdP p) {
     __shared__ float lds[32];
+    constexpr int U = units_per_block<L>();
     const UnitLane ul = unit_lane<L>();
-    const int64_t id = block_id() * units_per_block<L>() + ul.unit;
-    const bool valid = id < p.units;
-    const int64_t row = valid ? id / p.G : 0;
-    const int g = valid ? (int)(id % p.G) : 0, c0 = g * p.Wg;
-    const int wg = valid ? p.Wg : 0;
-    const T* y = static_cast<const T*>(p.y) + row * p.ld_y + c0;
-    const T* z = p.z ? static_cast<const T*>(p.z) + row * p.ld_z + c0 : nullptr;
-    Piece<T> yv[NC], zv[NC];
+    const int g = blockIdx.x % p.G, c0 = g * p.Wg, wg = p.Wg;
+    const T* y = static_cast<const T*>(p.y) + c0;
+    const T* z = static_cast<const T*>(p.z) + c0;
+    T* out = static_cast<T*>(p.out) + c0;
+    const Ckpt y8(p.y8, p.scale_off, p.W32, c0), z8(p.z8, p.scale_off, p.W32, c0), out8(p.out8, p.scale_off, p.W32, c0);
+    struct Row {
+        Piece<T> y[NC], z[NC];
+    };
+    auto load = [&](Row& r, int64_t row) {
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
-        const int c = ul.lane + k * ul.lanes, n = wg - 8 * c;
-        if (n > 0) {
-            yv[k] = load8(y + 8 * c, n);
-            if (z) zv[k] = load8(z + 8 * c, n);
+        for (int k = 0; k < NC; ++k) {
+            load8<RAGGED>(r.y[k], y + row * p.ld_y, ul.at(k), wg);
+            if (GATE != kNone) load8<RAGGED>(r.z[k], z + row * p.ld_z, ul.at(k), wg);
         }
-    }
-    // x: what is normalised; ga: the gate after the norm
-    float x[NC][8], ga[NC][8], ss = 0.0f;
+    };
+    // lanes past the width keep the zeros they start with
+    Row next = {};
+    Piece<float> w[NC] = {};
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
-        const bool on = wg - 8 * (ul.lane + k * ul.lanes) > 0;
+    for (int k = 0; k < NC; ++k) load8<RAGGED>(w[k], p.w + c0, ul.at(k), wg);
+    unit_sum_init<L>(lds);
+    int64_t row = (int64_t)(blockIdx.x / p.G) * U + ul.unit;
+    const int64_t step = (int64_t)p.slices * U;
+    if (row < p.M) load(next, row);
+    int turn = 0;
+    for (int64_t first = row - ul.unit; first < p.M; first += step, row += step, ++turn) {
+        const Row r = next;
+        if (row + step < p.M) load(next, row + step);
+        float x[NC][8], ss = 0.0f;  // x: what is normalised
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float yj = on ? yv[k][j] : 0.0f, gj = !on ? 0.0f : z ? silu(zv[k][j]) : 1.0f;
-            x[k][j] = AFTER ? yj : yj * gj;
-            ga[k][j] = AFTER ? gj : 1.0f;
-            ss += x[k][j] * x[k][j];
-        }
-    }
-    const float rstd = 1.0f / sqrtf(unit_sum<L>(ss, lds, 0) * p.inv_n + p.eps);
-    if (valid && p.rstd && ul.lane == 0) p.rstd[id] = rstd;
-    T* out = static_cast<T*>(p.out) + row * p.ld_out + c0;
+        for (int k = 0; k < NC; ++k)
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
-        const int c = ul.lane + k * ul.lanes, n = wg - 8 * c;
-        float o[8] = {};
-        if (n > 0) {
-            const Piece<float> w = load8(p.w + c0 + 8 * c, n);
+            for (int j = 0; j < 8; ++j) {
+                x[k][j] = GATE == kBefore ? r.y[k][j] * silu(r.z[k][j]) : r.y[k][j];
+                ss += x[k][j] * x[k][j];
+            }
+        const float rstd = rsqrt1(unit_sum<L>(ss, lds, turn) * p.inv_n + p.eps);
+        if (row >= p.M) continue;
+        if (p.rstd && ul.lane == 0) p.rstd[row * p.G + g] = rstd;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = x[k][j] * rstd * w[j] * ga[k][j];
-            store8(out + 8 * c, n, o);
-        }
-        if (8 * c < (valid ? (wg + 31) / 32 * 32 : 0)) {
+        for (int k = 0; k < NC; ++k) {
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                o[j] = x[k][j] * rstd * w[k][j];
+                if (GATE == kAfter) o[j] *= silu(r.z[k][j]);
+            }
+            store8<RAGGED>(out + row * p.ld_out, ul.at(k), wg, o);
+            if (ul.at(k) >= (wg + 31) / 32 * 32) continue;
             float v[8];
             if (p.y8) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = n > 0 ? yv[k][j] : 0.0f;
-                ckpt_store(ckpt_row(p.y8, p.scale_off, p.W32, row, c0), c, v);
+                for (int j = 0; j < 8; ++j) v[j] = r.y[k][j];
+                y8.store(row, ul.at(k), v);
             }
-            if (p.z8) {
+            if (GATE != kNone && p.z8) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = n > 0 ? zv[k][j] : 0.0f;
-                ckpt_store(ckpt_row(p.z8, p.scale_off, p.W32, row, c0), c, v);
+                for (int j = 0; j < 8; ++j) v[j] = r.z[k][j];
+                z8.store(row, ul.at(k), v);
             }
             if (p.out8) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = as_stored(o[j], T());
-                ckpt_store(ckpt_row(p.out8, p.scale_off, p.W32, row, c0), c, v);
+                out8.store(row, ul.at(k), v);
             }
         }
     }
@@ -105,111 +117,119 @@ struct BwdP {
     float inv_n;
 };
 
-template <typename T, int L, int NC, bool AFTER>
+template <typename T, int L, int NC, bool RAGGED, Gate GATE>
 __global__ __launch_bounds__(L ? kRowThreads : 1024) void gated_bwd(BwdP p) {
     __shared__ float lds[L ? kRowThreads * 8 : 32];
+    constexpr int U = units_per_block<L>();
     const UnitLane ul = unit_lane<L>();
-    const int g = blockIdx.x % p.G, slice = blockIdx.x / p.G, c0 = g * p.Wg;
-    const bool gate = p.z || p.z8;
-    float w[NC][8], dw[NC][8];
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-        const int c = ul.lane + k * ul.lanes, n = p.Wg - 8 * c;
-        if (n > 0) {
-            const Piece<float> t = load8(p.w + c0 + 8 * c, n);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[k][j] = t[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (n <= 0) w[k][j] = 0.0f;
-            dw[k][j] = 0.0f;
-        }
-    }
-    int turn = 0;
-    const int64_t step = (int64_t)p.slices * units_per_block<L>();
-    for (int64_t r0 = (int64_t)slice * units_per_block<L>(); r0 < p.M; r0 += step, ++turn) {
-        const int64_t row = r0 + ul.unit;
-        const bool valid = row < p.M;
-        const int wg = valid ? p.Wg : 0;
-        const int64_t rr = valid ? row : 0;
-        const float rstd = valid ? p.rstd[rr * p.G + g] : 0.0f;
-        // d: dout; x: the normalised value; then what dy and dz need
-        float d[NC][8], x[NC][8], y[NC][8], z[NC][8], dot = 0.0f;
+    const int g = blockIdx.x % p.G, slice = blockIdx.x / p.G, c0 = g * p.Wg, wg = p.Wg;
+    const T* dout = static_cast<const T*>(p.dout) + c0;
+    const T* y = static_cast<const T*>(p.y) + c0;
+    const T* z = static_cast<const T*>(p.z) + c0;
+    T* d_y = static_cast<T*>(p.d_y) + c0;
+    T* d_z = static_cast<T*>(p.d_z) + c0;
+    const Ckpt y8(p.y8, p.scale_off, p.W32, c0), z8(p.z8, p.scale_off, p.W32, c0);
+    struct Row {
+        Piece<T> d[NC];
+        PieceOr8<T> y[NC], z[NC];
+        float rstd;
+    };
+    auto load = [&](Row& r, int64_t row) {
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            const int c = ul.lane + k * ul.lanes, n = wg - 8 * c;
+            load8<RAGGED>(r.d[k], dout + row * p.ld_out, ul.at(k), wg);
+            if (!p.y8) load8<RAGGED>(r.y[k].t, y + row * p.ld_y, ul.at(k), wg);
+            else if (ul.at(k) < wg) r.y[k].c = y8.load(row, ul.at(k));
+            if (GATE == kNone) continue;
+            if (!p.z8) load8<RAGGED>(r.z[k].t, z + row * p.ld_z, ul.at(k), wg);
+            else if (ul.at(k) < wg) r.z[k].c = z8.load(row, ul.at(k));
+        }
+        r.rstd = p.rstd[row * p.G + g];
+    };
+    Row next;
+    __builtin_memset(&next, 0, sizeof next);
+    Piece<float> w[NC] = {};
+    float dw[NC][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[k][j] = y[k][j] = z[k][j] = 0.0f;
-            if (n > 0) {
-                const Piece<T> t = load8(static_cast<const T*>(p.dout) + rr * p.ld_out + c0 + 8 * c, n);
+    for (int k = 0; k < NC; ++k) {
+        load8<RAGGED>(w[k], p.w + c0, ul.at(k), wg);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[k][j] = t[j];
-                if (p.y8) {
-                    ckpt_load(ckpt_row(p.y8, p.scale_off, p.W32, rr, c0), c, y[k]);
-                } else {
-                    const Piece<T> u = load8(static_cast<const T*>(p.y) + rr * p.ld_y + c0 + 8 * c, n);
+        for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
+    }
+    unit_sum_init<L>(lds);
+    int64_t row = (int64_t)slice * U + ul.unit;
+    const int64_t step = (int64_t)p.slices * U;
+    if (row < p.M) load(next, row);
+    int turn = 0;
+    for (int64_t first = row - ul.unit; first < p.M; first += step, row += step, ++turn) {
+        const Row r = next;
+        if (row + step < p.M) load(next, row + step);
+        const bool valid = row < p.M;  // else r is the row before: it is not counted again
+        // x: the normalised value; yv, zv: y and z
+        float x[NC][8], yv[NC][8], zv[NC][8], dot = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) y[k][j] = u[j];
-                }
-                if (p.z8) {
-                    ckpt_load(ckpt_row(p.z8, p.scale_off, p.W32, rr, c0), c, z[k]);
-                } else if (gate) {
-                    const Piece<T> u = load8(static_cast<const T*>(p.z) + rr * p.ld_z + c0 + 8 * c, n);
+        for (int k = 0; k < NC; ++k) {
+            if (p.y8) r.y[k].c.values(yv[k]);
+            else
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) z[k][j] = u[j];
-                }
+                for (int j = 0; j < 8; ++j) yv[k][j] = r.y[k].t[j];
+            if (GATE != kNone) {
+                if (p.z8) r.z[k].c.values(zv[k]);
+                else
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) zv[k][j] = r.z[k].t[j];
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float gj = gate ? silu(z[k][j]) : 1.0f;
-                x[k][j] = (AFTER ? y[k][j] : y[k][j] * gj) * rstd;
-                const float dn = AFTER ? d[k][j] * gj : d[k][j];
-                if (n > 0) dw[k][j] += dn * x[k][j];
-                dot += dn * w[k][j] * x[k][j];
+                const float gate = GATE == kNone ? 1.0f : silu(zv[k][j]);
+                x[k][j] = (GATE == kBefore ? yv[k][j] * gate : yv[k][j]) * r.rstd;
+                const float dx = (GATE == kAfter ? r.d[k][j] * gate : r.d[k][j]) * x[k][j];
+                if (valid) dw[k][j] += dx;
+                dot += dx * w[k][j];
             }
         }
         const float c1 = unit_sum<L>(dot, lds, turn) * p.inv_n;
+        if (!valid) continue;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            const int c = ul.lane + k * ul.lanes, n = wg - 8 * c;
-            if (n <= 0) continue;
             float dy[8], dz[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float sg = sigmoid(z[k][j]);
-                const float gj = gate ? z[k][j] * sg : 1.0f, slope = sg * (1.0f + z[k][j] * (1.0f - sg));
-                if (AFTER) {
-                    dy[j] = rstd * (d[k][j] * gj * w[k][j] - x[k][j] * c1);
-                    dz[j] = d[k][j] * x[k][j] * w[k][j] * slope;
+                const float s = GATE == kNone ? 0.0f : sigmoid(zv[k][j]);
+                const float gate = GATE == kNone ? 1.0f : zv[k][j] * s, slope = s * (1.0f + zv[k][j] * (1.0f - s));
+                const float dn = r.d[k][j] * w[k][j];
+                if (GATE == kAfter) {
+                    dy[j] = r.rstd * (dn * gate - x[k][j] * c1);
+                    dz[j] = dn * x[k][j] * slope;
                 } else {
-                    const float du = rstd * (d[k][j] * w[k][j] - x[k][j] * c1);
-                    dy[j] = du * gj;
-                    dz[j] = du * y[k][j] * slope;
+                    const float du = r.rstd * (dn - x[k][j] * c1);
+                    dy[j] = du * gate;
+                    dz[j] = du * yv[k][j] * slope;
                 }
             }
-            if (p.d_y) store8(static_cast<T*>(p.d_y) + rr * p.ld_y + c0 + 8 * c, n, dy);
-            if (p.d_z) store8(static_cast<T*>(p.d_z) + rr * p.ld_z + c0 + 8 * c, n, dz);
+            if (p.d_y) store8<RAGGED>(d_y + row * p.ld_y, ul.at(k), wg, dy);
+            if (GATE != kNone && p.d_z) store8<RAGGED>(d_z + row * p.ld_z, ul.at(k), wg, dz);
         }
     }
-    if (p.part) store_column_sums<L, NC>(p.part + (int64_t)slice * p.W + c0, p.Wg, dw, lds);
+    if (p.part) store_column_sums<L, NC, RAGGED>(p.part + (int64_t)slice * p.W + c0, wg, dw, lds);
 }
 
 }  // namespace
 
 int launch_norm_gated_fwd(const GatedArgs& a, hipStream_t stream) {
     const NormShape& s = a.s;
-    FwdP p = {a.y, a.z, a.w, a.out, a.rstd, a.y8, a.z8, a.out8, s.ld_x, s.ld_z, s.ld_out,
-              s.M * s.G, s.scale_off, s.G, s.Wg, s.W32, s.eps, 1.0f / (float)s.Wg};
-    if (!p.units) return SSM_OK;
+    if (!s.M) return SSM_OK;
     return for_row_shape(s.Wg, [&](auto rs) {
         using RS = decltype(rs);
-        const dim3 grid = block_grid((p.units + units_per_block<RS::L>() - 1) / units_per_block<RS::L>());
-        const int threads = row_threads<RS>(s.Wg);
+        const int threads = row_threads<RS>(s.Wg), slices = row_slices<RS>(s.M, s.G, threads);
+        FwdP p = {a.y, a.z, a.w, a.out, a.rstd, a.y8, a.z8, a.out8, s.ld_x, s.ld_z, s.ld_out,
+                  s.M, s.scale_off, s.G, s.Wg, s.W32, slices, s.eps, 1.0f / (float)s.Wg};
+        const unsigned grid = (unsigned)(slices * s.G);
         auto go = [&](auto t) {
             using T = decltype(t);
-            if (s.after) gated_fwd<T, RS::L, RS::NC, true><<<grid, threads, 0, stream>>>(p);
-            else gated_fwd<T, RS::L, RS::NC, false><<<grid, threads, 0, stream>>>(p);
+            if (!a.z) gated_fwd<T, RS::L, RS::NC, RS::RAGGED, kNone><<<grid, threads, 0, stream>>>(p);
+            else if (s.after) gated_fwd<T, RS::L, RS::NC, RS::RAGGED, kAfter><<<grid, threads, 0, stream>>>(p);
+            else gated_fwd<T, RS::L, RS::NC, RS::RAGGED, kBefore><<<grid, threads, 0, stream>>>(p);
         };
         if (s.io == SSM_BF16) go(bf16_t());
         else go(float());
@@ -229,16 +249,16 @@ int launch_norm_gated_bwd(const GatedBwdArgs& a, hipStream_t stream) {
         const unsigned grid = (unsigned)(slices * s.G);
         auto go = [&](auto t) {
             using T = decltype(t);
-            if (s.after) gated_bwd<T, RS::L, RS::NC, true><<<grid, threads, 0, stream>>>(p);
-            else gated_bwd<T, RS::L, RS::NC, false><<<grid, threads, 0, stream>>>(p);
+            if (!a.z && !a.z8) gated_bwd<T, RS::L, RS::NC, RS::RAGGED, kNone><<<grid, threads, 0, stream>>>(p);
+            else if (s.after) gated_bwd<T, RS::L, RS::NC, RS::RAGGED, kAfter><<<grid, threads, 0, stream>>>(p);
+            else gated_bwd<T, RS::L, RS::NC, RS::RAGGED, kBefore><<<grid, threads, 0, stream>>>(p);
         };
         if (s.io == SSM_BF16) go(bf16_t());
         else go(float());
         return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
     });
     if (rc != SSM_OK || !a.d_w || slices == 1) return rc;
-    float* const out[3] = {a.d_w, nullptr, nullptr};
-    return launch_column_sums(a.part, slices, s.W, out, 1, stream);
+    return launch_column_sums(a.part, slices, s.W, ColumnSums{a.d_w}, stream);
 }
 
 }  // namespace ssm

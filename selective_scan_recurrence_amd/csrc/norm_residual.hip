@@ -1,20 +1,21 @@
-// The norm between two blocks, forward and backward.  Per row:
-//   t  = b,  or  b rstd_post w_post  (norm after the block)
-//   r' = r + alpha scale t           (residual add and scale)
+// The norm between two blocks, forward and backward.  Per row, with v = b (or,
+// with a norm after the block, v = b rstd_post) and the column constants
+// e = alpha scale w_post (factors that are not given are 1):
+//   r' = r + e v                     (residual add and scale)
 //   h  = r' rstd w                   (norm before the next block)
 // with rstd = 1 / sqrt(mean r'^2 + eps), rstd_post the same of b; and, with
 // c() the mean over the row:
 //   x  = r' rstd, dn = dh w, dx = rstd (dn - x c(dn x)) + d_r_out,  d_r = dx
-//   dt = alpha scale dx;  dw = sum_rows dh x;  dscale = sum_rows alpha dx t
-//   with the norm after the block: v = b rstd_post, dm = dt w_post,
-//     db = rstd_post (dm - v c(dm v)), dw_post = sum_rows dt v;  else db = dt
+//   dm = e dx;  d_b = dm,  or  rstd_post (dm - v c(dm v))
+//   d_w = sum_rows dh x;  S = sum_rows dx v:
+//   d_w_post = alpha scale S,  d_scale = alpha w_post S
 // All of it in f32; what is stored in fewer bits is rounded once.
 //
 // Bound by HBM: each input is read once and each output written once, the row
 // held in registers between its sums and the outputs (norm_rows.h).  The
-// column sums over rows also keep this file's second kernel: each workgroup
-// of the backward adds the rows of its slice in registers and stores one
-// partial row; column_sums adds the partial rows in a fixed order.
+// column sums over rows also keep this file's last kernel: each workgroup of a
+// backward adds the rows of its slice in registers and stores one partial row;
+// column_sums adds the partial rows in a fixed order.
 #include "block_internal.h"
 #include "norm_rows.h"
 
@@ -28,97 +29,113 @@ struct FwdP {
     float *rstd, *rstd_post;
     uint8_t *r8, *b8, *h8;
     int64_t ld_x, ld_res, ld_out, M, scale_off;
-    int W, W32;
+    int W, W32, slices;
     float eps, inv_n, alpha;
 };
 
-template <typename T, typename R, int L, int NC>
+// e of this lane's pieces
+template <bool RAGGED>
+__device__ __forceinline__ Piece<float> branch_factor(const float* w_post, const float* scale, float alpha, int at, int n) {
+    Piece<float> e = {}, t = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e.d[j] = alpha;
+    if (scale) {
+        load8<RAGGED>(t, scale, at, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e.d[j] *= t.d[j];
+    }
+    if (w_post) {
+        load8<RAGGED>(t, w_post, at, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e.d[j] *= t.d[j];
+    }
+    return e;
+}
+
+// Workgroup i takes every slices-th row (or set of rows) from i on, and loads
+// the next one while it works on the present one.
+template <typename T, typename R, int L, int NC, bool RAGGED>
 __global__ __launch_bounds__(L ? kRowThreads : 1024) void residual_fwd(FwdP p) {
     __shared__ float lds[32];
+    constexpr int U = units_per_block<L>();
     const UnitLane ul = unit_lane<L>();
-    const int64_t id = block_id() * units_per_block<L>() + ul.unit;
-    const bool valid = id < p.M;
-    const int64_t row = valid ? id : 0;
-    const int W = valid ? p.W : 0;
-    const T* b = p.b ? static_cast<const T*>(p.b) + row * p.ld_x : nullptr;
-    const R* r = p.r ? static_cast<const R*>(p.r) + row * p.ld_res : nullptr;
-    float bv[NC][8], x[NC][8];
+    const int n = p.W;
+    const T* b = static_cast<const T*>(p.b);
+    const R* r_in = static_cast<const R*>(p.r);
+    R* r_out = static_cast<R*>(p.r_out);
+    T* h = static_cast<T*>(p.h);
+    const Ckpt r8(p.r8, p.scale_off, p.W32, 0), b8(p.b8, p.scale_off, p.W32, 0), h8(p.h8, p.scale_off, p.W32, 0);
+    struct Row {
+        Piece<T> b[NC];
+        Piece<R> r[NC];
+    };
+    auto load = [&](Row& o, int64_t row) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            if (p.b) load8<RAGGED>(o.b[k], b + row * p.ld_x, ul.at(k), n);
+            if (p.r) load8<RAGGED>(o.r[k], r_in + row * p.ld_res, ul.at(k), n);
+        }
+    };
+    // what is not given, and lanes past the width, keep the zeros of the start
+    Row next = {};
+    Piece<float> w[NC] = {}, e[NC];
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-        const int c = ul.lane + k * ul.lanes, n = W - 8 * c;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) bv[k][j] = x[k][j] = 0.0f;
-        if (n > 0) {
-            if (b) {
-                const Piece<T> t = load8(b + 8 * c, n);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) bv[k][j] = t[j];
-            }
-            if (r) {
-                const Piece<R> t = load8(r + 8 * c, n);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] = t[j];
-            }
-        }
+        load8<RAGGED>(w[k], p.w, ul.at(k), n);
+        e[k] = branch_factor<RAGGED>(p.w_post, p.scale, p.alpha, ul.at(k), n);
     }
-    float post = 1.0f;
-    if (p.w_post) {
-        float ss = 0.0f;
+    unit_sum_init<L>(lds);
+    int64_t row = (int64_t)blockIdx.x * U + ul.unit;
+    const int64_t step = (int64_t)p.slices * U;
+    if (row < p.M) load(next, row);
+    int turn = 0;
+    for (int64_t first = row - ul.unit; first < p.M; first += step, row += step) {
+        const Row o = next;
+        if (row + step < p.M) load(next, row + step);
+        const bool valid = row < p.M;
+        float post = 1.0f;
+        if (p.w_post) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NC; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss += o.b[k][j] * o.b[k][j];
+            post = rsqrt1(unit_sum<L>(ss, lds, turn++) * p.inv_n + p.eps);
+            if (valid && p.rstd_post && ul.lane == 0) p.rstd_post[row] = post;
+        }
+        float x[NC][8], ss = 0.0f;
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss += bv[k][j] * bv[k][j];
-        post = 1.0f / sqrtf(unit_sum<L>(ss, lds, 0) * p.inv_n + p.eps);
-        if (valid && p.rstd_post && ul.lane == 0) p.rstd_post[row] = post;
-    }
-    float ss = 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                x[k][j] = o.r[k][j] + (o.b[k][j] * post) * e[k][j];
+                ss += x[k][j] * x[k][j];
+            }
+        const float rstd = rsqrt1(unit_sum<L>(ss, lds, turn++) * p.inv_n + p.eps);
+        if (!valid) continue;
+        if (p.rstd && ul.lane == 0) p.rstd[row] = rstd;
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
-        const int c = ul.lane + k * ul.lanes, n = W - 8 * c;
-        float t[8];
+        for (int k = 0; k < NC; ++k) {
+            float y[8], v[8];
+            if (r_out) store8<RAGGED>(r_out + row * p.ld_res, ul.at(k), n, x[k]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = p.w_post ? bv[k][j] * post : bv[k][j];
-        if (n > 0 && p.w_post) {
-            const Piece<float> w = load8(p.w_post + 8 * c, n);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] *= w[j];
-        }
-        if (n > 0 && p.scale) {
-            const Piece<float> w = load8(p.scale + 8 * c, n);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] *= w[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[k][j] += p.alpha * t[j];
-            ss += x[k][j] * x[k][j];
-        }
-    }
-    const float rstd = 1.0f / sqrtf(unit_sum<L>(ss, lds, 1) * p.inv_n + p.eps);
-    if (valid && p.rstd && ul.lane == 0) p.rstd[row] = rstd;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-        const int c = ul.lane + k * ul.lanes, n = W - 8 * c;
-        float h[8] = {};
-        if (n > 0) {
-            if (p.r_out) store8(static_cast<R*>(p.r_out) + row * p.ld_res + 8 * c, n, x[k]);
-            const Piece<float> w = load8(p.w + 8 * c, n);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[j] = x[k][j] * rstd * w[j];
-            store8(static_cast<T*>(p.h) + row * p.ld_out + 8 * c, n, h);
-        }
-        if (8 * c < (valid ? p.W32 : 0)) {
-            float v[8];
+            for (int j = 0; j < 8; ++j) y[j] = x[k][j] * rstd * w[k][j];
+            store8<RAGGED>(h + row * p.ld_out, ul.at(k), n, y);
+            if (ul.at(k) >= p.W32) continue;
             if (p.r8) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = as_stored(x[k][j], R());
-                ckpt_store(ckpt_row(p.r8, p.scale_off, p.W32, row, 0), c, v);
+                r8.store(row, ul.at(k), v);
             }
-            if (p.b8) ckpt_store(ckpt_row(p.b8, p.scale_off, p.W32, row, 0), c, bv[k]);
+            if (p.b8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = o.b[k][j];
+                b8.store(row, ul.at(k), v);
+            }
             if (p.h8) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = as_stored(h[j], T());
-                ckpt_store(ckpt_row(p.h8, p.scale_off, p.W32, row, 0), c, v);
+                for (int j = 0; j < 8; ++j) v[j] = as_stored(y[j], T());
+                h8.store(row, ul.at(k), v);
             }
         }
     }
@@ -129,129 +146,134 @@ struct BwdP {
     uint8_t *r8, *b8;
     const float *w_post, *scale, *w, *rstd, *rstd_post;
     void *d_r, *d_b;
-    float *part_w, *part_post, *part_scale;  // [slices][W] each, or null
+    float *part_w, *part_s;  // [slices][W] each, or null
     int64_t ld_x, ld_res, ld_out, M, scale_off;
     int W, W32, slices;
     float inv_n, alpha;
 };
 
-// BR: the branch b takes part (norm after the block, or the scale's gradient)
-template <typename T, typename R, int L, int NC, bool BR>
+// BRANCH: b takes part (a norm after the block, or the scale's gradient)
+template <typename T, typename R, int L, int NC, bool RAGGED, bool BRANCH>
 __global__ __launch_bounds__(L ? kRowThreads : 1024) void residual_bwd(BwdP p) {
     __shared__ float lds[L ? kRowThreads * 8 : 32];
+    constexpr int U = units_per_block<L>(), NB = BRANCH ? NC : 1;
     const UnitLane ul = unit_lane<L>();
-    float dw[NC][8], dwp[BR ? NC : 1][8], ds[BR ? NC : 1][8];
+    const int n = p.W;
+    const T* dh = static_cast<const T*>(p.dh);
+    const T* b = static_cast<const T*>(p.b);
+    const R* r_out = static_cast<const R*>(p.r_out);
+    const R* dr_out = static_cast<const R*>(p.dr_out);
+    R* d_r = static_cast<R*>(p.d_r);
+    T* d_b = static_cast<T*>(p.d_b);
+    const Ckpt r8(p.r8, p.scale_off, p.W32, 0), b8(p.b8, p.scale_off, p.W32, 0);
+    struct Row {
+        Piece<T> dh[NC];
+        Piece<R> dr[NC];
+        PieceOr8<R> r[NC];
+        PieceOr8<T> b[NB];
+        float rstd, post;
+    };
+    auto load = [&](Row& o, int64_t row) {
 #pragma unroll
-    for (int k = 0; k < NC; ++k)
+        for (int k = 0; k < NC; ++k) {
+            load8<RAGGED>(o.dh[k], dh + row * p.ld_out, ul.at(k), n);
+            if (!p.r8) load8<RAGGED>(o.r[k].t, r_out + row * p.ld_res, ul.at(k), n);
+            else if (ul.at(k) < n) o.r[k].c = r8.load(row, ul.at(k));
+            if (p.dr_out) load8<RAGGED>(o.dr[k], dr_out + row * p.ld_res, ul.at(k), n);
+            if constexpr (BRANCH) {
+                if (!p.b8) load8<RAGGED>(o.b[k].t, b + row * p.ld_x, ul.at(k), n);
+                else if (ul.at(k) < n) o.b[k].c = b8.load(row, ul.at(k));
+            }
+        }
+        o.rstd = p.rstd[row];
+        o.post = BRANCH && p.w_post ? p.rstd_post[row] : 1.0f;
+    };
+    Row next;
+    __builtin_memset(&next, 0, sizeof next);
+    Piece<float> w[NC] = {}, e[NC];
+    float dw[NC][8], ds[NB][8];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+        load8<RAGGED>(w[k], p.w, ul.at(k), n);
+        e[k] = branch_factor<RAGGED>(p.w_post, p.scale, p.alpha, ul.at(k), n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             dw[k][j] = 0.0f;
-            if (BR) dwp[k][j] = ds[k][j] = 0.0f;
+            if (BRANCH) ds[k][j] = 0.0f;
         }
+    }
+    unit_sum_init<L>(lds);
+    int64_t row = (int64_t)blockIdx.x * U + ul.unit;
+    const int64_t step = (int64_t)p.slices * U;
+    if (row < p.M) load(next, row);
     int turn = 0;
-    const int64_t step = (int64_t)p.slices * units_per_block<L>();
-    for (int64_t r0 = (int64_t)blockIdx.x * units_per_block<L>(); r0 < p.M; r0 += step) {
-        const int64_t row = r0 + ul.unit;
-        const bool valid = row < p.M;
-        const int W = valid ? p.W : 0;
-        const int64_t rr = valid ? row : 0;
-        const float rstd = valid ? p.rstd[rr] : 0.0f;
-        float x[NC][8], dn[NC][8], dx[NC][8], v[BR ? NC : 1][8], dot = 0.0f;
+    for (int64_t first = row - ul.unit; first < p.M; first += step, row += step) {
+        const Row o = next;
+        if (row + step < p.M) load(next, row + step);
+        const bool valid = row < p.M;  // else o is the row before: it is not counted again
+        float x[NC][8], dot = 0.0f;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            const int c = ul.lane + k * ul.lanes, n = W - 8 * c;
+            if (p.r8) o.r[k].c.values(x[k]);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[k][j] = o.r[k].t[j];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                x[k][j] = dn[k][j] = dx[k][j] = 0.0f;
-                if (BR) v[k][j] = 0.0f;
-            }
-            if (n <= 0) continue;
-            const Piece<T> d = load8(static_cast<const T*>(p.dh) + rr * p.ld_out + 8 * c, n);
-            if (p.r8) {
-                ckpt_load(ckpt_row(p.r8, p.scale_off, p.W32, rr, 0), c, x[k]);
-            } else {
-                const Piece<R> t = load8(static_cast<const R*>(p.r_out) + rr * p.ld_res + 8 * c, n);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] = t[j];
-            }
-            if (p.dr_out) {
-                const Piece<R> t = load8(static_cast<const R*>(p.dr_out) + rr * p.ld_res + 8 * c, n);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dx[k][j] = t[j];
-            }
-            if constexpr (BR) {
-                if (p.b8) {
-                    ckpt_load(ckpt_row(p.b8, p.scale_off, p.W32, rr, 0), c, v[k]);
-                } else {
-                    const Piece<T> t = load8(static_cast<const T*>(p.b) + rr * p.ld_x + 8 * c, n);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[k][j] = t[j];
-                }
-            }
-            const Piece<float> w = load8(p.w + 8 * c, n);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[k][j] *= rstd;
-                dw[k][j] += d[j] * x[k][j];
-                dn[k][j] = d[j] * w[j];
-                dot += dn[k][j] * x[k][j];
+                x[k][j] *= o.rstd;
+                const float dx = o.dh[k][j] * x[k][j];
+                if (valid) dw[k][j] += dx;
+                dot += dx * w[k][j];
             }
         }
         const float c1 = unit_sum<L>(dot, lds, turn++) * p.inv_n;
-        const float post = BR && p.w_post && valid ? p.rstd_post[rr] : 1.0f;
-        float dot2 = 0.0f;
-        // dn becomes dt, then (norm after the block) dm = dt w_post
+        // x becomes dx, then dm
+        float v[NB][8], dot2 = 0.0f;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            const int c = ul.lane + k * ul.lanes, n = W - 8 * c;
-            if (n <= 0) continue;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dx[k][j] += rstd * (dn[k][j] - x[k][j] * c1);
-            if (p.d_r) store8(static_cast<R*>(p.d_r) + rr * p.ld_res + 8 * c, n, dx[k]);
-            Piece<float> sc, wp;
-            if (p.scale) sc = load8(p.scale + 8 * c, n);
-            if (BR && p.w_post) wp = load8(p.w_post + 8 * c, n);
+            for (int j = 0; j < 8; ++j)
+                x[k][j] = o.rstd * (o.dh[k][j] * w[k][j] - x[k][j] * c1) + o.dr[k][j];
+            if (valid && d_r) store8<RAGGED>(d_r + row * p.ld_res, ul.at(k), n, x[k]);
+            if constexpr (BRANCH) {
+                if (p.b8) o.b[k].c.values(v[k]);
+                else
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float adx = p.alpha * dx[k][j];
-                dn[k][j] = p.scale ? adx * sc[j] : adx;
-                if constexpr (BR) {
-                    v[k][j] *= post;
-                    ds[k][j] += adx * (p.w_post ? v[k][j] * wp[j] : v[k][j]);
-                    if (p.w_post) {
-                        dwp[k][j] += dn[k][j] * v[k][j];
-                        dn[k][j] *= wp[j];
-                        dot2 += dn[k][j] * v[k][j];
-                    }
+                    for (int j = 0; j < 8; ++j) v[k][j] = o.b[k].t[j];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[k][j] *= o.post;
+                    if (valid) ds[k][j] += x[k][j] * v[k][j];
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[k][j] *= e[k][j];
+                if (BRANCH) dot2 += x[k][j] * v[k][j];
+            }
         }
-        if (BR && p.w_post) {
+        if (BRANCH && p.w_post) {
             const float c2 = unit_sum<L>(dot2, lds, turn++) * p.inv_n;
 #pragma unroll
             for (int k = 0; k < NC; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) dn[k][j] = post * (dn[k][j] - v[k][j] * c2);
+                for (int j = 0; j < 8; ++j) x[k][j] = o.post * (x[k][j] - v[k][j] * c2);
         }
-        if (p.d_b)
+        if (valid && d_b)
 #pragma unroll
-            for (int k = 0; k < NC; ++k) {
-                const int c = ul.lane + k * ul.lanes, n = W - 8 * c;
-                if (n > 0) store8(static_cast<T*>(p.d_b) + rr * p.ld_x + 8 * c, n, dn[k]);
-            }
+            for (int k = 0; k < NC; ++k) store8<RAGGED>(d_b + row * p.ld_x, ul.at(k), n, x[k]);
     }
-    const int64_t at = (int64_t)blockIdx.x * p.W;
-    if (p.part_w) store_column_sums<L, NC>(p.part_w + at, p.W, dw, lds);
-    if constexpr (BR) {
-        if (p.part_post) store_column_sums<L, NC>(p.part_post + at, p.W, dwp, lds);
-        if (p.part_scale) store_column_sums<L, NC>(p.part_scale + at, p.W, ds, lds);
-    }
+    const int64_t part = (int64_t)blockIdx.x * p.W;
+    if (p.part_w) store_column_sums<L, NC, RAGGED>(p.part_w + part, n, dw, lds);
+    if constexpr (BRANCH)
+        if (p.part_s) store_column_sums<L, NC, RAGGED>(p.part_s + part, n, ds, lds);
 }
 
-// out[c] = sum_s part[s][c]: 16 columns a workgroup, 64 lanes down the rows.
+// Sums S partial rows: 16 columns a workgroup, 64 lanes down the rows.  Array
+// 0 gives d_w; array 1 the S of the note above, hence d_w_post and d_scale.
 struct SumP {
+    ColumnSums o;
     const float* part;
-    float* out[3];
     int S, W;
 };
 constexpr int kSumCols = 16, kSumRows = 64;
@@ -259,8 +281,6 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sums(SumP p) {
     __shared__ float sm[kSumRows][kSumCols];
     const int c = threadIdx.x % kSumCols, l = threadIdx.x / kSumCols;
     const int col = blockIdx.x * kSumCols + c;
-    float* out = p.out[blockIdx.y];
-    if (!out) return;
     const float* part = p.part + (int64_t)blockIdx.y * p.S * p.W;
     float v = 0.0f;
     if (col < p.W)
@@ -271,7 +291,15 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sums(SumP p) {
         if (l < h) sm[l][c] += sm[l + h][c];
         __syncthreads();
     }
-    if (l == 0 && col < p.W) out[col] = sm[0][c];
+    if (l != 0 || col >= p.W) return;
+    v = sm[0][c];
+    if (blockIdx.y == 0) {
+        if (p.o.d_w) p.o.d_w[col] = v;
+    } else {
+        v *= p.o.alpha;
+        if (p.o.d_w_post) p.o.d_w_post[col] = p.o.scale ? v * p.o.scale[col] : v;
+        if (p.o.d_scale) p.o.d_scale[col] = p.o.w_post ? v * p.o.w_post[col] : v;
+    }
 }
 
 template <typename F>
@@ -293,24 +321,23 @@ int norm_bwd_slices(const NormShape& s) {
     return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 
-int launch_column_sums(const float* part, int S, int W, float* const out[3], int n_arr,
-                       hipStream_t stream) {
-    SumP p = {part, {out[0], out[1], out[2]}, S, W};
-    column_sums<<<dim3((W + kSumCols - 1) / kSumCols, n_arr), kSumCols * kSumRows, 0, stream>>>(p);
+int launch_column_sums(const float* part, int S, int W, const ColumnSums& out, hipStream_t stream) {
+    SumP p = {out, part, S, W};
+    column_sums<<<dim3((W + kSumCols - 1) / kSumCols, out.d_w_post || out.d_scale ? 2 : 1), kSumCols * kSumRows, 0,
+                  stream>>>(p);
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
 int launch_norm_residual_fwd(const ResidualArgs& a, hipStream_t stream) {
     const NormShape& s = a.s;
-    FwdP p = {a.b, a.r, a.w_post, a.scale, a.w, a.r_out, a.h, a.rstd, a.rstd_post, a.r8, a.b8, a.h8,
-              s.ld_x, s.ld_res, s.ld_out, s.M, s.scale_off, s.W, s.W32, s.eps, 1.0f / (float)s.W, s.alpha};
     if (!s.M) return SSM_OK;
     return for_row_shape(s.W, [&](auto rs) {
         using RS = decltype(rs);
-        const dim3 grid = block_grid((s.M + units_per_block<RS::L>() - 1) / units_per_block<RS::L>());
-        const int threads = row_threads<RS>(s.W);
+        const int threads = row_threads<RS>(s.W), slices = row_slices<RS>(s.M, 1, threads);
+        FwdP p = {a.b, a.r, a.w_post, a.scale, a.w, a.r_out, a.h, a.rstd, a.rstd_post, a.r8, a.b8, a.h8, s.ld_x,
+                  s.ld_res, s.ld_out, s.M, s.scale_off, s.W, s.W32, slices, s.eps, 1.0f / (float)s.W, s.alpha};
         for_types(s, [&](auto t, auto r) {
-            residual_fwd<decltype(t), decltype(r), RS::L, RS::NC><<<grid, threads, 0, stream>>>(p);
+            residual_fwd<decltype(t), decltype(r), RS::L, RS::NC, RS::RAGGED><<<slices, threads, 0, stream>>>(p);
         });
         return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
     });
@@ -319,26 +346,27 @@ int launch_norm_residual_fwd(const ResidualArgs& a, hipStream_t stream) {
 int launch_norm_residual_bwd(const ResidualBwdArgs& a, hipStream_t stream) {
     const NormShape& s = a.s;
     const int slices = norm_bwd_slices(s);
-    const int64_t n = (int64_t)slices * s.W;
-    auto part = [&](float* out, int i) { return !out ? nullptr : slices == 1 ? out : a.part + i * n; };
-    BwdP p = {a.dh, a.dr_out, a.r_out, a.b, const_cast<uint8_t*>(a.r8), const_cast<uint8_t*>(a.b8),
-              a.w_post, a.scale, a.w, a.rstd, a.rstd_post, a.d_r, a.d_b,
-              part(a.d_w, 0), part(a.d_w_post, 1), part(a.d_scale, 2),
-              s.ld_x, s.ld_res, s.ld_out, s.M, s.scale_off, s.W, s.W32, slices, 1.0f / (float)s.W, s.alpha};
+    const bool branch = a.w_post || a.d_scale, sums = a.d_w_post || a.d_scale;
+    const bool direct = slices == 1 && !sums;  // d_w is the one partial row
+    float* part_w = direct ? a.d_w : a.d_w || sums ? a.part : nullptr;
+    BwdP p = {a.dh, a.dr_out, a.r_out, a.b, const_cast<uint8_t*>(a.r8), const_cast<uint8_t*>(a.b8), a.w_post,
+              a.scale, a.w, a.rstd, a.rstd_post, a.d_r, a.d_b, part_w,
+              sums ? a.part + (int64_t)slices * s.W : nullptr, s.ld_x, s.ld_res, s.ld_out, s.M, s.scale_off, s.W,
+              s.W32, slices, 1.0f / (float)s.W, s.alpha};
     const int rc = for_row_shape(s.W, [&](auto rs) {
         using RS = decltype(rs);
         const int threads = row_threads<RS>(s.W);
         for_types(s, [&](auto t, auto r) {
             using T = decltype(t);
             using R = decltype(r);
-            if (a.w_post || a.d_scale) residual_bwd<T, R, RS::L, RS::NC, true><<<slices, threads, 0, stream>>>(p);
-            else residual_bwd<T, R, RS::L, RS::NC, false><<<slices, threads, 0, stream>>>(p);
+            if (branch) residual_bwd<T, R, RS::L, RS::NC, RS::RAGGED, true><<<slices, threads, 0, stream>>>(p);
+            else residual_bwd<T, R, RS::L, RS::NC, RS::RAGGED, false><<<slices, threads, 0, stream>>>(p);
         });
         return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
     });
-    if (rc != SSM_OK || slices == 1 || !(a.d_w || a.d_w_post || a.d_scale)) return rc;
-    float* const out[3] = {a.d_w, a.d_w_post, a.d_scale};
-    return launch_column_sums(a.part, slices, s.W, out, a.d_w_post || a.d_scale ? 3 : 1, stream);
+    if (rc != SSM_OK || direct || !part_w) return rc;
+    return launch_column_sums(a.part, slices, s.W, ColumnSums{a.d_w, a.d_w_post, a.d_scale, a.scale, a.w_post, s.alpha},
+                              stream);
 }
 
 }  // namespace ssm
