@@ -232,10 +232,7 @@ int for_row_shape_of(int pieces, F&& f) {
     if (pieces <= 32) return f(RowShape<32, 1, RAGGED>{});
     if (pieces <= 64) return f(RowShape<64, 1, RAGGED>{});
     if (pieces <= 128) return f(RowShape<64, 2, RAGGED>{});
-#ifndef NC1MAX
-#define NC1MAX 1024
-#endif
-    if (pieces <= NC1MAX) return f(RowShape<0, 1, RAGGED>{});
+    if (pieces <= 1024) return f(RowShape<0, 1, RAGGED>{});
     if (pieces <= 2048) return f(RowShape<0, 2, RAGGED>{});
     return f(RowShape<0, 4, RAGGED>{});
 }
@@ -251,15 +248,14 @@ int row_threads(int Wg) {
     return ((pieces + RS::NC - 1) / RS::NC + 63) / 64 * 64;
 }
 
-#ifndef ROW_WAVES
-#define ROW_WAVES 24
-#endif
-// Slices of a kernel whose workgroups (slice, group) walk the rows: as many as
-// stay resident on 256 compute units at 24 waves each, fewer for fewer rows.
+// Slices of a kernel whose workgroups (slice, group) walk the rows: 16 waves on
+// each of 256 compute units, fewer for fewer rows.  (32768 x 5120 bf16, gated:
+// 177, 176, 184, 222 us with 12, 16, 24, 32 waves; one workgroup a row 420 us.)
+constexpr int kRowWaves = 16;
 template <typename RS>
 int row_slices(int64_t M, int G, int threads) {
     const int64_t need = (M + units_per_block<RS::L>() - 1) / units_per_block<RS::L>();
-    const int64_t most = 256 * (int64_t)(ROW_WAVES * 64 / threads > 0 ? ROW_WAVES * 64 / threads : 1) / G;
+    const int64_t most = 256 * (int64_t)(kRowWaves * 64 / threads > 0 ? kRowWaves * 64 / threads : 1) / G;
     return (int)(need < most ? need : most > 0 ? most : 1);
 }
 
