@@ -1,6 +1,6 @@
 // Device helpers of the row kernels (norm_gated.hip, norm_residual.hip,
 // ckpt8.hip).  A unit, one (row, group), is held in registers by L lanes of a
-// wave (L = 8, 16, 32, 64) or, with L = 0, by a whole workgroup; where that
+// wave (L = 4, 8, 16, 32, 64) or, with L = 0, by a whole workgroup; where that
 // would leave many lanes idle, a workgroup holds a row with all its groups
 // (SEGMENTS) and adds each group's lanes through LDS.  Lane t of n
 // holds the 8-value pieces t, t + n, ... of the unit, as 16-byte accesses at
@@ -130,12 +130,13 @@ template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
-// sum over the 16 lanes of a DPP row (N = 16) or each half of it (N = 8), in every lane
+// sum over the 16 lanes of a DPP row (N = 16), each half (N = 8) or quad (N = 4)
+// of it, in every lane
 template <int N>
 __device__ __forceinline__ float sum16(float v) {
     v += quad_xor1(v);
     v += quad_xor2(v);
-    v += dpp<0x141>(v);                 // row_half_mirror: the other quad of 8
+    if (N >= 8) v += dpp<0x141>(v);     // row_half_mirror: the other quad of 8
     if (N == 16) v += dpp<0x140>(v);    // row_mirror: the other half
     return v;
 }
@@ -197,7 +198,7 @@ __device__ __forceinline__ void unit_sum(const float v[NC], float sum[NC], SumMe
     float a = v[0];
 #pragma unroll
     for (int k = 1; k < NC; ++k) a += v[k];
-    if constexpr (L == 8 || L == 16) a = sum16<L == 8 ? 8 : 16>(a);
+    if constexpr (L == 4 || L == 8 || L == 16) a = sum16<L ? L : 16>(a);
     else if constexpr (L == 32) a = sum_halves(sum16<16>(a));
     else a = sum_wave(a);
     if constexpr (L == 0) {
@@ -304,12 +305,13 @@ struct RowShape {
     static constexpr bool RAGGED = RAGGED_, SEGMENTS = SEGMENTS_;
 };
 
-// Host: the smallest unit that holds a group of so many pieces (8, 16, 32 or
+// Host: the smallest unit that holds a group of so many pieces (4, 8, 16, 32 or
 // 64 lanes with one piece each, a wave with two, then a workgroup with 1, 2 or
 // 4 pieces a lane), so that narrow rows share a wave and wide ones keep every
 // lane busy.
 template <bool RAGGED, typename F>
 int for_unit_shape(int pieces, F&& f) {
+    if (pieces <= 4) return f(RowShape<4, 1, RAGGED>{});
     if (pieces <= 8) return f(RowShape<8, 1, RAGGED>{});
     if (pieces <= 16) return f(RowShape<16, 1, RAGGED>{});
     if (pieces <= 32) return f(RowShape<32, 1, RAGGED>{});
