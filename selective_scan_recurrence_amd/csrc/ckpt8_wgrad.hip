@@ -67,7 +67,7 @@ struct DyRaw<bf16_t> {
         r[j] = __builtin_amdgcn_raw_buffer_load_b64(b, at, row, 0);
     }
     __device__ __forceinline__ void zero(int j) { r[j] = u32x2{0, 0}; }
-    __device__ __forceinline__ void frags(u32x4 f[1][4]) const {
+    __device__ __forceinline__ void frags(u32x4 (&f)[1][4]) const {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -84,7 +84,7 @@ struct DyRaw<float> {
     __device__ __forceinline__ void zero(int j) { r[j] = u32x4{0, 0, 0, 0}; }
     // v = hi + mid + lo, each the bf16 nearest to what is left; an infinity or
     // a NaN is all in hi
-    __device__ __forceinline__ void frags(u32x4 f[3][4]) const {
+    __device__ __forceinline__ void frags(u32x4 (&f)[3][4]) const {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -193,9 +193,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP
         for (int j = 0; j < 8; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
 
     // one half step: rows 32 ks .. 32 ks + 31 of the buffer
-    auto multiply = [&](const DyRaw<T>& d, const uint8_t* buf, int ks) {
-        u32x4 a[NT][4];
-        d.frags(a);
+    auto multiply = [&](const u32x4 (&a)[NT][4], const uint8_t* buf, int ks) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = 4 * i16 + (j & 3) + 64 * (j >> 2);
@@ -210,26 +208,34 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP
         }
     };
 
-    // buffers alternate: step n + 1 is loaded while step n is multiplied, and
-    // written to the other buffer after it, with one barrier a step
-    auto load = [&](int m0, auto last) {
-        const auto codes = rsrc_of(p.x8 + (int64_t)m0 * p.W32);
-        const auto scales = rsrc_of(p.x8 + p.scale_off + (int64_t)m0 * blocks);
-        const auto rows = rsrc_of(dy + (int64_t)m0 * p.ld);
-        load_x(m0, codes, scales, last);
-        load_dy(raw[0], m0, 0, rows, last);
-        load_dy(raw[1], m0, 1, rows, last);
-    };
-    auto step = [&](int m0, int cur, auto last) {  // multiplies buffer cur, loads the step at m0
-        const DyRaw<T> now[2] = {raw[0], raw[1]};
-        load(m0, last);
-        multiply(now[0], lds[cur], 0);
-        multiply(now[1], lds[cur], 1);
+    // Buffers alternate: step n + 1 is loaded while step n is multiplied, and
+    // written to the other buffer after it, with one barrier a step.  Each load
+    // is pinned a whole step ahead of its use (the compiler would sink them to
+    // save registers, and every step then waits for memory); a half step's dy
+    // is turned into operands first, so that its registers take the next one's.
+    auto step = [&](int next, int cur, auto last) {  // multiplies buffer cur, loads the step at next
+        u32x4 a[NT][4];
+        const auto rows = rsrc_of(dy + (int64_t)next * p.ld);
+        load_x(next, rsrc_of(p.x8 + (int64_t)next * p.W32), rsrc_of(p.x8 + p.scale_off + (int64_t)next * blocks), last);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            raw[ks].frags(a);
+            load_dy(raw[ks], next, ks, rows, last);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(a, lds[cur], ks);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         store_x(lds[cur ^ 1]);
         __syncthreads();
     };
     constexpr std::false_type whole{};
     constexpr std::true_type partial{};
+    auto load = [&](int m0, auto last) {
+        const auto rows = rsrc_of(dy + (int64_t)m0 * p.ld);
+        load_x(m0, rsrc_of(p.x8 + (int64_t)m0 * p.W32), rsrc_of(p.x8 + p.scale_off + (int64_t)m0 * blocks), last);
+        load_dy(raw[0], m0, 0, rows, last);
+        load_dy(raw[1], m0, 1, rows, last);
+    };
     if (m_begin < m_end) {
         int m = m_begin, cur = 0;
         if (m + kTM <= m_end) load(m, whole);
@@ -241,8 +247,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP
             step(m + kTM, cur, partial);
             cur ^= 1;
         }
-        multiply(raw[0], lds[cur], 0);
-        multiply(raw[1], lds[cur], 1);
+        u32x4 a[NT][4];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            raw[ks].frags(a);
+            multiply(a, lds[cur], ks);
+        }
     }
 
     // lane 16g + i holds rows 16g + 4r + t (r = 0 .. 3) and, over j % 4, four
