@@ -292,20 +292,33 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP
         }
 }
 
-// dw[e] = sum_s part[s][e] (+ dw[e])
+// dw[e] = sum_s part[s][e] (+ dw[e]): SL lanes share an element, lane l taking
+// the parts l, l + SL, ..., and are added in order.
+template <int SL>
 __global__ __launch_bounds__(256) void wgrad_join(const float* __restrict__ part, float* dw, int64_t n, int S,
                                                   bool accumulate) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (e >= n) return;
+    constexpr int E = 256 / SL;
+    __shared__ float sm[SL > 1 ? SL : 1][E];
+    const int l = threadIdx.x / E, i = threadIdx.x % E;
+    const int64_t e = (int64_t)blockIdx.x * E + i;
     float v = 0.0f;
-    for (int s = 0; s < S; ++s) v += part[s * n + e];
-    dw[e] = accumulate ? dw[e] + v : v;
+    if (e < n)
+#pragma unroll 4
+        for (int s = l; s < S; s += SL) v += part[s * n + e];
+    if constexpr (SL > 1) {
+        sm[l][i] = v;
+        __syncthreads();
+        if (l > 0) return;
+#pragma unroll
+        for (int s = 1; s < SL; ++s) v += sm[s][i];
+    }
+    if (e < n) dw[e] = accumulate ? dw[e] + v : v;
 }
 
 struct Split {
     int count, rows;
 };
-// Parts of the rows, each of at least two steps: the count with the least
+// Parts of the rows, each of at least a step: the count with the least
 // modelled time.  A step takes 1.25 us with one workgroup on a compute unit
 // and 2.0 with two (bf16), 3.9 with the one that f32 has room for; the join
 // costs a launch and moves each partial twice at 5 TB/s.  (8192 x 1024 x 512
@@ -314,7 +327,7 @@ Split split_rows(int64_t M, int64_t W, int64_t O, int dtype) {
     const int64_t tiles = ((W + kTC - 1) / kTC) * ((O + kTO - 1) / kTO), steps = (M + kTM - 1) / kTM;
     Split best{1, (int)((steps ? steps : 1) * kTM)};
     double best_us = 0;
-    for (int64_t n = 1; n == 1 || (n <= steps / 2 && n * tiles <= 512); ++n) {
+    for (int64_t n = 1; n == 1 || (n <= steps && n * tiles <= 512); ++n) {
         const int64_t each = steps ? (steps + n - 1) / n : 1, count = steps ? (steps + each - 1) / each : 1;
         const int64_t wgs = tiles * count, left = wgs % 512;
         const double step_us = dtype == SSM_BF16 ? (double)(wgs / 512) * 2.0 + (left == 0 ? 0.0 : left <= 256 ? 1.25 : 2.0)
@@ -354,7 +367,9 @@ int launch_ckpt8_wgrad(const void* dy, int64_t ld, const uint8_t* x8, float* dw,
     }
     if (joined) {
         const int64_t n = W * O;
-        wgrad_join<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(static_cast<float*>(ws), dw, n, s.count, accumulate);
+        const float* part = static_cast<float*>(ws);
+        if (s.count <= 8) wgrad_join<1><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(part, dw, n, s.count, accumulate);
+        else wgrad_join<8><<<(unsigned)((n + 31) / 32), 256, 0, stream>>>(part, dw, n, s.count, accumulate);
     }
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
