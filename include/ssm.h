@@ -394,7 +394,7 @@ enum { SSM_NORM_GATE_AFTER = 1u }; /* gated norm: the gate multiplies the normal
 
 typedef struct ssm_norm_desc {
     int64_t n_rows;     /* rows (>= 0); n_rows * n_group <= 2^31 - 1              */
-    int64_t width;      /* columns (>= 1)                                         */
+    int64_t width;      /* columns, 1..2^22                                       */
     int64_t n_group;    /* gated norm: groups of width / n_group columns (at most
                            32768), each with its own rms; residual norm: 1        */
     int64_t ld_x;       /* row stride of y and d_y, or of b and d_b               */
@@ -433,7 +433,8 @@ int ssm_ckpt8_unpack(const void *ckpt, void *x, int64_t ld, int64_t n_rows, int6
  * [n_rows][n_out] (dtype, row stride ld) and the checkpoint of x
  * [n_rows][width]:
  *   dw[o][c] = sum_m dy[m][o] x[m][c]   (+ dw[o][c] when accumulate != 0)
- * dw [n_out][width] f32, dense.  Products are exact and summed in f32.
+ * dw [n_out][width] f32, dense.  Products are exact and summed in f32 (those
+ * with a subnormal factor may count as zero).
  * width, n_out and ld are at most 2^22, width * n_out 2^37.  workspace:
  * ssm_ckpt8_wgrad_workspace_bytes bytes, 256-byte aligned, no initial
  * contents (may be NULL when that is 0). */

@@ -25,7 +25,7 @@ int check_norm(const ssm_norm_desc* d, NormShape* out) {
     if (!d) return SSM_ERR_NULL;
     if (!known(d->io_dtype) || !known(d->res_dtype)) return SSM_ERR_DTYPE;
     if (d->reserved != 0 || (d->flags & ~(uint32_t)SSM_NORM_GATE_AFTER)) return SSM_ERR_SHAPE;
-    if (d->n_rows < 0 || d->width < 1 || d->n_group < 1 || d->width > INT_MAX - 1024 ||
+    if (d->n_rows < 0 || d->width < 1 || d->n_group < 1 || d->width > 1 << 22 ||
         d->n_group > d->width || d->width % d->n_group || d->width / d->n_group > kNormMaxGroup)
         return SSM_ERR_SHAPE;
     int64_t t;

@@ -82,8 +82,9 @@ struct DyRaw<float> {
         r[j] = __builtin_amdgcn_raw_buffer_load_b128(b, at, row, 0);
     }
     __device__ __forceinline__ void zero(int j) { r[j] = u32x4{0, 0, 0, 0}; }
-    // v = hi + mid + lo, each the bf16 nearest to what is left; an infinity or
-    // a NaN is all in hi
+    // v = hi + mid + lo, the three bytes of its significand: each what is left
+    // with the low half cut off, so exact, and no rounding passes the largest
+    // value.  An infinity or a NaN is all in hi.
     __device__ __forceinline__ void frags(u32x4 (&f)[3][4]) const {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -92,16 +93,16 @@ struct DyRaw<float> {
                 uint32_t w[3][2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float v = __uint_as_float(r[2 * p + h][t]);
+                    const float v = __uint_as_float(r[2 * p + h][t]);
                     const bool finite = fabsf(v) < __builtin_inff();
-#pragma unroll
-                    for (int n = 0; n < 3; ++n) {
-                        w[n][h] = bf16_rne(v);
-                        v = finite ? v - to_f32((bf16_t)w[n][h]) : 0.0f;
-                    }
+                    const uint32_t top = r[2 * p + h][t] & 0xffff0000u;
+                    w[0][h] = v != v ? 0x7fc00000u : top;
+                    const float left = finite ? v - __uint_as_float(top) : 0.0f;
+                    w[1][h] = __float_as_uint(left) & 0xffff0000u;
+                    w[2][h] = __float_as_uint(left - __uint_as_float(w[1][h]));
                 }
 #pragma unroll
-                for (int n = 0; n < 3; ++n) f[n][t][p] = w[n][0] | w[n][1] << 16;
+                for (int n = 0; n < 3; ++n) f[n][t][p] = pair_rows(w[n][0], w[n][1], 1);
             }
     }
 };
@@ -327,7 +328,7 @@ Split split_rows(int64_t M, int64_t W, int64_t O, int dtype) {
     const int64_t tiles = ((W + kTC - 1) / kTC) * ((O + kTO - 1) / kTO), steps = (M + kTM - 1) / kTM;
     Split best{1, (int)((steps ? steps : 1) * kTM)};
     double best_us = 0;
-    for (int64_t n = 1; n == 1 || (n <= steps && n * tiles <= 512); ++n) {
+    for (int64_t n = 1, next; n == 1 || (n <= steps && n * tiles <= 512); n = next) {
         const int64_t each = steps ? (steps + n - 1) / n : 1, count = steps ? (steps + each - 1) / each : 1;
         const int64_t wgs = tiles * count, left = wgs % 512;
         const double step_us = dtype == SSM_BF16 ? (double)(wgs / 512) * 2.0 + (left == 0 ? 0.0 : left <= 256 ? 1.25 : 2.0)
@@ -337,6 +338,7 @@ Split split_rows(int64_t M, int64_t W, int64_t O, int dtype) {
             best = Split{(int)count, (int)(each * kTM)};
             best_us = us;
         }
+        next = each > 1 ? (steps + each - 2) / (each - 1) : n + steps + 1;  // the next count with fewer steps each
     }
     return best;
 }

@@ -53,7 +53,7 @@ NORMS = [_gated_fwd, _gated_bwd, _residual_fwd, _residual_bwd]
 
 @pytest.mark.parametrize("call", NORMS)
 @pytest.mark.parametrize("field,value", [
-    ("n_rows", -1), ("n_rows", 1 << 31), ("width", 0), ("width", -8), ("width", 1 << 31),
+    ("n_rows", -1), ("n_rows", 1 << 31), ("width", 0), ("width", -8), ("width", 1 << 31), ("width", (1 << 22) + 1),
     ("width", 40000), ("n_group", 0), ("n_group", 5), ("n_group", 192), ("ld_x", 95), ("ld_z", 1),
     ("ld_res", -96), ("ld_out", 95), ("ld_x", 1 << 61), ("eps", 0.0), ("eps", -1e-5),
     ("eps", float("nan")), ("eps", float("inf")), ("res_scale", float("inf")),
@@ -204,6 +204,16 @@ def test_wgrad_refusals():
         assert _status(wgrad, rows=8192, width=512, n_out=512, ld=512, ws_bytes=need - 1) == \
             ssm.SSM_ERR_WORKSPACE
         assert _status(wgrad, rows=8192, width=512, n_out=512, ld=512, ws=None) == ssm.SSM_ERR_NULL
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_wgrad_workspace(dtype):
+    """Whole partials of dw, none where one workgroup a tile takes all rows."""
+    for rows in (0, 1, 63, 64, 65, 777, 8192, 100000, (1 << 31) - 2000):
+        for width, n_out in ((1, 1), (515, 130), (2560, 10576), (1 << 22, 3)):
+            n = ssm.ssm_ckpt8_wgrad_workspace_bytes(rows, width, n_out, dtype)
+            counts = [0, *range(2, min(512, -(-rows // 64)) + 1)]  # rounded up to 256 bytes
+            assert n in {-(-4 * width * n_out * k // 256) * 256 for k in counts}, (rows, width, n_out)
 
 
 def test_tensors_are_checked():

@@ -82,6 +82,19 @@ def test_wide_scales():
     R.check("dw", got, dy.double().t() @ back, dy.double().abs().t() @ back.abs(), "f32", _bound(rows))
 
 
+def test_largest_gradients():
+    """f32 gradients up to the largest value, which no part of their split may
+    pass, and ones whose low parts are subnormal."""
+    top = torch.finfo(torch.float32).max
+    dy = torch.tensor([[top, -top, 1.0, 2.0 ** -100 * (1 + 2.0 ** -23)]] * 3)
+    x = torch.zeros(3, 32)
+    x[0] = 0.5
+    got = ops.ckpt8_wgrad(dy.cuda(), ops.ckpt8_pack(x.cuda()), 32).double().cpu()
+    want = (dy[0].double() * 0.5).unsqueeze(1).expand(4, 32)
+    assert torch.equal(got[:3], want[:3])
+    assert ((got[3] - want[3]).abs() <= want[3] * 2.0 ** -23).all()
+
+
 def test_nan_stays_in_its_column():
     x, dy = R.draw(1, 50, 96), R.draw(2, 50, 40)
     x[7, 5] = float("nan")

@@ -54,6 +54,48 @@ def test_forward_and_backward(rows, width, groups, pad, after, io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,width,groups", [(5, 2880, 4), (3, 4160, 4), (4, 2880, 40), (300, 72, 3),
+                                               (2, 8192, 1024), (7, 1344, 7)])
+def test_many_groups(rows, width, groups, io):
+    """Groups whose sums span lanes and waves of a row, one piece each, more
+    groups than waves."""
+    dt = R.DTYPES[io]
+    y, z, w, zd = _inputs(rows, width, 0, io, seed=width)
+    d = ops.norm_desc(n_rows=rows, width=width, n_group=groups, io=io, eps=EPS)
+    rstd = torch.empty(rows, groups, device="cuda")
+    r = ops.norm_gated_fwd(d, y.cuda(), zd, w.cuda(), rstd=rstd)
+    want, inv = R.gated_fwd(y.double(), z.double(), w.double(), groups, EPS)
+    R.check("out", r.out, want, want.abs(), io)
+    R.check("rstd", rstd, inv, inv, "f32")
+    dout = R.draw(width + 9, rows, width).to(dt)
+    g = ops.norm_gated_bwd(d, dout.cuda(), w.cuda(), rstd, y=y.cuda(), z=zd)
+    want = R.gated_bwd(dout.double(), y.double(), z.double(), w.double(), inv, groups)
+    R.check("d_y", g.d_y, *want["d_y"], io)
+    R.check("d_z", g.d_z, *want["d_z"], io)
+    R.check("d_w", g.d_w, *want["d_w"], "f32", R.COUNT_SUM)
+
+
+@pytest.mark.parametrize("after", [False, True])
+@pytest.mark.parametrize("rows,width,groups", [(12000, 5120, 8), (24000, 2048, 1), (400000, 128, 1)])
+def test_matrices_past_the_cache(rows, width, groups, after):
+    """Calls large enough to store past the caches give, row by row, what a
+    call on a few of their rows gives."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    y, z, dout = (torch.randn(rows, width, generator=gen, device="cuda").bfloat16() for _ in range(3))
+    w = torch.rand(width, generator=gen, device="cuda") + 0.5
+
+    def run(y, z, dout):
+        d = ops.norm_desc(n_rows=y.shape[0], width=width, n_group=groups, eps=EPS, gate_after=after)
+        f = ops.norm_gated_fwd(d, y, z, w, train=True)
+        g = ops.norm_gated_bwd(d, dout, w, f.rstd, y=y, z=z)
+        return f.out, f.rstd, g.d_y, g.d_z
+
+    some = torch.cat([torch.arange(5), torch.arange(rows // 2, rows // 2 + 40), torch.arange(rows - 6, rows)]).cuda()
+    for big, small in zip(run(y, z, dout), run(y[some], z[some], dout[some])):
+        assert torch.equal(big[some], small)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("after", [False, True])
 @pytest.mark.parametrize("rows,width,groups", [(5, 64, 1), (33, 256, 8), (7, 515, 1), (4, 5120, 8),
                                                (3, 10240, 1), (300, 40, 1)])
