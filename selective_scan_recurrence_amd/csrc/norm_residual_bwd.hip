@@ -148,14 +148,15 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_bwd(BwdP 
         if (p.part_s) store_column_sums<L, NC, RAGGED>(p.part_s + part, n, ds, sm);
 }
 
-// Sums S partial rows: 16 columns a workgroup, 64 lanes down the rows.  Array
+// Sums S partial rows: 32 columns (a cache line) a workgroup, 32 lanes down the
+// rows.  Array
 // 0 gives d_w; array 1 the S of the note above, hence d_w_post and d_scale.
 struct SumP {
     ColumnSums o;
     const float* part;
     int S, W;
 };
-constexpr int kSumCols = 16, kSumRows = 64;
+constexpr int kSumCols = 32, kSumRows = 32;
 __global__ __launch_bounds__(kSumCols* kSumRows) void column_sums(SumP p) {
     __shared__ float sm[kSumRows][kSumCols];
     const int c = threadIdx.x % kSumCols, l = threadIdx.x / kSumCols;
@@ -184,19 +185,23 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sums(SumP p) {
 
 }  // namespace
 
-// A unit of a workgroup takes at least 2 rows, and there are at most 768
-// workgroups over all groups, so that the partial sums stay few beside the
-// rows.  (1111 x 771 f32, gate after: 8.5, 9.4, 13.5, 21.4 us with 1, 2, 4, 8
-// rows, where the sum of the partial rows grows from 2 to 5 us with 1.  At
-// 16384 x 2560, 512 and 768 workgroups are alike, 1024 are 5% slower.)
+// A unit of a workgroup takes at least 2 rows, and the workgroups are those of
+// 16 waves on each of 256 compute units, at most 768, so that the partial sums
+// stay few beside the rows.  (1111 x 771 f32, gate after: 8.5, 9.4, 13.5, 21.4
+// us with 1, 2, 4, 8 rows, where the sum of the partial rows grows from 2 to 5
+// us with 1.  At 16384 x 2560, 512 and 768 workgroups are alike, 1024 are 5%
+// slower; at 16384 x 5120 in 8 groups 256, 512 and 768 are alike.)
 int norm_bwd_slices(const NormShape& s) {
-    int rows = 1, units = 1;
-    for_row_shape<true>(s.W, s.G, [&](auto rs, int, int u) {
+    int rows = 1;
+    int64_t most = 1;
+    for_row_shape<true>(s.W, s.G, [&](auto rs, int threads, int units) {
         rows = 2 * units_per_block<decltype(rs)::L>();
-        units = u;
+        const int each = 16 * 64 / threads;
+        most = 256 * (int64_t)(each > 0 ? each : 1) / units;
         return 0;
     });
-    const int64_t want = (s.M + rows - 1) / rows, most = 768 / units > 0 ? 768 / units : 1;
+    most = most < 1 ? 1 : most > 768 ? 768 : most;
+    const int64_t want = (s.M + rows - 1) / rows;
     return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 
