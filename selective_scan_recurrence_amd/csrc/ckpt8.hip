@@ -2,6 +2,8 @@
 // the format).  A lane takes 8 consecutive values; four lanes share a block.
 // Bound by HBM: the values cross it once in their type and once in 33/32
 // bytes.
+#include <type_traits>
+
 #include "block_internal.h"
 #include "norm_rows.h"
 
@@ -31,7 +33,7 @@ __device__ __forceinline__ Place place(const CkptP& p, int64_t first_row, int fi
     return Place{first_row + c / (uint32_t)p.P, 8 * (int)(c % (uint32_t)p.P)};
 }
 
-template <typename T, bool RAGGED>
+template <typename T, Ends RAGGED>
 __global__ __launch_bounds__(256) void ckpt8_pack(CkptP p) {
     constexpr int kEach = kPackEach, kPieces = 256 * kEach;
     const int64_t first = block_id() * kPieces, row0 = first / p.P;
@@ -50,13 +52,14 @@ __global__ __launch_bounds__(256) void ckpt8_pack(CkptP p) {
     for (int e = 0; e < kEach; ++e) {
         if (first + threadIdx.x + 256 * e >= p.pieces) return;
         float v[8];
+        settle8<RAGGED>(t[e], at[e].at, p.W);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = t[e][j];
         CkptRow(p.x8, p.scale_off, p.W32, at[e].row, 0).store(at[e].at, v);
     }
 }
 
-template <typename T, bool RAGGED>
+template <typename T, Ends RAGGED>
 __global__ __launch_bounds__(256) void ckpt8_unpack(CkptP p) {
     constexpr int kEach = kUnpackEach, kPieces = 256 * kEach;
     const int64_t first = block_id() * kPieces, row0 = first / p.P;
@@ -88,13 +91,13 @@ int launch(uint8_t* x8, void* x, int64_t ld, int64_t M, int64_t W, int dtype, hi
     const CkptP p = {x8, x, ld, pieces, M * W32, (int)(W32 / 8), (int)W, (int)W32};
     auto go = [&](auto t) {
         using T = decltype(t);
-        if constexpr (PACK) {
-            if (W % 8) ckpt8_pack<T, true><<<grid, 256, 0, stream>>>(p);
-            else ckpt8_pack<T, false><<<grid, 256, 0, stream>>>(p);
-        } else {
-            if (W % 8) ckpt8_unpack<T, true><<<grid, 256, 0, stream>>>(p);
-            else ckpt8_unpack<T, false><<<grid, 256, 0, stream>>>(p);
-        }
+        auto ends = [&](auto e) {
+            if constexpr (PACK) ckpt8_pack<T, e.value><<<grid, 256, 0, stream>>>(p);
+            else ckpt8_unpack<T, e.value><<<grid, 256, 0, stream>>>(p);
+        };
+        if (W < 8) ends(std::integral_constant<Ends, kTiny>());
+        else if (W % 8) ends(std::integral_constant<Ends, kRagged>());
+        else ends(std::integral_constant<Ends, kWhole>());
     };
     if (dtype == SSM_BF16) go(bf16_t());
     else go(float());

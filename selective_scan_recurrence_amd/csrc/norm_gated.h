@@ -21,7 +21,7 @@ void for_gate(const NormShape& s, bool gated, int matrices, F&& f) {
     const bool past = s.M * s.W * (s.io == SSM_BF16 ? 2 : 4) * matrices > kStreamBytes;
     auto typed = [&](auto t) {
         auto streamed = [&](auto gate) {
-            if constexpr (RS::NC == 1 && !RS::RAGGED && gate.value != kNone)
+            if constexpr (RS::NC == 1 && RS::RAGGED == kWhole && gate.value != kNone)
                 if (past) return f(t, gate, std::true_type());
             f(t, gate, std::false_type());
         };

@@ -32,7 +32,7 @@ struct FwdP {
 template <typename T, typename RS, Gate GATE, bool STREAM>
 __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_fwd(FwdP p) {
     constexpr int L = RS::L, NC = RS::NC, U = units_per_block<L>();
-    constexpr bool RAGGED = RS::RAGGED;
+    constexpr Ends RAGGED = RS::RAGGED;
     __shared__ SumMemory<L, NC, RS::SEGMENTS> lds;
     const RowLane<RS> lane(p.G, p.Wg);
     const Groups groups{p.G, p.Wg / 8};
@@ -56,17 +56,19 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_fwd(FwdP p) 
     Row next = {};
     Piece<float> w[NC] = {};
 #pragma unroll
-    for (int k = 0; k < NC; ++k) load8<RAGGED>(w[k], p.w + c0, lane.at(k), n);
+    for (int k = 0; k < NC; ++k) fetch8<RAGGED>(w[k], p.w + c0, lane.at(k), n);
     lds.init();
     if (row < p.M) load(next);
     int turn = 0;
-    walk_rows(next, row - lane.ul.unit, p.M, stride, [&](const Row& r, Row& next) {
+    walk_rows(next, row - lane.ul.unit, p.M, stride, [&](Row& r, Row& next) {
         y.skip(stride);
         z.skip(stride);
         if (row + stride < p.M) load(next);
         float x[NC][8], ss[NC], rstd[NC];  // x: what is normalised
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
+            settle8<RAGGED>(r.y[k], lane.at(k), n);
+            if (GATE != kNone) settle8<RAGGED>(r.z[k], lane.at(k), n);
             ss[k] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {

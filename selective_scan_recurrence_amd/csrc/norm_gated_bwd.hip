@@ -24,7 +24,7 @@ struct BwdP {
 template <typename T, typename RS, Gate GATE, bool STREAM>
 __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) {
     constexpr int L = RS::L, NC = RS::NC, U = units_per_block<L>();
-    constexpr bool RAGGED = RS::RAGGED;
+    constexpr Ends RAGGED = RS::RAGGED;
     __shared__ SumMemory<L, NC, RS::SEGMENTS> lds;
     __shared__ float sm[L ? kRowThreads * 8 : 1];
     const RowLane<RS> lane(p.G, p.Wg);
@@ -60,14 +60,14 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) 
     float dw[NC][8];
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-        load8<RAGGED>(w[k], p.w + c0, lane.at(k), n);
+        fetch8<RAGGED>(w[k], p.w + c0, lane.at(k), n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
     }
     lds.init();
     if (row < p.M) load(next);
     int turn = 0;
-    walk_rows(next, row - lane.ul.unit, p.M, stride, [&](const Row& r, Row& next) {
+    walk_rows(next, row - lane.ul.unit, p.M, stride, [&](Row& r, Row& next) {
         dout.skip(stride);
         y.skip(stride);
         z.skip(stride);
@@ -80,16 +80,9 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) 
         float x[NC][8], yv[NC][8], zv[NC][8], dot[NC], c1[NC];
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            if (p.y8) r.y[k].c.values(yv[k]);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) yv[k][j] = r.y[k].t[j];
-            if (GATE != kNone) {
-                if (p.z8) r.z[k].c.values(zv[k]);
-                else
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) zv[k][j] = r.z[k].t[j];
-            }
+            settle8<RAGGED>(r.d[k], lane.at(k), n);
+            r.y[k].template values<RAGGED>(p.y8, yv[k], lane.at(k), n);
+            if (GATE != kNone) r.z[k].template values<RAGGED>(p.z8, zv[k], lane.at(k), n);
             dot[k] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {

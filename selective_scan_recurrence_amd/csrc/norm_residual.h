@@ -8,18 +8,18 @@
 namespace ssm {
 
 // e of this lane's pieces
-template <bool RAGGED>
+template <Ends RAGGED>
 __device__ __forceinline__ Piece<float> branch_factor(const float* w_post, const float* scale, float alpha, int at, int n) {
     Piece<float> e = {}, t = {};
 #pragma unroll
     for (int j = 0; j < 8; ++j) e.d[j] = alpha;
     if (scale) {
-        load8<RAGGED>(t, scale, at, n);
+        fetch8<RAGGED>(t, scale, at, n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) e.d[j] *= t.d[j];
     }
     if (w_post) {
-        load8<RAGGED>(t, w_post, at, n);
+        fetch8<RAGGED>(t, w_post, at, n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) e.d[j] *= t.d[j];
     }

@@ -34,7 +34,7 @@ struct FwdP {
 template <typename T, typename R, typename RS>
 __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_fwd(FwdP p) {
     constexpr int L = RS::L, NC = RS::NC, U = units_per_block<L>();
-    constexpr bool RAGGED = RS::RAGGED;
+    constexpr Ends RAGGED = RS::RAGGED;
     __shared__ SumMemory<L, NC, false> lds;
     const RowLane<RS> lane(1, p.W);
     const Groups groups{1, 0};
@@ -60,20 +60,24 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_fwd(FwdP 
     Piece<float> w[NC] = {}, e[NC];
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-        load8<RAGGED>(w[k], p.w, lane.at(k), n);
+        fetch8<RAGGED>(w[k], p.w, lane.at(k), n);
         e[k] = branch_factor<RAGGED>(p.w_post, p.scale, p.alpha, lane.at(k), n);
     }
     lds.init();
     if (row < p.M) load(next);
     int turn = 0;
-    walk_rows(next, row - lane.ul.unit, p.M, stride, [&](const Row& o, Row& next) {
+    walk_rows(next, row - lane.ul.unit, p.M, stride, [&](Row& o, Row& next) {
         b.skip(stride);
         r.skip(stride);
         if (row + stride < p.M) load(next);
         const bool valid = row < p.M;
         float x[NC][8], ss[NC], post[NC], rstd[NC];
 #pragma unroll
-        for (int k = 0; k < NC; ++k) post[k] = 1.0f;
+        for (int k = 0; k < NC; ++k) {
+            settle8<RAGGED>(o.b[k], lane.at(k), n);
+            settle8<RAGGED>(o.r[k], lane.at(k), n);
+            post[k] = 1.0f;
+        }
         if (p.w_post) {
 #pragma unroll
             for (int k = 0; k < NC; ++k) {

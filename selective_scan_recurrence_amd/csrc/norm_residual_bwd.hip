@@ -22,7 +22,7 @@ struct BwdP {
 template <typename T, typename R, typename RS, bool BRANCH>
 __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_bwd(BwdP p) {
     constexpr int L = RS::L, NC = RS::NC, NB = BRANCH ? NC : 1, U = units_per_block<L>();
-    constexpr bool RAGGED = RS::RAGGED;
+    constexpr Ends RAGGED = RS::RAGGED;
     __shared__ SumMemory<L, NC, false> lds;
     __shared__ float sm[L ? kRowThreads * 8 : 1];
     const RowLane<RS> lane(1, p.W);
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_bwd(BwdP 
     float dw[NC][8], ds[NB][8];
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-        load8<RAGGED>(w[k], p.w, lane.at(k), n);
+        fetch8<RAGGED>(w[k], p.w, lane.at(k), n);
         e[k] = branch_factor<RAGGED>(p.w_post, p.scale, p.alpha, lane.at(k), n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_bwd(BwdP 
     lds.init();
     if (row < p.M) load(next, row);
     int turn = 0;
-    walk_rows(next, row - lane.ul.unit, p.M, stride, [&](const Row& o, Row& next) {
+    walk_rows(next, row - lane.ul.unit, p.M, stride, [&](Row& o, Row& next) {
         dh.skip(stride);
         r_out.skip(stride);
         dr_out.skip(stride);
@@ -85,10 +85,9 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_bwd(BwdP 
         float x[NC][8], dot[NC], c1[NC];
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            if (p.r8) o.r[k].c.values(x[k]);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] = o.r[k].t[j];
+            settle8<RAGGED>(o.dh[k], lane.at(k), n);
+            settle8<RAGGED>(o.dr[k], lane.at(k), n);
+            o.r[k].template values<RAGGED>(p.r8, x[k], lane.at(k), n);
             dot[k] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -110,10 +109,7 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_bwd(BwdP 
                 x[k][j] = o.rstd * (o.dh[k][j] * w[k][j] - x[k][j] * c1[0]) + o.dr[k][j];
             if (valid && p.d_r) store8<RAGGED>(d_r.p, lane.at(k), n, x[k]);
             if constexpr (BRANCH) {
-                if (p.b8) o.b[k].c.values(v[k]);
-                else
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[k][j] = o.b[k].t[j];
+                o.b[k].template values<RAGGED>(p.b8, v[k], lane.at(k), n);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     v[k][j] *= o.post;
@@ -196,7 +192,7 @@ int norm_bwd_slices(const NormShape& s) {
     int64_t most = 1;
     for_row_shape<true>(s.W, s.G, [&](auto rs, int threads, int units) {
         rows = 2 * units_per_block<decltype(rs)::L>();
-        const int each = 16 * 64 / threads;
+        const int each = (decltype(rs)::L && decltype(rs)::NC > 1 ? 8 : 16) * 64 / threads;
         most = 256 * (int64_t)(each > 0 ? each : 1) / units;
         return 0;
     });

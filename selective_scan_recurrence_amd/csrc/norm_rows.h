@@ -6,13 +6,19 @@
 // holds the 8-value pieces t, t + n, ... of the unit, as 16-byte accesses at
 // the element's own alignment, which gfx950 takes.  A width that is not a
 // multiple of 8 (RAGGED) leaves a last piece of s = width % 8 values: it is
-// loaded as the unit's last 8 values and shifted down in registers, so that
-// no load is divided or waits behind a branch, and stored value by value.
+// loaded as the unit's last 8 values and shifted down in registers when it is
+// used, so that no load is divided or waits behind a branch, and stored value
+// by value.
 #pragma once
 
 #include "ckpt8.h"
 
 namespace ssm {
+
+// Whether a unit is whole pieces, ends in a part of one, or is less than one
+// (its values are then loaded one by one: kept apart, because where the two ways
+// of loading meet in one kernel every load is waited for at once).
+enum Ends { kWhole, kRagged, kTiny };
 
 constexpr int kRowThreads = 256;  // workgroup of the kernels with L > 0
 
@@ -75,14 +81,14 @@ typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 // outputs would not stay for a reader, may store past the caches.
 constexpr int64_t kStreamBytes = int64_t(256) << 20;
 
-// Loads the piece at value `at` of a unit of n values; nothing past its end.
-template <bool RAGGED, typename T>
+// Loads the piece at value `at` of a unit of n values; nothing past its end.  A
+// ragged end is in place only after settle8, which waits for the load.
+template <Ends RAGGED, typename T>
 __device__ __forceinline__ void load8(Piece<T>& r, const T* unit, int at, int n) {
-    if constexpr (!RAGGED) {
+    if constexpr (RAGGED == kWhole) {
         if (at < n) __builtin_memcpy(&r, unit + at, sizeof r);
-    } else if (n >= 8) {
+    } else if constexpr (RAGGED == kRagged) {
         if (at < n) __builtin_memcpy(&r, unit + min(at, n - 8), sizeof r);
-        r.shift(8 - n % 8, at < n && at + 8 > n);
     } else if (at == 0) {
         T v[8];
 #pragma unroll
@@ -90,9 +96,23 @@ __device__ __forceinline__ void load8(Piece<T>& r, const T* unit, int at, int n)
         __builtin_memcpy(&r, v, sizeof r);
     }
 }
+template <Ends RAGGED, typename T>
+__device__ __forceinline__ void settle8(Piece<T>& r, int at, int n) {
+    if constexpr (RAGGED == kRagged) {
+        // only the wave that holds the end has anything to shift
+        const bool end = at < n && at + 8 > n;
+        if (__builtin_amdgcn_ballot_w64(end)) r.shift(8 - n % 8, end);
+    }
+}
+// Both, for what is used at once.
+template <Ends RAGGED, typename T>
+__device__ __forceinline__ void fetch8(Piece<T>& r, const T* unit, int at, int n) {
+    load8<RAGGED>(r, unit, at, n);
+    settle8<RAGGED>(r, at, n);
+}
 
 // STREAM: past the caches
-template <bool RAGGED, bool STREAM = false, typename T>
+template <Ends RAGGED, bool STREAM = false, typename T>
 __device__ __forceinline__ void store8(T* unit, int at, int n, const float v[8]) {
     Piece<T> r;
     r.set(v);
@@ -274,11 +294,18 @@ template <typename T>
 union PieceOr8 {
     Piece<T> t;
     CkptRow::Raw c;
+    template <Ends RAGGED>
+    __device__ __forceinline__ void values(bool kept, float v[8], int at, int n) {
+        if (kept) return c.values(v);
+        settle8<RAGGED>(t, at, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = t[j];
+    }
 };
 
 // Adds the units' column sums of a workgroup and writes them to dst, n columns.
 // sm: kRowThreads * 8 floats for L > 0.
-template <int L, int NC, bool RAGGED>
+template <int L, int NC, Ends RAGGED>
 __device__ __forceinline__ void store_column_sums(float* dst, int n, const float acc[NC][8], float* sm) {
     const UnitLane ul = unit_lane<L>();
 #pragma unroll
@@ -299,17 +326,18 @@ __device__ __forceinline__ void store_column_sums(float* dst, int n, const float
     }
 }
 
-template <int L_, int NC_, bool RAGGED_, bool SEGMENTS_ = false>
+template <int L_, int NC_, Ends RAGGED_, bool SEGMENTS_ = false>
 struct RowShape {
     static constexpr int L = L_, NC = NC_;
-    static constexpr bool RAGGED = RAGGED_, SEGMENTS = SEGMENTS_;
+    static constexpr Ends RAGGED = RAGGED_;
+    static constexpr bool SEGMENTS = SEGMENTS_;
 };
 
 // Host: the smallest unit that holds a group of so many pieces (4, 8, 16, 32 or
 // 64 lanes with one piece each, a wave with two, then a workgroup with 1, 2 or
 // 4 pieces a lane), so that narrow rows share a wave and wide ones keep every
 // lane busy.
-template <bool RAGGED, typename F>
+template <Ends RAGGED, typename F>
 int for_unit_shape(int pieces, F&& f) {
     if (pieces <= 4) return f(RowShape<4, 1, RAGGED>{});
     if (pieces <= 8) return f(RowShape<8, 1, RAGGED>{});
@@ -332,7 +360,7 @@ inline bool row_segments(int W, int G) {
     if (G == 1 || (W / G) % 8 || W / 8 > 1024) return false;
     const int pieces = W / G / 8, row = W / 8;
     int lanes = 0;
-    for_unit_shape<false>(pieces, [&](auto rs) {
+    for_unit_shape<kWhole>(pieces, [&](auto rs) {
         using RS = decltype(rs);
         return lanes = RS::L ? RS::L * RS::NC : row_threads<RS>(pieces) * RS::NC;
     });
@@ -345,10 +373,11 @@ int for_row_shape(int W, int G, F&& f) {
     auto unit = [&](auto rs) { return f(rs, row_threads<decltype(rs)>((Wg + 7) / 8), G); };
     if constexpr (GROUPED)
         if (row_segments(W, G)) {
-            using RS = RowShape<0, 1, false, true>;
+            using RS = RowShape<0, 1, kWhole, true>;
             return f(RS{}, row_threads<RS>(W / 8), 1);
         }
-    return Wg % 8 ? for_unit_shape<true>((Wg + 7) / 8, unit) : for_unit_shape<false>(Wg / 8, unit);
+    if (Wg < 8) return unit(RowShape<4, 1, kTiny>{});
+    return Wg % 8 ? for_unit_shape<kRagged>((Wg + 7) / 8, unit) : for_unit_shape<kWhole>(Wg / 8, unit);
 }
 
 // Slices of a forward, whose workgroups (slice, group) walk the rows: 16 waves
@@ -389,7 +418,7 @@ struct RowLane {
 template <typename Row, typename F>
 __device__ __forceinline__ void walk_rows(Row& next, int64_t first, int64_t M, int64_t stride, F&& step) {
     for (; first < M; first += stride) {
-        const Row present = next;
+        Row present = next;
         step(present, next);
     }
 }
