@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 EPS = 1e-5
 TYPES = [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")]
 SHAPES = [(1, 1, 0), (3, 8, 1), (70, 61, 0), (33, 64, 8), (9, 128, 0), (5, 250, 3), (40, 256, 0),
-          (6, 500, 12), (7, 1000, 5), (5, 1024, 0), (4, 2560, 16), (2, 8190, 0), (2, 9000, 2),
+          (6, 500, 12), (7, 1000, 5), (5, 1024, 0), (9, 768, 0), (11, 523, 1), (4, 2560, 16), (2, 8190, 0), (2, 9000, 2),
           (1, 32768, 0), (2, 16640, 8)]
 
 
