@@ -25,6 +25,12 @@ template <typename T, typename RS, Gate GATE, bool STREAM>
 __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) {
     constexpr int L = RS::L, NC = RS::NC, U = units_per_block<L>();
     constexpr Ends RAGGED = RS::RAGGED;
+    // A workgroup's row with more than one piece a lane (groups past 8192) does
+    // not fit the 128 registers that 1024 lanes leave each: no piece is kept
+    // between the sums nor loaded a row ahead, each is loaded when it is needed,
+    // the second time from the caches.  8192 x 16384 bf16: 1160 us with every
+    // piece held and half of them spilled, 700 us so; 8192 x 12288: 920 and 605.
+    constexpr bool LEAN = L == 0 && NC > 1;
     __shared__ SumMemory<L, NC, RS::SEGMENTS> lds;
     __shared__ float sm[L ? kRowThreads * 8 : 1];
     const RowLane<RS> lane(p.G, p.Wg);
@@ -41,18 +47,28 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) 
     RowPtr<T> d_y(p.d_y, p.ld_y, row, c0), d_z(p.d_z, p.ld_z, row, c0);
     CkptRow y8(p.y8, p.scale_off, p.W32, row, c0), z8(p.z8, p.scale_off, p.W32, row, c0);
     RowPtr<float> rstd(p.rstd, p.G, row, 0);
+    auto load_piece = [&](Row& r, int k) {
+        const int at = lane.at(k);
+        load8<RAGGED>(r.d[k], dout.p, at, n);
+        if (!p.y8) load8<RAGGED>(r.y[k].t, y.p, at, n);
+        else if (at < n) r.y[k].c = y8.load(at);
+        r.rstd[k] = k == 0 || RS::SEGMENTS ? rstd.p[lane.group[k]] : r.rstd[0];
+        if (GATE == kNone) return;
+        if (!p.z8) load8<RAGGED>(r.z[k].t, z.p, at, n);
+        else if (at < n) r.z[k].c = z8.load(at);
+    };
     auto load = [&](Row& r) {
+        if (LEAN) return;
 #pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int at = lane.at(k);
-            load8<RAGGED>(r.d[k], dout.p, at, n);
-            if (!p.y8) load8<RAGGED>(r.y[k].t, y.p, at, n);
-            else if (at < n) r.y[k].c = y8.load(at);
-            r.rstd[k] = k == 0 || RS::SEGMENTS ? rstd.p[lane.group[k]] : r.rstd[0];
-            if (GATE == kNone) continue;
-            if (!p.z8) load8<RAGGED>(r.z[k].t, z.p, at, n);
-            else if (at < n) r.z[k].c = z8.load(at);
-        }
+        for (int k = 0; k < NC; ++k) load_piece(r, k);
+    };
+    auto skip_inputs = [&] {
+        dout.skip(stride);
+        y.skip(stride);
+        z.skip(stride);
+        y8.skip(stride);
+        z8.skip(stride);
+        rstd.skip(stride);
     };
     Row next;
     __builtin_memset(&next, 0, sizeof next);
@@ -60,7 +76,7 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) 
     float dw[NC][8];
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-        fetch8<RAGGED>(w[k], p.w + c0, lane.at(k), n);
+        if (!LEAN) fetch8<RAGGED>(w[k], p.w + c0, lane.at(k), n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
     }
@@ -68,26 +84,33 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) 
     if (row < p.M) load(next);
     int turn = 0;
     walk_rows(next, row - lane.ul.unit, p.M, stride, [&](Row& r, Row& next) {
-        dout.skip(stride);
-        y.skip(stride);
-        z.skip(stride);
-        y8.skip(stride);
-        z8.skip(stride);
-        rstd.skip(stride);
-        if (row + stride < p.M) load(next);
+        if (!LEAN) {
+            skip_inputs();
+            if (row + stride < p.M) load(next);
+        }
         const bool valid = row < p.M;  // else r is an earlier row: it is not counted again
         // x: the normalised value; yv, zv: y and z
         float x[NC][8], yv[NC][8], zv[NC][8], dot[NC], c1[NC];
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
+        auto ready = [&](int k) {
+            if (LEAN) {
+                __builtin_amdgcn_sched_barrier(0);  // one piece at a time
+                load_piece(r, k);
+                fetch8<RAGGED>(w[k], p.w + c0, lane.at(k), n);
+            }
             settle8<RAGGED>(r.d[k], lane.at(k), n);
             r.y[k].template values<RAGGED>(p.y8, yv[k], lane.at(k), n);
             if (GATE != kNone) r.z[k].template values<RAGGED>(p.z8, zv[k], lane.at(k), n);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[k][j] = (GATE == kBefore ? yv[k][j] * silu(zv[k][j]) : yv[k][j]) * r.rstd[k];
+        };
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            ready(k);
             dot[k] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float gate = GATE == kNone ? 1.0f : silu(zv[k][j]);
-                x[k][j] = (GATE == kBefore ? yv[k][j] * gate : yv[k][j]) * r.rstd[k];
+                const float gate = GATE == kAfter ? silu(zv[k][j]) : 1.0f;
                 const float dx = (GATE == kAfter ? r.d[k][j] * gate : r.d[k][j]) * x[k][j];
                 if (valid) dw[k][j] += dx;
                 dot[k] += dx * w[k][j];
@@ -98,6 +121,7 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) 
 #pragma unroll
             for (int k = 0; k < NC; ++k) {
                 float dy[8], dz[8];
+                if (LEAN) ready(k);
                 c1[k] *= p.inv_n;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -118,6 +142,7 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) 
             }
         }
         row += stride;
+        if (LEAN) skip_inputs();
         d_y.skip(stride);
         d_z.skip(stride);
     });
