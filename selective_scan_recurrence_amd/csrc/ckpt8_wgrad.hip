@@ -20,6 +20,16 @@
 //     i: c = 4i + j % 4 + 64 (j / 4)) then meet 8 different 16-byte columns.
 // With few tiles the rows are split over workgroups, each of which leaves an
 // f32 partial in the workspace, and a second kernel adds them in order.
+//
+// Bound by the matrix units, two workgroups a CU: 8192 rows, 4096 x 4096, bf16
+// dy, 242 us = 1136 TFLOP/s when 512 tiles fill the CUs at once (a library product
+// of 8192^3 in bf16 reaches 1251); 8192 rows, 10576 x 2560, 485 - 512 us = 867 -
+// 915 TFLOP/s (840 tiles: a round of 512 and a part of one; a library product of
+// the same sizes with x in bf16 takes 565 us).  Leaving out half of the dy loads
+// there gains 10% (its rows start off the cache lines), the loads of scales or
+// the conversions nothing; narrower tiles that fill the rounds better lose
+// (columns 112: 544 - 579 us, 96: 670), and so do other orders of the loads and
+// the MFMAs.  f32 dy, 4096 rows, 5120 x 2560: 447 us, three MFMAs a product.
 #include <type_traits>
 
 #include "block_internal.h"
