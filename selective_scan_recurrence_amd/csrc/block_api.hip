@@ -53,8 +53,11 @@ int check_residual(const ssm_norm_desc* d, NormShape* out) {
     return out->io == SSM_F32 && out->res == SSM_BF16 ? SSM_ERR_UNSUPPORTED : SSM_OK;
 }
 
+// partial rows of the gated norm's d_w, or of the residual norm's d_w and of its
+// two sums over the branch: the larger, since a descriptor serves both
 size_t norm_bwd_workspace(const NormShape& s) {
-    const size_t n = (size_t)norm_bwd_slices(s) * s.W * 4 * 2;
+    const size_t gated = norm_bwd_slices(s, true), residual = s.G == 1 ? 2 * (size_t)norm_bwd_slices(s, false) : 0;
+    const size_t n = (gated > residual ? gated : residual) * s.W * 4;
     return (n + 255) / 256 * 256;
 }
 

@@ -28,7 +28,7 @@ struct NormShape {
 };
 
 // Row slices of a backward: each is one row of per-column partial sums.
-int norm_bwd_slices(const NormShape& s);
+int norm_bwd_slices(const NormShape& s, bool gated);
 
 struct GatedArgs {
     NormShape s;

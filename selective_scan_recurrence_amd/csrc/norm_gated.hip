@@ -120,7 +120,7 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_fwd(FwdP p) 
 int launch_norm_gated_fwd(const GatedArgs& a, hipStream_t stream) {
     const NormShape& s = a.s;
     if (!s.M) return SSM_OK;
-    return for_row_shape<true>(s.W, s.G, [&](auto rs, int threads, int units) {
+    return for_row_shape<kGatedFwd>(s.M, s.W, s.G, [&](auto rs, int threads, int units) {
         using RS = decltype(rs);
         const int slices = row_slices<RS>(s.M, units, threads);
         FwdP p = {a.y, a.z, a.w, a.out, a.rstd, a.y8, a.z8, a.out8, s.ld_x, s.ld_z, s.ld_out,

@@ -153,11 +153,11 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) 
 
 int launch_norm_gated_bwd(const GatedBwdArgs& a, hipStream_t stream) {
     const NormShape& s = a.s;
-    const int slices = norm_bwd_slices(s);
+    const int slices = norm_bwd_slices(s, true);
     BwdP p = {a.dout, a.y, a.z, const_cast<uint8_t*>(a.y8), const_cast<uint8_t*>(a.z8), a.w, a.rstd,
               a.d_y, a.d_z, a.d_w ? (slices == 1 ? a.d_w : a.part) : nullptr, s.ld_x, s.ld_z,
               s.ld_out, s.M, s.scale_off, s.G, s.W, s.Wg, s.W32, slices, 1.0f / (float)s.Wg};
-    const int rc = for_row_shape<true>(s.W, s.G, [&](auto rs, int threads, int units) {
+    const int rc = for_row_shape<kGatedBwd>(s.M, s.W, s.G, [&](auto rs, int threads, int units) {
         using RS = decltype(rs);
         const unsigned grid = (unsigned)(slices * units);
         for_gate<RS>(s, a.z || a.z8, 5, [&](auto t, auto gate, auto past) {

@@ -141,7 +141,7 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_fwd(FwdP 
 int launch_norm_residual_fwd(const ResidualArgs& a, hipStream_t stream) {
     const NormShape& s = a.s;
     if (!s.M) return SSM_OK;
-    return for_row_shape<false>(s.W, 1, [&](auto rs, int threads, int) {
+    return for_row_shape<kResidual>(s.M, s.W, 1, [&](auto rs, int threads, int) {
         using RS = decltype(rs);
         const int slices = row_slices<RS>(s.M, 1, threads);
         FwdP p = {a.b, a.r, a.w_post, a.scale, a.w, a.r_out, a.h, a.rstd, a.rstd_post, a.r8, a.b8, a.h8, s.ld_x,

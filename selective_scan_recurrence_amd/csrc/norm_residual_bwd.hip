@@ -181,22 +181,31 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sums(SumP p) {
 
 }  // namespace
 
-// A unit of a workgroup takes at least 2 rows, and the workgroups are those of
-// 16 waves on each of 256 compute units, at most 768, so that the partial sums
-// stay few beside the rows.  (1111 x 771 f32, gate after: 8.5, 9.4, 13.5, 21.4
-// us with 1, 2, 4, 8 rows, where the sum of the partial rows grows from 2 to 5
-// us with 1.  At 16384 x 2560, 512 and 768 workgroups are alike, 1024 are 5%
-// slower; at 16384 x 5120 in 8 groups 256, 512 and 768 are alike.)
-int norm_bwd_slices(const NormShape& s) {
+// A unit of a workgroup takes at least 2 rows, and the workgroups are those that
+// 256 compute units hold at a time with 4 waves on each SIMD, where a workgroup
+// of more than 4 waves counts as if it filled its last four; beyond 768 of them
+// only as many as leave 16 rows for each, so that the partial sums stay few
+// beside the rows.  (Gated backward of 65536 rows in bf16, times of a copy's:
+// width 2560, 5 waves, 1.66, 1.08, 1.38 with 1, 2, 3 workgroups on a unit; width
+// 1280, 3 waves, 1.35, 1.13, 1.01, 1.35 with 3 to 6; width 2048, 4 waves, 0.93,
+// 0.88, 1.18 with 3 to 5.  1111 x 771 f32, gate after: 8.5, 9.4, 13.5, 21.4 us
+// with 1, 2, 4, 8 rows, where the sum of the partial rows grows from 2 to 5 us
+// with 1.)
+int norm_bwd_slices(const NormShape& s, bool gated) {
     int rows = 1;
     int64_t most = 1;
-    for_row_shape<true>(s.W, s.G, [&](auto rs, int threads, int units) {
-        rows = 2 * units_per_block<decltype(rs)::L>();
-        const int each = (decltype(rs)::L && decltype(rs)::NC > 1 ? 8 : 16) * 64 / threads;
-        most = 256 * (int64_t)(each > 0 ? each : 1) / units;
+    auto count = [&](auto rs, int threads, int units) {
+        using RS = decltype(rs);
+        rows = 2 * units_per_block<RS::L>();
+        const int waves = threads / 64, simds = (waves + 3) / 4;
+        const int each = RS::L && RS::NC > 1 ? 2 : waves <= 4 ? 16 / waves : 4 / simds;
+        most = 256 * each / units;
         return 0;
-    });
-    most = most < 1 ? 1 : most > 768 ? 768 : most;
+    };
+    if (gated) for_row_shape<kGatedBwd>(s.M, s.W, s.G, count);
+    else for_row_shape<kResidual>(s.M, s.W, 1, count);
+    const int64_t cap = s.M / 16 > 768 ? s.M / 16 : 768;
+    most = most < 1 ? 1 : most > cap ? cap : most;
     const int64_t want = (s.M + rows - 1) / rows;
     return (int)(want < 1 ? 1 : want < most ? want : most);
 }
@@ -210,7 +219,7 @@ int launch_column_sums(const float* part, int S, int W, const ColumnSums& out, h
 
 int launch_norm_residual_bwd(const ResidualBwdArgs& a, hipStream_t stream) {
     const NormShape& s = a.s;
-    const int slices = norm_bwd_slices(s);
+    const int slices = norm_bwd_slices(s, false);
     const bool branch = a.w_post || a.d_scale, sums = a.d_w_post || a.d_scale;
     const bool direct = slices == 1 && !sums;  // d_w is the one partial row
     float* part_w = direct ? a.d_w : a.d_w || sums ? a.part : nullptr;
@@ -218,7 +227,7 @@ int launch_norm_residual_bwd(const ResidualBwdArgs& a, hipStream_t stream) {
               a.scale, a.w, a.rstd, a.rstd_post, a.d_r, a.d_b, part_w,
               sums ? a.part + (int64_t)slices * s.W : nullptr, s.ld_x, s.ld_res, s.ld_out, s.M, s.scale_off, s.W,
               s.W32, slices, 1.0f / (float)s.W, s.alpha};
-    const int rc = for_row_shape<false>(s.W, 1, [&](auto rs, int threads, int) {
+    const int rc = for_row_shape<kResidual>(s.M, s.W, 1, [&](auto rs, int threads, int) {
         using RS = decltype(rs);
         for_types(s, [&](auto t, auto r) {
             using T = decltype(t);

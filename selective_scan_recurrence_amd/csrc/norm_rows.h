@@ -333,23 +333,31 @@ struct RowShape {
     static constexpr bool SEGMENTS = SEGMENTS_;
 };
 
+// The kernels that ask for a shape: 65 to 128 pieces suit them differently.
+enum RowUse { kGatedFwd, kGatedBwd, kResidual };
+
 // Host: the smallest unit that holds a group of so many pieces (4, 8, 16, 32 or
 // 64 lanes with one piece each, a wave with two, then a workgroup with 1, 2 or
 // 4 pieces a lane), so that narrow rows share a wave and wide ones keep every
-// lane busy.  THREE: up to 96 pieces take 32 lanes with three each, where a wave
-// with two leaves up to half its lanes idle.  (131072 x 640 bf16, residual norm:
-// forward 1.04 -> 0.95 times a copy's time, backward 1.13 -> 0.97; the gated
-// norm's backward, which then holds 300 registers, 1.65 -> 2.15.)
-template <Ends RAGGED, bool THREE = false, typename F>
-int for_unit_shape(int pieces, F&& f) {
+// lane busy.  Where a wave with two pieces would leave up to half its lanes idle:
+//  - the residual norm gives up to 96 pieces to 32 lanes with three each (131072
+//    x 640 bf16: forward 1.04 -> 0.95 times a copy's time, backward 1.13 -> 0.97;
+//    the gated backward would hold 300 registers and go from 1.65 to 2.15);
+//  - the gated backward, short of registers with two pieces, gives them to a
+//    workgroup of two waves when there are many rows (131072 x 640 1.63 -> 1.19,
+//    x 1024 1.18 -> 0.95, 32768 x 768 1.52 -> 1.22; 16384 x 768 would go from
+//    1.28 to 1.45, the gated forward at 150000 x 523 from 1.16 to 1.43).
+template <Ends RAGGED, RowUse USE, typename F>
+int for_unit_shape(int pieces, bool many, F&& f) {
     if (pieces <= 4) return f(RowShape<4, 1, RAGGED>{});
     if (pieces <= 8) return f(RowShape<8, 1, RAGGED>{});
     if (pieces <= 16) return f(RowShape<16, 1, RAGGED>{});
     if (pieces <= 32) return f(RowShape<32, 1, RAGGED>{});
     if (pieces <= 64) return f(RowShape<64, 1, RAGGED>{});
-    if constexpr (THREE)
+    if constexpr (USE == kResidual)
         if (pieces <= 96) return f(RowShape<32, 3, RAGGED>{});
-    if (pieces <= 128) return f(RowShape<64, 2, RAGGED>{});
+    if (USE != kGatedBwd || !many)
+        if (pieces <= 128) return f(RowShape<64, 2, RAGGED>{});
     if (pieces <= 1024) return f(RowShape<0, 1, RAGGED>{});
     if (pieces <= 2048) return f(RowShape<0, 2, RAGGED>{});
     return f(RowShape<0, 4, RAGGED>{});
@@ -365,25 +373,26 @@ inline bool row_segments(int W, int G) {
     if (G == 1 || (W / G) % 8 || W / 8 > 1024) return false;
     const int pieces = W / G / 8, row = W / 8;
     int lanes = 0;
-    for_unit_shape<kWhole>(pieces, [&](auto rs) {
+    for_unit_shape<kWhole, kGatedFwd>(pieces, false, [&](auto rs) {
         using RS = decltype(rs);
         return lanes = RS::L ? RS::L * RS::NC : row_threads<RS>(pieces) * RS::NC;
     });
     return (double)row / ((row + 63) / 64 * 64) > 1.125 * pieces / lanes;
 }
 // Calls f(RowShape, threads, groups that are units of their own) for a norm.
-template <bool GROUPED, typename F>
-int for_row_shape(int W, int G, F&& f) {
+template <RowUse USE, typename F>
+int for_row_shape(int64_t M, int W, int G, F&& f) {
     const int Wg = W / G;
+    const bool many = M >= 32768;
     auto unit = [&](auto rs) { return f(rs, row_threads<decltype(rs)>((Wg + 7) / 8), G); };
-    if constexpr (GROUPED)
+    if constexpr (USE != kResidual)
         if (row_segments(W, G)) {
             using RS = RowShape<0, 1, kWhole, true>;
             return f(RS{}, row_threads<RS>(W / 8), 1);
         }
     if (Wg < 8) return unit(RowShape<4, 1, kTiny>{});
-    return Wg % 8 ? for_unit_shape<kRagged, !GROUPED>((Wg + 7) / 8, unit)
-                  : for_unit_shape<kWhole, !GROUPED>(Wg / 8, unit);
+    return Wg % 8 ? for_unit_shape<kRagged, USE>((Wg + 7) / 8, many, unit)
+                  : for_unit_shape<kWhole, USE>(Wg / 8, many, unit);
 }
 
 // Slices of a forward, whose workgroups (slice, group) walk the rows: 16 waves

@@ -75,6 +75,27 @@ def test_many_groups(rows, width, groups, io):
     R.check("d_w", g.d_w, *want["d_w"], "f32", R.COUNT_SUM)
 
 
+@pytest.mark.parametrize("rows,width,groups,after,io", [(32768, 523, 1, False, "bf16"), (33001, 640, 1, True, "bf16"),
+                                                        (32771, 1042, 2, False, "bf16"), (32769, 1024, 1, False, "f32"),
+                                                        (32767, 768, 1, False, "bf16")])
+def test_many_rows_of_middling_width(rows, width, groups, after, io):
+    """Groups of 520 to 1024 columns in both forms, of few rows and of many.  A
+    sum over the rows adds at most 17 of them in a lane, then up to 64 partial
+    rows in each of 32 lanes, and those."""
+    dt = R.DTYPES[io]
+    y, z, w, zd = _inputs(rows, width, 0, io, seed=width)
+    d = ops.norm_desc(n_rows=rows, width=width, n_group=groups, io=io, eps=EPS, gate_after=after)
+    rstd = torch.empty(rows, groups, device="cuda")
+    ops.norm_gated_fwd(d, y.cuda(), zd, w.cuda(), rstd=rstd)
+    _, inv = R.gated_fwd(y.double(), z.double(), w.double(), groups, EPS, after)
+    dout = R.draw(width + 9, rows, width).to(dt)
+    g = ops.norm_gated_bwd(d, dout.cuda(), w.cuda(), rstd, y=y.cuda(), z=zd)
+    want = R.gated_bwd(dout.double(), y.double(), z.double(), w.double(), inv, groups, after)
+    R.check("d_y", g.d_y, *want["d_y"], io)
+    R.check("d_z", g.d_z, *want["d_z"], io)
+    R.check("d_w", g.d_w, *want["d_w"], "f32", R.COUNT + 17 + 64 + 32)
+
+
 @pytest.mark.parametrize("after", [False, True])
 @pytest.mark.parametrize("rows,width,groups", [(12000, 5120, 8), (24000, 2048, 1), (400000, 128, 1)])
 def test_matrices_past_the_cache(rows, width, groups, after):
