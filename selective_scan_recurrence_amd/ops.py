@@ -205,12 +205,14 @@ def _refuse(status, where, name, t):
 
 
 def _matrix(where, name, t, rows, width, ld, dtype):
-    """t is None or [rows][width] in dtype with row stride ld."""
+    """t is None or [rows][width] in dtype with row stride ld (0: width, as the
+    library takes it).  Rows that share or overlap have no such stride."""
     if t is None:
         return
     if t.dtype is not dtype:
         _refuse(B.SSM_ERR_DTYPE, where, name, t)
-    if t.shape != (rows, width) or (rows > 1 and t.stride(0) != ld) or \
+    ld = ld or width
+    if t.shape != (rows, width) or (rows > 1 and (t.stride(0) != ld or ld < width)) or \
             (width > 1 and rows > 0 and t.stride(1) != 1):
         _refuse(B.SSM_ERR_SHAPE, where, name, t)
     if not t.is_cuda:
@@ -241,7 +243,7 @@ def _empty(shape, dtype, device, stream):
 
 
 def _matrix_like(rows, width, ld, dtype, device, stream):
-    if ld == width or rows < 2:
+    if ld in (0, width) or rows < 2:
         return _empty((rows, width), dtype, device, stream)
     return _empty((rows, ld), dtype, device, stream)[:, :width]
 
@@ -282,11 +284,14 @@ def ckpt8_unpack(ckpt: torch.Tensor, n_rows, width, io="bf16", out=None, stream=
     """The values an 8-bit checkpoint holds, [n_rows][width] in out's type (io
     without out)."""
     where = "ckpt8_unpack"
-    _dense(where, "ckpt", ckpt, ckpt8_bytes(n_rows, width), torch.uint8)
     if out is None:
+        _dense(where, "ckpt", ckpt, ckpt8_bytes(n_rows, width), torch.uint8)
         out = _empty((n_rows, width), TORCH_IO[IO_DTYPES[io]], ckpt.device, stream)
-    ld = out.stride(0) if n_rows > 1 else width
-    _matrix(where, "out", out, n_rows, width, ld, out.dtype)
+        ld = width
+    else:
+        ld = out.stride(0) if n_rows > 1 else width
+        _matrix(where, "out", out, n_rows, width, ld, out.dtype)
+        _dense(where, "ckpt", ckpt, ckpt8_bytes(n_rows, width), torch.uint8)
     B.ssm_ckpt8_unpack(ckpt, out, ld, n_rows, width, _io_of(out, where), stream)
     return out
 
