@@ -34,6 +34,7 @@
 
 #include "block_internal.h"
 #include "norm_rows.h"
+#include "row_split.h"
 
 namespace ssm {
 namespace {
@@ -42,8 +43,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-constexpr int kTO = 256, kTC = 128, kTM = 64;
 
 struct WgradP {
     const void* dy;
@@ -131,7 +130,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void wgrad_tile(WgradP
     const uint32_t id = xcd * per + min(xcd, extra) + pid / 8;
     const int split = id / p.tiles, tile = id % p.tiles;
     const int o0 = tile / p.tiles_c * kTO + 64 * wave, c0 = tile % p.tiles_c * kTC;
-    const int m_begin = split * p.rows, m_end = min(p.M, m_begin + p.rows);
+    const int m_begin = split * p.rows, m_end = part_end(p.M, p.rows, split);
 
     // dy: columns past O are never stored, so a lane past the end takes the
     // last four.  A step's rows past the end (LAST) are loaded from the last
@@ -326,43 +325,16 @@ __global__ __launch_bounds__(256) void wgrad_join(const float* __restrict__ part
     if (e < n) dw[e] = accumulate ? dw[e] + v : v;
 }
 
-struct Split {
-    int count, rows;
-};
-// Parts of the rows, each of at least a step: the count with the least
-// modelled time.  A step takes 1.25 us with one workgroup on a compute unit
-// and 2.0 with two (bf16), 3.9 with the one that f32 has room for; the join
-// costs a launch and moves each partial twice at 5 TB/s.  (8192 x 1024 x 512
-// in bf16, 16 tiles: 36 us with the 32 parts that fill the chip, 24 with 10.)
-Split split_rows(int64_t M, int64_t W, int64_t O, int dtype) {
-    const int64_t tiles = ((W + kTC - 1) / kTC) * ((O + kTO - 1) / kTO), steps = (M + kTM - 1) / kTM;
-    Split best{1, (int)((steps ? steps : 1) * kTM)};
-    double best_us = 0;
-    for (int64_t n = 1, next; n == 1 || (n <= steps && n * tiles <= 512); n = next) {
-        const int64_t each = steps ? (steps + n - 1) / n : 1, count = steps ? (steps + each - 1) / each : 1;
-        const int64_t wgs = tiles * count, left = wgs % 512;
-        const double step_us = dtype == SSM_BF16 ? (double)(wgs / 512) * 2.0 + (left == 0 ? 0.0 : left <= 256 ? 1.25 : 2.0)
-                                                 : (double)((wgs + 255) / 256) * 3.9;
-        const double us = step_us * (double)each + (count > 1 ? 4.0 + (double)count * W * O * 8.0 / 5e6 : 0.0);
-        if (n == 1 || us < best_us) {
-            best = Split{(int)count, (int)(each * kTM)};
-            best_us = us;
-        }
-        next = each > 1 ? (steps + each - 2) / (each - 1) : n + steps + 1;  // the next count with fewer steps each
-    }
-    return best;
-}
-
 }  // namespace
 
 size_t ckpt8_wgrad_workspace_bytes(int64_t M, int64_t W, int64_t O, int dtype) {
-    const Split s = split_rows(M, W, O, dtype);
+    const RowSplit s = split_rows(M, W, O, dtype);
     return s.count > 1 ? (size_t)s.count * W * O * 4 : 0;
 }
 
 int launch_ckpt8_wgrad(const void* dy, int64_t ld, const uint8_t* x8, float* dw, int64_t M, int64_t W,
                        int64_t O, int dtype, bool accumulate, void* ws, hipStream_t stream) {
-    const Split s = split_rows(M, W, O, dtype);
+    const RowSplit s = split_rows(M, W, O, dtype);
     const int64_t W32 = ckpt8_width(W);
     const int tiles_c = (int)((W + kTC - 1) / kTC);
     const int64_t tiles = tiles_c * ((O + kTO - 1) / kTO);
