@@ -196,7 +196,9 @@ def state_update(desc, s, x, dt, A, Bm, Cm, D, ids, *, dt_bias=None, z=None, con
 # These take [n_rows][width] tensors whose last axis is contiguous; the row
 # stride may be larger (a slice of the projection's output).  What the C ABI
 # cannot see of a tensor -- its shape, strides, type and device -- is checked
-# here, with the ABI's status codes.
+# here, with the ABI's status codes.  A call launches on its stream's device,
+# without a stream (or with one given by its address) on the current one, and
+# every tensor has to be there.
 
 
 def _refuse(status, where, name, t):
@@ -204,30 +206,58 @@ def _refuse(status, where, name, t):
                              f"strides {t.stride()}")
 
 
-def _matrix(where, name, t, rows, width, ld, dtype):
+_current_device = None
+
+
+def _find_current_device():
+    """A function that gives the current GPU's index, -2 (which no tensor has)
+    where there is none.  torch's own raw getter takes 0.1 us."""
+    if not torch.cuda.is_available():
+        return lambda: -2
+    return getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _device_of(stream):
+    """Index of the GPU that a call on this stream launches on."""
+    if stream is not None:
+        index = getattr(stream, "device_index", None)
+        if index is not None:
+            return index
+    global _current_device
+    if _current_device is None:
+        _current_device = _find_current_device()
+    return _current_device()
+
+
+def _matrix(where, name, t, rows, width, ld, dtype, dev=None):
     """t is None or [rows][width] in dtype with row stride ld (0: width, as the
-    library takes it).  Rows that share or overlap have no such stride."""
+    library takes it) on GPU dev.  Rows that share or overlap have no such
+    stride."""
     if t is None:
         return
     if t.dtype is not dtype:
         _refuse(B.SSM_ERR_DTYPE, where, name, t)
     ld = ld or width
-    if t.shape != (rows, width) or (rows > 1 and (t.stride(0) != ld or ld < width)) or \
-            (width > 1 and rows > 0 and t.stride(1) != 1):
+    if t.shape != (rows, width):
         _refuse(B.SSM_ERR_SHAPE, where, name, t)
-    if not t.is_cuda:
+    if t.stride() != (ld, 1) or ld < width:
+        # neither one row's stride nor one column's matters
+        if (rows > 1 and (t.stride(0) != ld or ld < width)) or \
+                (width > 1 and rows > 0 and t.stride(1) != 1):
+            _refuse(B.SSM_ERR_SHAPE, where, name, t)
+    if t.get_device() != (_device_of(None) if dev is None else dev):
         _refuse(B.SSM_ERR_UNSUPPORTED, where, name, t)
 
 
-def _dense(where, name, t, numel, dtype):
-    """t is None or a contiguous tensor of at least numel elements."""
+def _dense(where, name, t, numel, dtype, dev=None):
+    """t is None or a contiguous tensor of at least numel elements on GPU dev."""
     if t is None:
         return
     if t.dtype is not dtype:
         _refuse(B.SSM_ERR_DTYPE, where, name, t)
     if t.numel() < numel or not t.is_contiguous():
         _refuse(B.SSM_ERR_SHAPE, where, name, t)
-    if not t.is_cuda:
+    if t.get_device() != (_device_of(None) if dev is None else dev):
         _refuse(B.SSM_ERR_UNSUPPORTED, where, name, t)
 
 
@@ -269,13 +299,13 @@ def ckpt8_empty(n_rows, width, device="cuda", stream=None) -> torch.Tensor:
 
 def ckpt8_pack(x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """The 8-bit checkpoint of x [n_rows][width] (f32 or bf16)."""
-    where = "ckpt8_pack"
+    where, dev = "ckpt8_pack", _device_of(stream)
     io, (rows, width) = _io_of(x, where), x.shape
     ld = x.stride(0) if rows > 1 else width
-    _matrix(where, "x", x, rows, width, ld, x.dtype)
+    _matrix(where, "x", x, rows, width, ld, x.dtype, dev)
     if out is None:
         out = ckpt8_empty(rows, width, x.device, stream)
-    _dense(where, "out", out, ckpt8_bytes(rows, width), torch.uint8)
+    _dense(where, "out", out, ckpt8_bytes(rows, width), torch.uint8, dev)
     B.ssm_ckpt8_pack(x, ld, rows, width, io, out, stream)
     return out
 
@@ -283,15 +313,15 @@ def ckpt8_pack(x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
 def ckpt8_unpack(ckpt: torch.Tensor, n_rows, width, io="bf16", out=None, stream=None) -> torch.Tensor:
     """The values an 8-bit checkpoint holds, [n_rows][width] in out's type (io
     without out)."""
-    where = "ckpt8_unpack"
+    where, dev = "ckpt8_unpack", _device_of(stream)
     if out is None:
-        _dense(where, "ckpt", ckpt, ckpt8_bytes(n_rows, width), torch.uint8)
+        _dense(where, "ckpt", ckpt, ckpt8_bytes(n_rows, width), torch.uint8, dev)
         out = _empty((n_rows, width), TORCH_IO[IO_DTYPES[io]], ckpt.device, stream)
         ld = width
     else:
         ld = out.stride(0) if n_rows > 1 else width
-        _matrix(where, "out", out, n_rows, width, ld, out.dtype)
-        _dense(where, "ckpt", ckpt, ckpt8_bytes(n_rows, width), torch.uint8)
+        _matrix(where, "out", out, n_rows, width, ld, out.dtype, dev)
+        _dense(where, "ckpt", ckpt, ckpt8_bytes(n_rows, width), torch.uint8, dev)
     B.ssm_ckpt8_unpack(ckpt, out, ld, n_rows, width, _io_of(out, where), stream)
     return out
 
@@ -306,19 +336,21 @@ def ckpt8_wgrad(dy: torch.Tensor, ckpt: torch.Tensor, width, *, dw=None, accumul
     """Weight gradient dw [n_out][width] (f32) of out = x W^T from dy
     [n_rows][n_out] and the 8-bit checkpoint of x [n_rows][width]; added to dw
     with accumulate."""
-    where = "ckpt8_wgrad"
+    where, dev = "ckpt8_wgrad", _device_of(stream)
     io, (rows, n_out) = _io_of(dy, where), dy.shape
     ld = dy.stride(0) if rows > 1 else n_out
-    _matrix(where, "dy", dy, rows, n_out, ld, dy.dtype)
-    _dense(where, "ckpt", ckpt, ckpt8_bytes(rows, width), torch.uint8)
+    _matrix(where, "dy", dy, rows, n_out, ld, dy.dtype, dev)
+    _dense(where, "ckpt", ckpt, ckpt8_bytes(rows, width), torch.uint8, dev)
     if dw is None:
         if accumulate:
             raise B.SsmError(B.SSM_ERR_NULL, f"{where}: accumulate without dw")
         dw = _empty((n_out, width), torch.float32, dy.device, stream)
-    _dense(where, "dw", dw, n_out * width, torch.float32)
+    _dense(where, "dw", dw, n_out * width, torch.float32, dev)
     if ws is None:
         n = B.ssm_ckpt8_wgrad_workspace_bytes(rows, width, n_out, io)
         ws = _empty((n,), torch.uint8, dy.device, stream)
+    else:
+        _dense(where, "ws", ws, 0, ws.dtype, dev)
     B.ssm_ckpt8_wgrad(dy, ld, ckpt, dw, rows, width, n_out, io, bool(accumulate), ws,
                       ws.numel(), stream)
     return dw
@@ -360,24 +392,25 @@ def norm_gated_fwd(desc, y, z, w, *, train=False, out=None, rstd=None, y8=None, 
     the backward needs, rstd and the 8-bit checkpoints y8 and z8, in new
     tensors where none is given."""
     where, M, W, io = "norm_gated_fwd", desc.n_rows, desc.width, TORCH_IO[desc.io_dtype]
-    _matrix(where, "y", y, M, W, desc.ld_x, io)
-    _matrix(where, "z", z, M, W, desc.ld_z, io)
-    _dense(where, "w", w, W, torch.float32)
+    dev = _device_of(stream)
+    _matrix(where, "y", y, M, W, desc.ld_x, io, dev)
+    _matrix(where, "z", z, M, W, desc.ld_z, io, dev)
+    _dense(where, "w", w, W, torch.float32, dev)
     if out is None:
         out = _matrix_like(M, W, desc.ld_out, io, y.device, stream)
     else:
-        _matrix(where, "out", out, M, W, desc.ld_out, io)
+        _matrix(where, "out", out, M, W, desc.ld_out, io, dev)
     if train:
         rstd = _empty((M, desc.n_group), torch.float32, y.device, stream) if rstd is None else rstd
         y8 = ckpt8_empty(M, W, y.device, stream) if y8 is None else y8
         if z is not None:
             z8 = ckpt8_empty(M, W, y.device, stream) if z8 is None else z8
-    _dense(where, "rstd", rstd, M * desc.n_group, torch.float32)
+    _dense(where, "rstd", rstd, M * desc.n_group, torch.float32, dev)
     if y8 is not None or z8 is not None or out8 is not None:
         n = ckpt8_bytes(M, W)
-        _dense(where, "y8", y8, n, torch.uint8)
-        _dense(where, "z8", z8, n, torch.uint8)
-        _dense(where, "out8", out8, n, torch.uint8)
+        _dense(where, "y8", y8, n, torch.uint8, dev)
+        _dense(where, "z8", z8, n, torch.uint8, dev)
+        _dense(where, "out8", out8, n, torch.uint8, dev)
     B.ssm_norm_gated_fwd(desc, y, z, w, out, rstd, y8, z8, out8, stream)
     return NormGatedResult(out, rstd, y8, z8, out8)
 
@@ -393,29 +426,32 @@ def norm_gated_bwd(desc, dout, w, rstd, *, y=None, z=None, y8=None, z8=None, d_y
                    d_w=None, ws=None, stream=None) -> NormGatedGrad:
     """Backward of ``norm_gated_fwd`` from y and z or their 8-bit checkpoints."""
     where, M, W, io = "norm_gated_bwd", desc.n_rows, desc.width, TORCH_IO[desc.io_dtype]
-    _matrix(where, "dout", dout, M, W, desc.ld_out, io)
-    _matrix(where, "y", y, M, W, desc.ld_x, io)
-    _matrix(where, "z", z, M, W, desc.ld_z, io)
-    _dense(where, "w", w, W, torch.float32)
-    _dense(where, "rstd", rstd, M * desc.n_group, torch.float32)
+    dev = _device_of(stream)
+    _matrix(where, "dout", dout, M, W, desc.ld_out, io, dev)
+    _matrix(where, "y", y, M, W, desc.ld_x, io, dev)
+    _matrix(where, "z", z, M, W, desc.ld_z, io, dev)
+    _dense(where, "w", w, W, torch.float32, dev)
+    _dense(where, "rstd", rstd, M * desc.n_group, torch.float32, dev)
     if y8 is not None or z8 is not None:
         n = ckpt8_bytes(M, W)
-        _dense(where, "y8", y8, n, torch.uint8)
-        _dense(where, "z8", z8, n, torch.uint8)
+        _dense(where, "y8", y8, n, torch.uint8, dev)
+        _dense(where, "z8", z8, n, torch.uint8, dev)
     if d_y is None:
         d_y = _matrix_like(M, W, desc.ld_x, io, dout.device, stream)
     else:
-        _matrix(where, "d_y", d_y, M, W, desc.ld_x, io)
+        _matrix(where, "d_y", d_y, M, W, desc.ld_x, io, dev)
     if d_z is not None:
-        _matrix(where, "d_z", d_z, M, W, desc.ld_z, io)
+        _matrix(where, "d_z", d_z, M, W, desc.ld_z, io, dev)
     elif z is not None or z8 is not None:
         d_z = _matrix_like(M, W, desc.ld_z, io, dout.device, stream)
     if d_w is None:
         d_w = _empty((W,), torch.float32, dout.device, stream)
     else:
-        _dense(where, "d_w", d_w, W, torch.float32)
+        _dense(where, "d_w", d_w, W, torch.float32, dev)
     if ws is None:
         ws = norm_bwd_workspace(desc, dout.device, stream)
+    else:
+        _dense(where, "ws", ws, 0, ws.dtype, dev)
     B.ssm_norm_gated_bwd(desc, dout, y, z, y8, z8, w, rstd, d_y, d_z, d_w, ws, ws.numel(), stream)
     return NormGatedGrad(d_y, d_z, d_w)
 
@@ -440,20 +476,21 @@ def norm_residual_fwd(desc, b, r, w, *, w_post=None, scale=None, train=False, r_
     and (with w_post or scale) b8, and h8 for the next projection's weight
     gradient, in new tensors where none is given.  r_out may be r."""
     where, M, W = "norm_residual_fwd", desc.n_rows, desc.width
+    dev = _device_of(stream)
     io, res = TORCH_IO[desc.io_dtype], TORCH_IO[desc.res_dtype]
-    _matrix(where, "b", b, M, W, desc.ld_x, io)
-    _matrix(where, "r", r, M, W, desc.ld_res, res)
-    _dense(where, "w", w, W, torch.float32)
-    _dense(where, "w_post", w_post, W, torch.float32)
-    _dense(where, "scale", scale, W, torch.float32)
+    _matrix(where, "b", b, M, W, desc.ld_x, io, dev)
+    _matrix(where, "r", r, M, W, desc.ld_res, res, dev)
+    _dense(where, "w", w, W, torch.float32, dev)
+    _dense(where, "w_post", w_post, W, torch.float32, dev)
+    _dense(where, "scale", scale, W, torch.float32, dev)
     if r_out is None:
         r_out = _matrix_like(M, W, desc.ld_res, res, w.device, stream)
     else:
-        _matrix(where, "r_out", r_out, M, W, desc.ld_res, res)
+        _matrix(where, "r_out", r_out, M, W, desc.ld_res, res, dev)
     if h is None:
         h = _matrix_like(M, W, desc.ld_out, io, w.device, stream)
     else:
-        _matrix(where, "h", h, M, W, desc.ld_out, io)
+        _matrix(where, "h", h, M, W, desc.ld_out, io, dev)
     if train:
         rstd = _empty((M,), torch.float32, w.device, stream) if rstd is None else rstd
         if w_post is not None and rstd_post is None:
@@ -462,13 +499,13 @@ def norm_residual_fwd(desc, b, r, w, *, w_post=None, scale=None, train=False, r_
         h8 = ckpt8_empty(M, W, w.device, stream) if h8 is None else h8
         if (w_post is not None or scale is not None) and b8 is None:
             b8 = ckpt8_empty(M, W, w.device, stream)
-    _dense(where, "rstd", rstd, M, torch.float32)
-    _dense(where, "rstd_post", rstd_post, M, torch.float32)
+    _dense(where, "rstd", rstd, M, torch.float32, dev)
+    _dense(where, "rstd_post", rstd_post, M, torch.float32, dev)
     if r8 is not None or b8 is not None or h8 is not None:
         n = ckpt8_bytes(M, W)
-        _dense(where, "r8", r8, n, torch.uint8)
-        _dense(where, "b8", b8, n, torch.uint8)
-        _dense(where, "h8", h8, n, torch.uint8)
+        _dense(where, "r8", r8, n, torch.uint8, dev)
+        _dense(where, "b8", b8, n, torch.uint8, dev)
+        _dense(where, "h8", h8, n, torch.uint8, dev)
     B.ssm_norm_residual_fwd(desc, b, r, w_post, scale, w, r_out, h, rstd, rstd_post, r8, b8, h8,
                             stream)
     return NormResidualResult(r_out, h, rstd, rstd_post, r8, b8, h8)
@@ -489,39 +526,42 @@ def norm_residual_bwd(desc, dh, w, rstd, *, dr_out=None, r_out=None, r8=None, b=
     """Backward of ``norm_residual_fwd`` from r_out or its 8-bit checkpoint
     (and b or its, with w_post or scale).  d_r may be dr_out."""
     where, M, W = "norm_residual_bwd", desc.n_rows, desc.width
+    dev = _device_of(stream)
     io, res = TORCH_IO[desc.io_dtype], TORCH_IO[desc.res_dtype]
-    _matrix(where, "dh", dh, M, W, desc.ld_out, io)
-    _matrix(where, "dr_out", dr_out, M, W, desc.ld_res, res)
-    _matrix(where, "r_out", r_out, M, W, desc.ld_res, res)
-    _matrix(where, "b", b, M, W, desc.ld_x, io)
-    _dense(where, "w", w, W, torch.float32)
-    _dense(where, "w_post", w_post, W, torch.float32)
-    _dense(where, "scale", scale, W, torch.float32)
-    _dense(where, "rstd", rstd, M, torch.float32)
-    _dense(where, "rstd_post", rstd_post, M, torch.float32)
+    _matrix(where, "dh", dh, M, W, desc.ld_out, io, dev)
+    _matrix(where, "dr_out", dr_out, M, W, desc.ld_res, res, dev)
+    _matrix(where, "r_out", r_out, M, W, desc.ld_res, res, dev)
+    _matrix(where, "b", b, M, W, desc.ld_x, io, dev)
+    _dense(where, "w", w, W, torch.float32, dev)
+    _dense(where, "w_post", w_post, W, torch.float32, dev)
+    _dense(where, "scale", scale, W, torch.float32, dev)
+    _dense(where, "rstd", rstd, M, torch.float32, dev)
+    _dense(where, "rstd_post", rstd_post, M, torch.float32, dev)
     if r8 is not None or b8 is not None:
         n = ckpt8_bytes(M, W)
-        _dense(where, "r8", r8, n, torch.uint8)
-        _dense(where, "b8", b8, n, torch.uint8)
+        _dense(where, "r8", r8, n, torch.uint8, dev)
+        _dense(where, "b8", b8, n, torch.uint8, dev)
     if d_r is None:
         d_r = _matrix_like(M, W, desc.ld_res, res, dh.device, stream)
     else:
-        _matrix(where, "d_r", d_r, M, W, desc.ld_res, res)
+        _matrix(where, "d_r", d_r, M, W, desc.ld_res, res, dev)
     if d_b is None:
         d_b = _matrix_like(M, W, desc.ld_x, io, dh.device, stream)
     else:
-        _matrix(where, "d_b", d_b, M, W, desc.ld_x, io)
+        _matrix(where, "d_b", d_b, M, W, desc.ld_x, io, dev)
     if d_w is None:
         d_w = _empty((W,), torch.float32, dh.device, stream)
     if w_post is not None and d_w_post is None:
         d_w_post = _empty((W,), torch.float32, dh.device, stream)
     if scale is not None and d_scale is None:
         d_scale = _empty((W,), torch.float32, dh.device, stream)
-    _dense(where, "d_w", d_w, W, torch.float32)
-    _dense(where, "d_w_post", d_w_post, W, torch.float32)
-    _dense(where, "d_scale", d_scale, W, torch.float32)
+    _dense(where, "d_w", d_w, W, torch.float32, dev)
+    _dense(where, "d_w_post", d_w_post, W, torch.float32, dev)
+    _dense(where, "d_scale", d_scale, W, torch.float32, dev)
     if ws is None:
         ws = norm_bwd_workspace(desc, dh.device, stream)
+    else:
+        _dense(where, "ws", ws, 0, ws.dtype, dev)
     B.ssm_norm_residual_bwd(desc, dh, dr_out, r_out, r8, b, b8, w_post, scale, w, rstd, rstd_post,
                             d_r, d_b, d_w, d_w_post, d_scale, ws, ws.numel(), stream)
     return NormResidualGrad(d_r, d_b, d_w, d_w_post, d_scale)

@@ -48,3 +48,18 @@ def test_descriptor_without_strides():
         runs.append([f.out, g.d_y, g.d_z, g.d_w, n.r_out, n.h, m.d_r, m.d_b, m.d_w])
     for a, b in zip(*runs):
         assert a.shape[-1] == width and torch.equal(a, b)
+
+
+def test_workspace_in_host_memory():
+    """A workspace that the GPU could not write is refused before the launch."""
+    rows, width = 300, 96
+    y, w = R.draw(1, rows, width).bfloat16().cuda(), torch.ones(width, device="cuda")
+    d = ops.norm_desc(n_rows=rows, width=width)
+    f = ops.norm_gated_fwd(d, y, y, w, train=True)
+    n = ops.norm_residual_fwd(d, y, None, w, train=True)
+    host = torch.empty(1 << 22, dtype=torch.uint8)
+    for call in (lambda ws: ops.norm_gated_bwd(d, y, w, f.rstd, y8=f.y8, z8=f.z8, ws=ws),
+                 lambda ws: ops.norm_residual_bwd(d, y, w, n.rstd, r8=n.r8, ws=ws),
+                 lambda ws: ops.ckpt8_wgrad(y, f.y8, width, ws=ws)):
+        assert _status(call, host) == ssm.SSM_ERR_UNSUPPORTED
+        call(host.cuda())
