@@ -524,7 +524,8 @@ def norm_residual_bwd(desc, dh, w, rstd, *, dr_out=None, r_out=None, r8=None, b=
                       rstd_post=None, w_post=None, scale=None, d_r=None, d_b=None, d_w=None,
                       d_w_post=None, d_scale=None, ws=None, stream=None) -> NormResidualGrad:
     """Backward of ``norm_residual_fwd`` from r_out or its 8-bit checkpoint
-    (and b or its, with w_post or scale).  d_r may be dr_out."""
+    (and b or its, with w_post or for d_scale).  A scale without b, b8 and
+    d_scale is a constant: its gradient is not formed.  d_r may be dr_out."""
     where, M, W = "norm_residual_bwd", desc.n_rows, desc.width
     dev = _device_of(stream)
     io, res = TORCH_IO[desc.io_dtype], TORCH_IO[desc.res_dtype]
@@ -553,7 +554,7 @@ def norm_residual_bwd(desc, dh, w, rstd, *, dr_out=None, r_out=None, r8=None, b=
         d_w = _empty((W,), torch.float32, dh.device, stream)
     if w_post is not None and d_w_post is None:
         d_w_post = _empty((W,), torch.float32, dh.device, stream)
-    if scale is not None and d_scale is None:
+    if scale is not None and d_scale is None and (b is not None or b8 is not None):
         d_scale = _empty((W,), torch.float32, dh.device, stream)
     _dense(where, "d_w", d_w, W, torch.float32, dev)
     _dense(where, "d_w_post", d_w_post, W, torch.float32, dev)

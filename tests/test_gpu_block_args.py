@@ -63,3 +63,26 @@ def test_workspace_in_host_memory():
                  lambda ws: ops.ckpt8_wgrad(y, f.y8, width, ws=ws)):
         assert _status(call, host) == ssm.SSM_ERR_UNSUPPORTED
         call(host.cuda())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_frozen_scale(io):
+    """A scale that is not trained needs no branch in the backward, in ops as in
+    the library: without b there is no d_scale, and the rest is the same."""
+    rows, width = 33, 200
+    b, dh = (R.draw(k, rows, width).to(R.DTYPES[io]).cuda() for k in (1, 2))
+    r, dr = (R.draw(k, rows, width).cuda() for k in (3, 4))
+    w, scale = (1 + 0.1 * R.draw(5, width)).cuda(), (0.3 + 0.1 * R.draw(6, width)).cuda()
+    d = ops.norm_desc(n_rows=rows, width=width, io=io, res_scale=0.7)
+    f = ops.norm_residual_fwd(d, b, r, w, scale=scale, train=True)
+    args = dict(dr_out=dr, r8=f.r8, scale=scale)
+    full = ops.norm_residual_bwd(d, dh, w, f.rstd, b8=f.b8, **args)
+    frozen = ops.norm_residual_bwd(d, dh, w, f.rstd, **args)
+    assert full.d_scale is not None and frozen.d_scale is None
+    want = R.residual_bwd(dh.double().cpu(), dr.double().cpu(), R.kept(f.r_out.cpu()), R.kept(b.cpu()),
+                          w.double().cpu(), f.rstd.double().cpu(), scale=scale.double().cpu(), alpha=0.7)
+    for name, kind in (("d_r", "f32"), ("d_b", io), ("d_w", "f32")):
+        R.check(name, getattr(frozen, name), *want[name], kind, R.COUNT_SUM if name == "d_w" else R.COUNT)
+    # asked for by its tensor, it still needs the branch
+    assert _status(ops.norm_residual_bwd, d, dh, w, f.rstd, d_scale=torch.empty(width, device="cuda"),
+                   **args) == ssm.SSM_ERR_NULL
