@@ -387,8 +387,10 @@ int selective_state_update(const ssm_scan_desc *desc, float *s, const void *x, c
  * their own alignment only; checkpoints need 16 bytes.  n_rows may be 0:
  * column sums are then written as zero.  A NaN or an infinity in a row stays
  * in that row's outputs and in the column sums.  Statistics and sums are f32;
- * a result is rounded once, to nearest even, when it is stored.  Sums over
- * rows have a fixed order: results repeat bitwise. */
+ * a result is rounded once, to nearest even, when it is stored.  What a norm
+ * is taken of (u, b, r_out below) may have any magnitude that f32 holds: a row
+ * whose squares add up past f32 is normalised like any other.  Sums over rows
+ * have a fixed order: results repeat bitwise. */
 
 enum { SSM_NORM_GATE_AFTER = 1u }; /* gated norm: the gate multiplies the normalised value */
 

@@ -76,12 +76,11 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_fwd(FwdP p) 
                 ss[k] += x[k][j] * x[k][j];
             }
         }
-        unit_sum(ss, rstd, lds, turn++, lane.group, groups);
+        unit_rstd(ss, [&](int k, int j) { return x[k][j]; }, rstd, lds, turn, lane.group, groups, p.inv_n, p.eps);
         if (row < p.M) {
 #pragma unroll
             for (int k = 0; k < NC; ++k) {
                 const int at = lane.at(k);
-                rstd[k] = rsqrt1(rstd[k] * p.inv_n + p.eps);
                 if (p.rstd && (RS::SEGMENTS ? at < n && at % p.Wg == 0 : at == 0)) p.rstd[row * p.G + lane.group[k]] = rstd[k];
                 float o[8], v[8];
 #pragma unroll

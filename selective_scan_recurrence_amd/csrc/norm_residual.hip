@@ -85,9 +85,7 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_fwd(FwdP 
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ss[k] += o.b[k][j] * o.b[k][j];
             }
-            unit_sum(ss, post, lds, turn++, lane.group, groups);
-#pragma unroll
-            for (int k = 0; k < NC; ++k) post[k] = rsqrt1(post[k] * p.inv_n + p.eps);
+            unit_rstd(ss, [&](int k, int j) { return o.b[k][j]; }, post, lds, turn, lane.group, groups, p.inv_n, p.eps);
             if (valid && p.rstd_post && lane.ul.lane == 0) p.rstd_post[row] = post[0];
         }
 #pragma unroll
@@ -99,9 +97,8 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void residual_fwd(FwdP 
                 ss[k] += x[k][j] * x[k][j];
             }
         }
-        unit_sum(ss, rstd, lds, turn++, lane.group, groups);
+        unit_rstd(ss, [&](int k, int j) { return x[k][j]; }, rstd, lds, turn, lane.group, groups, p.inv_n, p.eps);
         if (valid) {
-            rstd[0] = rsqrt1(rstd[0] * p.inv_n + p.eps);
             if (p.rstd && lane.ul.lane == 0) p.rstd[row] = rstd[0];
 #pragma unroll
             for (int k = 0; k < NC; ++k) {
