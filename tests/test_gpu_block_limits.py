@@ -106,3 +106,18 @@ def test_infinities_keep_to_their_row():
     assert torch.isfinite(want).all() and bool(want.any(1).all())
     assert float(rstd2[2]) == 0.0 and float(rstd2[5]) == 0.0 and torch.isnan(rstd2[6]).all()
     assert torch.isnan(got[2, 60]) and not got[2, :60].any() and torch.isnan(got[6]).all()
+
+
+@pytest.mark.parametrize("width", [20, 200, 900, 2560, 9000, 32768])
+def test_norms_of_the_largest_values(width):
+    """Rows of plus and minus the largest f32 have rms of that size and come out
+    as plus and minus w.  (rstd = 2.9e-39 is subnormal, with steps of 2^-149:
+    half of one is 2^-22 of it, which is 4 more half steps.)"""
+    rows, top = 5, torch.finfo(torch.float32).max
+    sign = torch.where(R.draw(width, rows, width) < 0, -1.0, 1.0)
+    w = 1 + 0.2 * R.draw(width + 1, width)
+    d = ops.norm_desc(n_rows=rows, width=width, io="f32")
+    x = (sign * top).cuda()
+    want = sign.double() * w.double()
+    R.check("gated", ops.norm_gated_fwd(d, x, None, w.cuda()).out, want, want.abs(), "f32", R.COUNT + 4)
+    R.check("residual", ops.norm_residual_fwd(d, None, x, w.cuda()).h, want, want.abs(), "f32", R.COUNT + 4)
