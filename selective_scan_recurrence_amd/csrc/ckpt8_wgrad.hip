@@ -22,14 +22,17 @@
 // f32 partial in the workspace, and a second kernel adds them in order.
 //
 // Bound by the matrix units, two workgroups a CU: 8192 rows, 4096 x 4096, bf16
-// dy, 242 us = 1136 TFLOP/s when 512 tiles fill the CUs at once (a library product
-// of 8192^3 in bf16 reaches 1251); 8192 rows, 10576 x 2560, 485 - 512 us = 867 -
-// 915 TFLOP/s (840 tiles: a round of 512 and a part of one; a library product of
-// the same sizes with x in bf16 takes 565 us).  Leaving out half of the dy loads
+// dy, where 512 tiles fill the CUs at once, 242 us = 1136 TFLOP/s over one set of
+// tensors, which the last-level cache holds, and 273 us = 1007 over three in turn
+// (a library product of 8192^3 in bf16 reaches 1251); 8192 rows, 10576 x 2560,
+// 497 and 514 us = 892 and 863 TFLOP/s (840 tiles: a round of 512 and a part of
+// one; a library product of the same sizes with x in bf16 takes 565 to 578 us).  Leaving out half of the dy loads
 // there gains 10% (its rows start off the cache lines), the loads of scales or
 // the conversions nothing; narrower tiles that fill the rounds better lose
 // (columns 112: 544 - 579 us, 96: 670), and so do other orders of the loads and
-// the MFMAs.  f32 dy, 4096 rows, 5120 x 2560: 447 us, three MFMAs a product.
+// the MFMAs.  f32 dy, 4096 rows, 5120 x 2560: 450 us = 716 TFLOP/s of its three
+// MFMAs a product: 400 tiles on 256 places, one workgroup a CU with 400 registers
+// a lane, whose one wave a SIMD splits dy and multiplies in turn.
 #include <type_traits>
 
 #include "block_internal.h"

@@ -26,10 +26,13 @@ __global__ __launch_bounds__(RS::L ? kRowThreads : 1024) void gated_bwd(BwdP p) 
     constexpr int L = RS::L, NC = RS::NC, U = units_per_block<L>();
     constexpr Ends RAGGED = RS::RAGGED;
     // A workgroup's row with more than one piece a lane (groups past 8192) does
-    // not fit the 128 registers that 1024 lanes leave each: no piece is kept
-    // between the sums nor loaded a row ahead, each is loaded when it is needed,
-    // the second time from the caches.  8192 x 16384 bf16: 1160 us with every
-    // piece held and half of them spilled, 700 us so; 8192 x 12288: 920 and 605.
+    // not fit the 128 registers that 1024 lanes leave each: none is loaded a row
+    // ahead, each is loaded when it is needed, the second time from the caches.
+    // 8192 x 16384 bf16: 1160 us with every piece held and half of them spilled,
+    // 700 us so; 8192 x 12288: 920 and 605.  What bounds it now are spills still:
+    // a lane past the end loads nothing and so keeps its piece, which makes every
+    // piece live across the sum (gated: 28 to 56 registers spilled with two
+    // pieces, 152 to 321 with four), beside the 16 or 32 column sums.
     constexpr bool LEAN = L == 0 && NC > 1;
     __shared__ SumMemory<L, NC, RS::SEGMENTS> lds;
     __shared__ float sm[L ? kRowThreads * 8 : 1];

@@ -182,9 +182,13 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sums(SumP p) {
 }  // namespace
 
 // A unit of a workgroup takes at least 2 rows, and the workgroups are those that
-// 256 compute units hold at a time with 4 waves on each SIMD, where a workgroup
-// of more than 4 waves counts as if it filled its last four; beyond 768 of them
-// only as many as leave 16 rows for each, so that the partial sums stay few
+// 256 compute units hold at a time with 4 waves on each SIMD (2 for a wave with
+// more than one piece), where a workgroup of more than 4 waves counts as if it
+// filled its last four.  That is what 128 registers a lane (256) leave room for:
+// the residual norm with the branch takes up to 171, and with three pieces up to
+// 374 in all but the bf16 form without the branch, so that theirs run in more
+// rounds than one.  Beyond 768 of them
+// there are only as many as leave 16 rows for each, so that the partial sums stay few
 // beside the rows.  (Gated backward of 65536 rows in bf16, times of a copy's:
 // width 2560, 5 waves, 1.66, 1.08, 1.38 with 1, 2, 3 workgroups on a unit; width
 // 1280, 3 waves, 1.35, 1.13, 1.01, 1.35 with 3 to 6; width 2048, 4 waves, 0.93,
