@@ -80,6 +80,7 @@ enum {
 enum {
     SSM_DEVERR_IDS = 1u,     /* an ids[i] was outside [0, n_state_rows) */
     SSM_DEVERR_SEQLENS = 2u, /* a cu_seqlens span was invalid (selective_scan_fwd_ext) */
+    SSM_DEVERR_TARGET = 8u,  /* a target or a teacher's id was n_vocab or more (ssm_vocab_*) */
     SSM_DEVERR_RELAY = 4u    /* a workgroup of a split grid gave up waiting for the
                                 values of the time piece before its own (only if the
                                 device stalls for seconds); that call's results are
@@ -508,6 +509,87 @@ int ssm_norm_residual_bwd(const ssm_norm_desc *desc, const void *dh, const void 
                           const float *rstd_post, void *d_r, void *d_b, float *d_w, float *d_w_post,
                           float *d_scale, void *workspace, size_t workspace_bytes,
                           ssm_stream_t stream);
+
+/* ---- the loss over the vocabulary -------------------------------------------
+ * What follows the last norm of a model that answers with tokens: the product
+ * of the normed rows with the vocabulary's weights, and a loss of its softmax.
+ * The pages define none of them; their formulas are those given here.  With
+ *   s_iv = scale * sum_d h_id W_vd,  lse_i = log sum_v exp(s_iv)
+ *   cross entropy:  loss_i = lse_i - s_{i,target_i}
+ *   distillation:   loss_i = sum_k p_ik (log p_ik - logq_ik),
+ *                   logq_ik = s_{i,top_id_ik} - lse_i
+ * where p_i is the softmax of top_scale * top_logit_i over the row's entries, or
+ * with top_lse exp(top_scale * top_logit_ik - top_lse_i) as it stands (a part
+ * of the teacher's mass: then sum_k p_ik <= 1).  The backward gives the gradients
+ * of sum_i (d_loss_i loss_i + d_lse_i lse_i):
+ *   g_iv = scale * ((d_loss_i sum_k p_ik + d_lse_i) exp(s_iv - lse_i)
+ *                   - d_loss_i sum_{k: top_id_ik = v} p_ik)
+ *   d_h = g W,  d_W = g^T h             (cross entropy: one entry with p = 1)
+ * The logits are formed in pieces of the vocabulary and never kept; the backward
+ * forms them again.
+ *
+ * Rows without a target (target < 0; no entry with an id >= 0 and a logit above
+ * -inf) are left out: loss, lse and logq are 0, d_h is 0, and their rows of h,
+ * d_loss and d_lse are not read, so they may hold anything.  A row with a target
+ * or an id of n_vocab or more has loss, lse, logq and d_h NaN, adds nothing to
+ * d_W, and sets SSM_DEVERR_TARGET in *err (a device word, NULL: dropped).  Entries
+ * with the same id add up; an absent entry's logq is 0.
+ *
+ * Products of bf16 values are exact and summed in f32; in f32 they are formed of
+ * three bf16 terms a value and are off by at most 2^-21 of the product (an
+ * infinity may come out as NaN; parts below 2^-126 may count as zero).  g enters
+ * its two products in the io type's terms: with bf16 io it is rounded to bf16, as
+ * the outputs are, also when d_W is f32.  Sums have a fixed order: results repeat
+ * bitwise. */
+typedef struct ssm_vocab_desc {
+    int64_t n_rows;     /* 0..2^21                                               */
+    int64_t width;      /* 1..2^16                                               */
+    int64_t n_vocab;    /* 1..2^24                                               */
+    int64_t n_top;      /* teacher's entries a row, 1..1024; cross entropy: 0    */
+    int64_t ld_h;       /* row strides of h and d_h, and of w and d_w, in        */
+    int64_t ld_w;       /* elements (0: width), at most 2^22                     */
+    int32_t io_dtype;   /* ssm_dtype of h, w and d_h                             */
+    int32_t dw_dtype;   /* ssm_dtype of d_w: io's, or f32                        */
+    float scale;        /* of the logits (1 / temperature); finite               */
+    float top_scale;    /* of the teacher's logits; finite                       */
+    uint32_t flags;     /* SSM_VOCAB_ACCUMULATE                                  */
+    uint32_t reserved;  /* must be 0                                             */
+} ssm_vocab_desc;
+
+enum { SSM_VOCAB_ACCUMULATE = 1u }; /* the backward adds to d_w */
+
+/* Workspace of a forward (backward = 0) or a backward (1): bytes, 256-byte
+ * aligned, no initial contents.  0 for a bad descriptor.  One of a backward
+ * serves the forward too. */
+size_t ssm_vocab_workspace_bytes(const ssm_vocab_desc *desc, int backward);
+
+/* Cross entropy of h [n_rows][width] with w [n_vocab][width] against target
+ * [n_rows] int32.  loss, lse [n_rows] f32: either may be NULL. */
+int ssm_vocab_ce_fwd(const ssm_vocab_desc *desc, const void *h, const void *w, const int32_t *target,
+                     float *loss, float *lse, uint32_t *err, void *workspace, size_t workspace_bytes,
+                     ssm_stream_t stream);
+
+/* Its backward.  loss and lse are the forward's.  d_loss [n_rows] f32, d_lse the
+ * same or NULL (zeros).  d_h [n_rows][width] io, d_w [n_vocab][width]: either may
+ * be NULL. */
+int ssm_vocab_ce_bwd(const ssm_vocab_desc *desc, const void *h, const void *w, const int32_t *target,
+                     const float *loss, const float *lse, const float *d_loss, const float *d_lse,
+                     void *d_h, void *d_w, void *workspace, size_t workspace_bytes,
+                     ssm_stream_t stream);
+
+/* Distillation from top_id [n_rows][n_top] int32 and top_logit [n_rows][n_top] f32
+ * (top_lse [n_rows] f32 or NULL).  loss, lse [n_rows], logq [n_rows][n_top] f32:
+ * each may be NULL. */
+int ssm_vocab_kd_fwd(const ssm_vocab_desc *desc, const void *h, const void *w, const int32_t *top_id,
+                     const float *top_logit, const float *top_lse, float *loss, float *lse,
+                     float *logq, uint32_t *err, void *workspace, size_t workspace_bytes,
+                     ssm_stream_t stream);
+
+/* Its backward, from the forward's logq and lse; the rest as ssm_vocab_ce_bwd. */
+int ssm_vocab_kd_bwd(const ssm_vocab_desc *desc, const void *h, const void *w, const int32_t *top_id,
+                     const float *top_logit, const float *top_lse, const float *logq,
+                     const float *lse, const float *d_loss, const float *d_lse, void *d_h, void *d_w,
+                     void *workspace, size_t workspace_bytes, ssm_stream_t stream);
 
 /* Copies the device-error word of a workspace to *bits (synchronises the
  * stream; for tests and debugging, not for the hot path). */

@@ -15,4 +15,6 @@ from ._binding import (  # noqa: F401
     SSM_NORM_GATE_AFTER, SsmNormDesc, ssm_ckpt8_bytes, ssm_ckpt8_pack, ssm_ckpt8_unpack,
     ssm_ckpt8_wgrad, ssm_ckpt8_wgrad_workspace_bytes, ssm_norm_bwd_workspace_bytes,
     ssm_norm_gated_bwd, ssm_norm_gated_fwd, ssm_norm_residual_bwd, ssm_norm_residual_fwd,
+    SSM_DEVERR_TARGET, SSM_VOCAB_ACCUMULATE, SsmVocabDesc, ssm_vocab_ce_bwd, ssm_vocab_ce_fwd,
+    ssm_vocab_kd_bwd, ssm_vocab_kd_fwd, ssm_vocab_workspace_bytes,
 )

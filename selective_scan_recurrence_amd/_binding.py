@@ -18,7 +18,8 @@ SSM_OK, SSM_ERR_NULL, SSM_ERR_SHAPE, SSM_ERR_DTYPE, SSM_ERR_UNSUPPORTED, \
 SSM_F32, SSM_BF16 = 0, 1
 SSM_HAS_D, SSM_DT_SOFTPLUS = 1, 2
 SSM_NORM_GATE_AFTER = 1
-SSM_DEVERR_IDS, SSM_DEVERR_SEQLENS, SSM_DEVERR_RELAY = 1, 2, 4
+SSM_VOCAB_ACCUMULATE = 1
+SSM_DEVERR_IDS, SSM_DEVERR_SEQLENS, SSM_DEVERR_RELAY, SSM_DEVERR_TARGET = 1, 2, 4, 8
 
 EXPORTS = ("ssm_status_str", "ssm_version", "ssm_scan_out_bytes", "ssm_scan_state_offset_bytes",
            "ssm_scan_dgrad_layout", "ssm_scan_workspace_bytes", "ssm_conv_fwd",
@@ -28,7 +29,9 @@ EXPORTS = ("ssm_status_str", "ssm_version", "ssm_scan_out_bytes", "ssm_scan_stat
            "selective_scan_fwd_static", "selective_scan_bwd_conv", "ssm_ckpt8_bytes",
            "ssm_ckpt8_pack", "ssm_ckpt8_unpack", "ssm_ckpt8_wgrad_workspace_bytes",
            "ssm_ckpt8_wgrad", "ssm_norm_gated_fwd", "ssm_norm_bwd_workspace_bytes",
-           "ssm_norm_gated_bwd", "ssm_norm_residual_fwd", "ssm_norm_residual_bwd")
+           "ssm_norm_gated_bwd", "ssm_norm_residual_fwd", "ssm_norm_residual_bwd",
+           "ssm_vocab_workspace_bytes", "ssm_vocab_ce_fwd", "ssm_vocab_ce_bwd", "ssm_vocab_kd_fwd",
+           "ssm_vocab_kd_bwd")
 
 
 class SsmError(RuntimeError):
@@ -60,6 +63,15 @@ class SsmNormDesc(ctypes.Structure):
                 ("res_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("res_scale", ctypes.c_float), ("flags", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32)]
+
+
+class SsmVocabDesc(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("n_vocab", ctypes.c_int64), ("n_top", ctypes.c_int64),
+                ("ld_h", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("top_scale", ctypes.c_float),
+                ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
 
 
 _lib = None
@@ -127,7 +139,16 @@ def load():
         lib.ssm_norm_residual_fwd.argtypes = [N] + [P] * 13
         lib.ssm_norm_residual_bwd.argtypes = [N] + [P] * 17 + [SZ, P]
         for fn in ("ssm_ckpt8_pack", "ssm_ckpt8_unpack", "ssm_ckpt8_wgrad", "ssm_norm_gated_fwd",
-                   "ssm_norm_gated_bwd", "ssm_norm_residual_fwd", "ssm_norm_residual_bwd"):
+                   "ssm_norm_gated_bwd", "ssm_norm_residual_fwd", "ssm_norm_residual_bwd",
+           "ssm_vocab_workspace_bytes", "ssm_vocab_ce_fwd", "ssm_vocab_ce_bwd", "ssm_vocab_kd_fwd",
+           "ssm_vocab_kd_bwd"):
+            getattr(lib, fn).restype = ctypes.c_int
+        V = ctypes.POINTER(SsmVocabDesc)
+        lib.ssm_vocab_workspace_bytes.argtypes = [V, ctypes.c_int]
+        lib.ssm_vocab_workspace_bytes.restype = SZ
+        for fn, n in (("ssm_vocab_ce_fwd", 7), ("ssm_vocab_ce_bwd", 10), ("ssm_vocab_kd_fwd", 10),
+                      ("ssm_vocab_kd_bwd", 12)):
+            getattr(lib, fn).argtypes = [V] + [P] * n + [SZ, P]
             getattr(lib, fn).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -359,6 +380,42 @@ def ssm_norm_residual_bwd(desc, dh, dr_out, r_out, r8, b, b8, w_post, scale, w, 
                                       _ptr(d_w), _ptr(d_w_post), _ptr(d_scale), _ptr(workspace),
                                       int(workspace_bytes), _stream(stream))
     return _check(rc, "ssm_norm_residual_bwd")
+
+
+def ssm_vocab_workspace_bytes(desc: SsmVocabDesc, backward: int) -> int:
+    return load().ssm_vocab_workspace_bytes(ctypes.byref(desc), int(backward))
+
+
+def ssm_vocab_ce_fwd(desc, h, w, target, loss, lse, err, workspace, workspace_bytes, stream=None):
+    rc = load().ssm_vocab_ce_fwd(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(target), _ptr(loss),
+                                 _ptr(lse), _ptr(err), _ptr(workspace), int(workspace_bytes),
+                                 _stream(stream))
+    return _check(rc, "ssm_vocab_ce_fwd")
+
+
+def ssm_vocab_ce_bwd(desc, h, w, target, loss, lse, d_loss, d_lse, d_h, d_w, workspace,
+                     workspace_bytes, stream=None):
+    rc = load().ssm_vocab_ce_bwd(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(target), _ptr(loss),
+                                 _ptr(lse), _ptr(d_loss), _ptr(d_lse), _ptr(d_h), _ptr(d_w),
+                                 _ptr(workspace), int(workspace_bytes), _stream(stream))
+    return _check(rc, "ssm_vocab_ce_bwd")
+
+
+def ssm_vocab_kd_fwd(desc, h, w, top_id, top_logit, top_lse, loss, lse, logq, err, workspace,
+                     workspace_bytes, stream=None):
+    rc = load().ssm_vocab_kd_fwd(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(top_id),
+                                 _ptr(top_logit), _ptr(top_lse), _ptr(loss), _ptr(lse), _ptr(logq),
+                                 _ptr(err), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    return _check(rc, "ssm_vocab_kd_fwd")
+
+
+def ssm_vocab_kd_bwd(desc, h, w, top_id, top_logit, top_lse, logq, lse, d_loss, d_lse, d_h, d_w,
+                     workspace, workspace_bytes, stream=None):
+    rc = load().ssm_vocab_kd_bwd(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(top_id),
+                                 _ptr(top_logit), _ptr(top_lse), _ptr(logq), _ptr(lse),
+                                 _ptr(d_loss), _ptr(d_lse), _ptr(d_h), _ptr(d_w), _ptr(workspace),
+                                 int(workspace_bytes), _stream(stream))
+    return _check(rc, "ssm_vocab_kd_bwd")
 
 
 def ssm_get_device_error(workspace, stream=None) -> int:

@@ -1,0 +1,335 @@
+// The C ABI of the losses over a vocabulary (declared in include/ssm.h): argument
+// checks on the host, the workspace's layout, and the launches of a call.
+// Nothing here reads device memory or allocates.
+#include <math.h>
+
+#include <initializer_list>
+
+#include "vocab.h"
+
+namespace ssm {
+namespace {
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }  // NULL passes
+bool known(int32_t dtype) { return dtype == SSM_F32 || dtype == SSM_BF16; }
+size_t size_of(int32_t dtype) { return dtype == SSM_BF16 ? 2 : 4; }
+int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+struct VocabShape {
+    int N, D, V, K, top;
+    int64_t ld_h, ld_w;
+    int io, dw, terms;
+    float scale, top_scale;
+    bool accumulate;
+};
+
+int check(const ssm_vocab_desc* d, VocabShape* out) {
+    if (!d) return SSM_ERR_NULL;
+    if (!known(d->io_dtype) || !known(d->dw_dtype)) return SSM_ERR_DTYPE;
+    if (d->reserved != 0 || (d->flags & ~(uint32_t)SSM_VOCAB_ACCUMULATE)) return SSM_ERR_SHAPE;
+    if (d->n_rows < 0 || d->n_rows > 1 << 21 || d->width < 1 || d->width > 1 << 16 || d->n_vocab < 1 ||
+        d->n_vocab > 1 << 24 || d->n_top < 0 || d->n_top > 1024)
+        return SSM_ERR_SHAPE;
+    VocabShape s;
+    s.N = (int)d->n_rows; s.D = (int)d->width; s.V = (int)d->n_vocab;
+    s.top = (int)d->n_top; s.K = s.top ? s.top : 1;
+    s.ld_h = d->ld_h ? d->ld_h : s.D;
+    s.ld_w = d->ld_w ? d->ld_w : s.D;
+    if (s.ld_h < s.D || s.ld_w < s.D || s.ld_h > 1 << 22 || s.ld_w > 1 << 22) return SSM_ERR_SHAPE;
+    if (!isfinite(d->scale) || !isfinite(d->top_scale)) return SSM_ERR_SHAPE;
+    s.io = d->io_dtype; s.dw = d->dw_dtype; s.terms = s.io == SSM_BF16 ? 1 : 3;
+    if (s.io == SSM_F32 && s.dw == SSM_BF16) return SSM_ERR_UNSUPPORTED;
+    s.scale = d->scale; s.top_scale = d->top_scale;
+    s.accumulate = d->flags & SSM_VOCAB_ACCUMULATE;
+    *out = s;
+    return SSM_OK;
+}
+
+// Where a call keeps what in its workspace, and the vocabulary's pieces.  A
+// piece's tensors take about a gigabyte: with 16384 rows in bf16 that is 16384
+// of the vocabulary, long enough a sum that adding to d_h once a piece costs
+// little (a piece's d_h product takes over a millisecond, the addition 0.07).
+struct Plan {
+    int64_t Np, Kd, piece;
+    int pieces;
+    bool packed;  // W goes through the workspace
+    size_t count, rows, pos, kid, h, part, state, slog, w, ht, wt, g, gt, lse2, coef, at, acc, bytes;
+};
+
+constexpr int64_t kPieceBytes = (int64_t)1 << 30;
+
+Plan plan_of(const VocabShape& s, bool backward, bool packed) {
+    Plan p;
+    p.Np = round_up(s.N ? s.N : 1, kVocabTile);
+    p.Kd = round_up(s.D, kVocabStep);
+    p.packed = packed;
+    const int64_t T = s.terms, V = round_up(s.V, kVocabTile);
+    // bytes a vocabulary entry of a piece
+    int64_t each = packed ? T * p.Kd * 2 : 0;
+    each += backward ? T * (4 * p.Np + 2 * p.Kd) : p.Np / 8;
+    int64_t most = kPieceBytes / each / kVocabTile * kVocabTile;
+    if (most < kVocabTile) most = kVocabTile;
+    p.pieces = (int)((V + most - 1) / most);
+    p.piece = round_up((V + p.pieces - 1) / p.pieces, kVocabTile);
+    p.pieces = (int)((V + p.piece - 1) / p.piece);
+
+    size_t at = 0;
+    auto take = [&](int64_t n) {
+        const size_t here = at;
+        at += (size_t)round_up(n, 256);
+        return here;
+    };
+    p.count = take(4);
+    p.rows = take(p.Np * 4);
+    p.pos = take(p.Np * 4);
+    p.kid = take(p.Np * s.K * 4);
+    p.h = take(T * p.Np * p.Kd * 2);
+    p.w = packed ? take(T * p.piece * p.Kd * 2) : 0;
+    if (backward) {
+        p.ht = take(T * s.D * p.Np * 2);
+        p.wt = take(T * s.D * p.piece * 2);
+        p.g = take(T * p.Np * p.piece * 2);
+        p.gt = take(T * p.Np * p.piece * 2);
+        p.lse2 = take(p.Np * 4);
+        p.coef = take(p.Np * 4);
+        p.at = take(p.Np * s.K * 4);
+        p.acc = take(p.Np * p.Kd * 4);
+    } else {
+        p.part = take(p.piece / 64 * p.Np * 8);
+        p.state = take(p.Np * 8);
+        p.slog = take(p.Np * s.K * 4);
+    }
+    p.bytes = at;
+    return p;
+}
+
+// W's rows are read where they are when they are whole pieces of 128 bytes
+bool reads_w(const VocabShape& s, const void* w) {
+    return s.io == SSM_BF16 && s.D % kVocabStep == 0 && s.ld_w % 8 == 0 && aligned(w, 16);
+}
+
+size_t workspace_bytes(const VocabShape& s, bool backward) {
+    // w's address is not known here: it may need the packed form
+    const size_t packed = plan_of(s, backward, true).bytes, direct = plan_of(s, backward, false).bytes;
+    size_t n = packed > direct ? packed : direct;
+    if (backward) {
+        const size_t f = workspace_bytes(s, false);
+        n = n > f ? n : f;
+    }
+    return n;
+}
+
+struct Call {
+    VocabShape s;
+    Plan p;
+    VocabRows r;
+    const void *h, *w;
+    char* ws;
+    hipStream_t stream;
+    template <typename T>
+    T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
+};
+
+Call make_call(const VocabShape& s, bool backward, const void* h, const void* w, const int32_t* id,
+               const float* logit, const float* top_lse, void* ws, hipStream_t stream) {
+    Call c = {s, plan_of(s, backward, !reads_w(s, w)), {}, h, w, static_cast<char*>(ws), stream};
+    c.r = {s.N, s.D, s.V, s.K, (int)c.p.Np, s.terms, id, logit, top_lse, s.top_scale,
+           c.at<int32_t>(c.p.count), c.at<int32_t>(c.p.rows), c.at<int32_t>(c.p.pos), c.at<int32_t>(c.p.kid)};
+    return c;
+}
+
+#define RUN(x)                  \
+    do {                        \
+        const int rc_ = (x);    \
+        if (rc_) return rc_;    \
+    } while (0)
+
+VocabPack pack_h(const Call& c, size_t to, int64_t plane) {
+    return {c.h, c.s.ld_h, c.s.io, c.s.D, c.s.N, 0, c.r.rows, c.r.count, c.at<uint16_t>(to), c.p.Np, plane};
+}
+
+VocabPack pack_w(const Call& c, int64_t v0, int n, size_t to, int64_t plane) {
+    return {c.w, c.s.ld_w, c.s.io, c.s.D, n, v0, nullptr, nullptr, c.at<uint16_t>(to), c.p.piece, plane};
+}
+
+// the product of a piece's logits; W's rows where they are, or packed
+int logits(const Call& c, VocabGemm g, int64_t v0, int n) {
+    g.terms = c.s.terms;
+    if (c.p.packed) {
+        RUN(launch_vocab_pack(pack_w(c, v0, n, c.p.w, c.p.piece * c.p.Kd), c.stream));
+        g.a = c.at<uint16_t>(c.p.w);
+        g.a_plane = c.p.piece * c.p.Kd;
+        g.lda = c.p.Kd;
+    } else {
+        g.a = static_cast<const uint16_t*>(c.w) + v0 * c.s.ld_w;
+        g.lda = c.s.ld_w;
+    }
+    g.b = c.at<uint16_t>(c.p.h);
+    g.b_plane = c.p.Np * c.p.Kd;
+    g.ldb = c.p.Kd;
+    g.m = n; g.n = c.s.N; g.k = (int)c.p.Kd;
+    g.count = c.r.count;
+    g.Np = c.p.Np;
+    g.scale2 = c.s.scale * kLog2e;
+    g.v0 = (int)v0; g.K = c.s.K; g.P = (int)c.p.piece;
+    g.kid = c.r.kid;
+    g.splits = 1;
+    return launch_vocab_gemm(g, c.stream);
+}
+
+int forward(const Call& c, float* loss, float* lse, float* logq, uint32_t* err) {
+    const Plan& p = c.p;
+    RUN(launch_vocab_rows(c.r, err, c.stream));
+    RUN(launch_vocab_pack(pack_h(c, p.h, p.Np * p.Kd), c.stream));
+    VocabGemm g = {};
+    g.mode = kLogitsFwd;
+    g.part = c.at<float2>(p.part);
+    g.slog = c.at<float>(p.slog);
+    for (int x = 0; x < p.pieces; ++x) {
+        const int64_t v0 = x * p.piece;
+        const int n = (int)(c.s.V - v0 < p.piece ? c.s.V - v0 : p.piece);
+        RUN(logits(c, g, v0, n));
+        RUN(launch_vocab_join({c.r, g.part, vocab_parts(n, c.s.N), c.at<float2>(p.state), x == 0,
+                               x == p.pieces - 1, g.slog, loss, lse, logq}, c.stream));
+    }
+    return SSM_OK;
+}
+
+int backward(const Call& c, const float* logq, const float* loss, const float* lse, const float* d_loss,
+             const float* d_lse, void* d_h, void* d_w) {
+    const Plan& p = c.p;
+    const VocabShape& s = c.s;
+    RUN(launch_vocab_rows(c.r, nullptr, c.stream));
+    if (s.N > 0) {
+        RUN(launch_vocab_pack(pack_h(c, p.h, p.Np * p.Kd), c.stream));
+        if (d_w) RUN(launch_vocab_turn(pack_h(c, p.ht, s.D * p.Np), c.stream));
+        RUN(launch_vocab_coef({c.r, logq, loss, lse, d_loss, d_lse, s.scale, c.at<float>(p.lse2),
+                               c.at<float>(p.coef), c.at<float>(p.at)}, c.stream));
+    }
+    for (int x = 0; x < p.pieces; ++x) {
+        const int64_t v0 = x * p.piece;
+        const int n = (int)(s.V - v0 < p.piece ? s.V - v0 : p.piece);
+        VocabGemm g = {};
+        if (s.N > 0) {
+            g.mode = kLogitsBwd;
+            g.lse2 = c.at<float>(p.lse2);
+            g.coef = c.at<float>(p.coef);
+            g.g = c.at<uint16_t>(p.g);
+            g.gt = c.at<uint16_t>(p.gt);
+            RUN(logits(c, g, v0, n));
+            RUN(launch_vocab_patch({c.r, c.at<float>(p.at), (int)v0, (int)p.piece, g.g, g.gt}, c.stream));
+        }
+        if (d_h && s.N > 0) {
+            RUN(launch_vocab_turn(pack_w(c, v0, n, p.wt, s.D * p.piece), c.stream));
+            g = {};
+            g.mode = kGradH; g.terms = s.terms;
+            g.a = c.at<uint16_t>(p.wt); g.a_plane = s.D * p.piece; g.lda = p.piece;
+            g.b = c.at<uint16_t>(p.g); g.b_plane = p.Np * p.piece; g.ldb = p.piece;
+            g.m = s.D; g.n = s.N; g.k = (int)round_up(n, kVocabStep);
+            g.count = c.r.count;
+            g.out = c.at<float>(p.acc); g.ld_out = p.Kd;
+            g.splits = 1; g.accumulate = x > 0;
+            RUN(launch_vocab_gemm(g, c.stream));
+        }
+        if (d_w) {
+            g = {};
+            g.mode = kGradW; g.terms = s.terms;
+            g.a = c.at<uint16_t>(p.ht); g.a_plane = s.D * p.Np; g.lda = p.Np;
+            g.b = c.at<uint16_t>(p.gt); g.b_plane = p.Np * p.piece; g.ldb = p.Np;
+            g.m = s.D; g.n = n;
+            g.count = c.r.count;
+            g.out = static_cast<char*>(d_w) + v0 * s.ld_w * (int64_t)size_of(s.dw); g.ld_out = s.ld_w;
+            g.out_dtype = s.dw; g.splits = 1; g.accumulate = s.accumulate;
+            RUN(launch_vocab_gemm(g, c.stream));
+        }
+    }
+    if (d_h && s.N > 0)
+        RUN(launch_vocab_dh({c.r, c.at<float>(p.acc), 1, (int)p.Kd, s.io, d_h, s.ld_h}, c.stream));
+    return SSM_OK;
+}
+
+// what every call checks of its tensors
+int check_call(const VocabShape& s, bool backward, const void* h, const void* w, const int32_t* id,
+               const void* ws, size_t bytes) {
+    if (!w || !ws || (s.N > 0 && (!h || !id))) return SSM_ERR_NULL;
+    if (bytes < workspace_bytes(s, backward)) return SSM_ERR_WORKSPACE;
+    const size_t es = size_of(s.io);
+    return aligned(h, es) && aligned(w, es) && aligned(id, 4) && aligned(ws, 256) ? SSM_OK : SSM_ERR_ALIGN;
+}
+
+bool all_aligned(size_t a, std::initializer_list<const void*> list) {
+    for (const void* p : list)
+        if (!aligned(p, a)) return false;
+    return true;
+}
+
+}  // namespace
+}  // namespace ssm
+
+using namespace ssm;
+
+extern "C" {
+
+size_t ssm_vocab_workspace_bytes(const ssm_vocab_desc* desc, int backward) {
+    VocabShape s;
+    return check(desc, &s) == SSM_OK ? workspace_bytes(s, backward != 0) : 0;
+}
+
+int ssm_vocab_ce_fwd(const ssm_vocab_desc* desc, const void* h, const void* w, const int32_t* target,
+                     float* loss, float* lse, uint32_t* err, void* workspace, size_t workspace_bytes,
+                     ssm_stream_t stream) {
+    VocabShape s;
+    RUN(check(desc, &s));
+    if (s.top) return SSM_ERR_SHAPE;
+    RUN(check_call(s, false, h, w, target, workspace, workspace_bytes));
+    if (!all_aligned(4, {loss, lse, err})) return SSM_ERR_ALIGN;
+    if (s.N == 0) return SSM_OK;
+    const Call c = make_call(s, false, h, w, target, nullptr, nullptr, workspace, static_cast<hipStream_t>(stream));
+    return forward(c, loss, lse, nullptr, err);
+}
+
+int ssm_vocab_ce_bwd(const ssm_vocab_desc* desc, const void* h, const void* w, const int32_t* target,
+                     const float* loss, const float* lse, const float* d_loss, const float* d_lse,
+                     void* d_h, void* d_w, void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
+    VocabShape s;
+    RUN(check(desc, &s));
+    if (s.top) return SSM_ERR_SHAPE;
+    RUN(check_call(s, true, h, w, target, workspace, workspace_bytes));
+    if (s.N > 0 && (!loss || !lse || !d_loss)) return SSM_ERR_NULL;
+    if (!all_aligned(4, {loss, lse, d_loss, d_lse}) || !aligned(d_h, size_of(s.io)) || !aligned(d_w, size_of(s.dw)))
+        return SSM_ERR_ALIGN;
+    const Call c = make_call(s, true, h, w, target, nullptr, nullptr, workspace, static_cast<hipStream_t>(stream));
+    return backward(c, nullptr, loss, lse, d_loss, d_lse, d_h, d_w);
+}
+
+int ssm_vocab_kd_fwd(const ssm_vocab_desc* desc, const void* h, const void* w, const int32_t* top_id,
+                     const float* top_logit, const float* top_lse, float* loss, float* lse, float* logq,
+                     uint32_t* err, void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
+    VocabShape s;
+    RUN(check(desc, &s));
+    if (!s.top) return SSM_ERR_SHAPE;
+    RUN(check_call(s, false, h, w, top_id, workspace, workspace_bytes));
+    if (s.N > 0 && !top_logit) return SSM_ERR_NULL;
+    if (!all_aligned(4, {top_logit, top_lse, loss, lse, logq, err})) return SSM_ERR_ALIGN;
+    if (s.N == 0) return SSM_OK;
+    const Call c = make_call(s, false, h, w, top_id, top_logit, top_lse, workspace, static_cast<hipStream_t>(stream));
+    return forward(c, loss, lse, logq, err);
+}
+
+int ssm_vocab_kd_bwd(const ssm_vocab_desc* desc, const void* h, const void* w, const int32_t* top_id,
+                     const float* top_logit, const float* top_lse, const float* logq, const float* lse,
+                     const float* d_loss, const float* d_lse, void* d_h, void* d_w, void* workspace,
+                     size_t workspace_bytes, ssm_stream_t stream) {
+    VocabShape s;
+    RUN(check(desc, &s));
+    if (!s.top) return SSM_ERR_SHAPE;
+    RUN(check_call(s, true, h, w, top_id, workspace, workspace_bytes));
+    if (s.N > 0 && (!top_logit || !logq || !lse || !d_loss)) return SSM_ERR_NULL;
+    if (!all_aligned(4, {top_logit, top_lse, logq, lse, d_loss, d_lse}) || !aligned(d_h, size_of(s.io)) ||
+        !aligned(d_w, size_of(s.dw)))
+        return SSM_ERR_ALIGN;
+    const Call c = make_call(s, true, h, w, top_id, top_logit, top_lse, workspace, static_cast<hipStream_t>(stream));
+    return backward(c, logq, nullptr, lse, d_loss, d_lse, d_h, d_w);
+}
+
+}  // extern "C"

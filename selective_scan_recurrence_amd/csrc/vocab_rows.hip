@@ -1,0 +1,401 @@
+// The losses over a vocabulary, around their products: which rows count, the
+// operands' layouts, the join of the softmax statistics, the gradient at the
+// ids, and d_h's rows.  All bound by memory or by launches; together a few
+// percent of the products' time.
+#include "vocab.h"
+
+namespace ssm {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float fast_log2(float v) { return __builtin_amdgcn_logf(v); }
+
+// A teacher's entry that counts: its id is no padding and it has some mass.
+__device__ __forceinline__ bool present(const VocabRows& r, int64_t e) {
+    return r.id[e] >= 0 && !(r.logit && r.logit[e] == -__builtin_inff());
+}
+
+__device__ __forceinline__ int row_state(const VocabRows& r, int i) {
+    int state = kRowOut;
+    for (int k = 0; k < r.K; ++k) {
+        const int64_t e = (int64_t)i * r.K + k;
+        if (!present(r, e)) continue;
+        if (r.id[e] >= r.V) return kRowBad;
+        state = 0;
+    }
+    return state;
+}
+
+__global__ __launch_bounds__(256) void rows_state(VocabRows r, uint32_t* err) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= r.N) return;
+    const int state = row_state(r, i);
+    r.pos[i] = state;
+    if (state == kRowBad && err) atomicOr(err, (uint32_t)SSM_DEVERR_TARGET);
+}
+
+// The rows that count, in order, by one workgroup: 4096 rows a round.  With
+// one entry a row (a target) the states are found here.
+__global__ __launch_bounds__(1024) void rows_list(VocabRows r, uint32_t* err) {
+    __shared__ int wave_sum[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int done = 0;
+    for (int64_t base = 0; base < r.N; base += 4096) {
+        int state[4], mine = 0;
+        const int i0 = (int)base + 4 * tid;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            state[x] = i0 + x >= r.N ? kRowOut : r.K > 1 ? r.pos[i0 + x] : row_state(r, i0 + x);
+            if (r.K == 1 && state[x] == kRowBad && err) atomicOr(err, (uint32_t)SSM_DEVERR_TARGET);
+            mine += state[x] >= 0;
+        }
+        int before = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int v = __shfl_up(before, d);
+            if (lane >= d) before += v;
+        }
+        if (lane == 63) wave_sum[wave] = before;
+        __syncthreads();
+        int c = done + before - mine, all = 0;
+        for (int w = 0; w < 16; ++w) {
+            if (w < wave) c += wave_sum[w];
+            all += wave_sum[w];
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (i0 + x >= r.N) break;
+            r.pos[i0 + x] = state[x] >= 0 ? c : state[x];
+            if (state[x] < 0) continue;
+            r.rows[c] = i0 + x;
+            if (r.K == 1) r.kid[c] = r.id[i0 + x];
+            ++c;
+        }
+        done += all;
+        __syncthreads();
+    }
+    if (tid == 0) *r.count = done;
+}
+
+__global__ __launch_bounds__(256) void rows_ids(VocabRows r) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int c = (int)(e / r.K), k = (int)(e % r.K);
+    if (c >= *r.count) return;
+    const int64_t from = (int64_t)r.rows[c] * r.K + k;
+    r.kid[e] = present(r, from) ? r.id[from] : -1;
+}
+
+// ---- layouts ----------------------------------------------------------------
+
+__device__ __forceinline__ const char* row_of(const VocabPack& p, int r) {
+    const int64_t row = p.rows ? p.rows[r] : p.r0 + r;
+    return static_cast<const char*>(p.src) + row * p.ld * (p.dtype == SSM_BF16 ? 2 : 4);
+}
+
+// eight values of a row from column c, as terms; zero past the width
+template <int TERMS>
+__device__ __forceinline__ void load8(const VocabPack& p, const char* row, int c, bool wide, uint16_t (&t)[TERMS][8]) {
+    if constexpr (TERMS == 1) {
+        const uint16_t* s = reinterpret_cast<const uint16_t*>(row) + c;
+        if (wide && c + 8 <= p.width) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(s);
+            __builtin_memcpy(t[0], &v, 16);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[0][e] = c + e < p.width ? s[e] : 0;
+    } else {
+        const float* s = reinterpret_cast<const float*>(row) + c;
+        float v[8];
+        if (wide && c + 8 <= p.width) {
+            const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < p.width ? s[e] : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint16_t w[3];
+            bf16_terms(v[e], w);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) t[n][e] = w[n];
+        }
+    }
+}
+
+template <int TERMS>
+__global__ __launch_bounds__(256) void pack_rows(VocabPack p, int pieces, bool wide) {
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int r = (int)(x / pieces), c = 8 * (int)(x % pieces);
+    if (r >= (p.count ? min(p.n, *p.count) : p.n)) return;
+    uint16_t t[TERMS][8];
+    load8<TERMS>(p, row_of(p, r), c, wide, t);
+#pragma unroll
+    for (int n = 0; n < TERMS; ++n)
+        __builtin_memcpy(__builtin_assume_aligned(p.out + n * p.plane + (int64_t)r * (8 * pieces) + c, 16), t[n], 16);
+}
+
+// a tile of 64 rows x 64 columns through LDS
+template <int TERMS>
+__global__ __launch_bounds__(256) void turn_rows(VocabPack p, bool wide) {
+    __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
+    const int n = p.count ? min(p.n, *p.count) : p.n;
+    const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64, tid = threadIdx.x;
+    if (r0 >= n) return;
+    uint16_t t[2][TERMS][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = r0 + 32 * h + tid / 8, c = c0 + 8 * (tid % 8);
+#pragma unroll
+        for (int x = 0; x < TERMS; ++x)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[h][x][e] = 0;
+        if (r < n && c < p.width) load8<TERMS>(p, row_of(p, r), c, wide, t[h]);
+    }
+#pragma unroll
+    for (int x = 0; x < TERMS; ++x) {
+        if (x) __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) tile[8 * (tid % 8) + e][32 * h + tid / 8] = t[h][x][e];
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = 32 * h + tid / 8, r = 8 * (tid % 8);
+            if (c0 + c < p.width)
+                *reinterpret_cast<u32x4*>(p.out + x * p.plane + (int64_t)(c0 + c) * p.ld_rows + r0 + r) =
+                    *reinterpret_cast<const u32x4*>(&tile[c][r]);
+        }
+    }
+}
+
+bool is_wide(const VocabPack& p) {
+    const int64_t es = p.dtype == SSM_BF16 ? 2 : 4;
+    return reinterpret_cast<uintptr_t>(p.src) % 16 == 0 && p.ld * es % 16 == 0;
+}
+
+// ---- the teacher's probabilities -----------------------------------------------
+
+// log2 p_k = t2_k - off, t2 = top_scale log2 e * logit: off from the row's
+// entries (their largest, and the sum of the rest against it) or from top_lse.
+__device__ __forceinline__ float top2(const VocabRows& r, int64_t e) {
+    return present(r, e) ? r.logit[e] * (r.top_scale * kLog2e) : -__builtin_inff();
+}
+
+// by the 2^x lanes of a group with the same row
+__device__ __forceinline__ float top_offset(const VocabRows& r, int64_t i, int lane, int lanes) {
+    if (r.top_lse) return r.top_lse[i] * kLog2e;
+    float m = -__builtin_inff(), s = 0.0f;
+    for (int k = lane; k < r.K; k += lanes) m = fmaxf(m, top2(r, i * r.K + k));
+    for (int d = 1; d < lanes; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    for (int k = lane; k < r.K; k += lanes) s += fast_exp2(top2(r, i * r.K + k) - m);
+    for (int d = 1; d < lanes; d *= 2) s += __shfl_xor(s, d);
+    return m + fast_log2(s);
+}
+
+// ---- softmax statistics ----------------------------------------------------------
+
+__device__ __forceinline__ void merge(float& m, float& s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    // an infinite sum stays one whatever it is scaled by
+    s = (s < __builtin_inff() ? s * fast_exp2(m - top) : s) + (s2 < __builtin_inff() ? s2 * fast_exp2(m2 - top) : s2);
+    m = top;
+}
+
+// 32 rows a workgroup, 8 lanes a row: a wave is 8 rows by 8 lanes
+__global__ __launch_bounds__(256) void join_rows(VocabJoin j) {
+    const VocabRows& r = j.r;
+    const int lane = threadIdx.x & 7;
+    const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x / 8;
+    if (i >= r.N) return;
+    const int c = r.pos[i];
+    if (c < 0) {
+        if (!j.last) return;
+        const float v = c == kRowBad ? __builtin_nanf("") : 0.0f;
+        if (lane == 0) {
+            if (j.loss) j.loss[i] = v;
+            if (j.lse) j.lse[i] = v;
+        }
+        if (j.logq)
+            for (int k = lane; k < r.K; k += 8) j.logq[i * r.K + k] = v;
+        return;
+    }
+    // a lane without a part holds a sum of nothing
+    float m = -0x1p127f, s = 0.0f;
+    for (int x = lane; x < j.parts; x += 8) {
+        const float2 v = j.part[(int64_t)x * r.Np + c];
+        merge(m, s, v.x, v.y);
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) merge(m, s, __shfl_xor(m, d), __shfl_xor(s, d));
+    if (!j.first) merge(m, s, j.state[c].x, j.state[c].y);
+    if (!j.last) {
+        if (lane == 0) j.state[c] = make_float2(m, s);
+        return;
+    }
+    const float l = fast_log2(s);
+    if (lane == 0 && j.lse) j.lse[i] = (m + l) * kLn2;
+    if (!r.logit) {
+        if (lane == 0 && j.loss) j.loss[i] = ((m - j.slog[c]) + l) * kLn2;
+        return;
+    }
+    const float off = top_offset(r, i, lane, 8);
+    float loss = 0.0f;
+    for (int k = lane; k < r.K; k += 8) {
+        const int64_t e = i * r.K + k;
+        const bool there = present(r, e);
+        const float q = there ? (j.slog[(int64_t)c * r.K + k] - m) - l : 0.0f, p = top2(r, e) - off;
+        if (j.logq) j.logq[e] = q * kLn2;
+        if (there) loss += fast_exp2(p) * (p - q);
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) loss += __shfl_xor(loss, d);
+    if (lane == 0 && j.loss) j.loss[i] = loss * kLn2;
+}
+
+// ---- the gradient's factors ---------------------------------------------------
+
+__global__ __launch_bounds__(256) void coef_target(VocabCoef f) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= *f.r.count) return;
+    const int i = f.r.rows[c];
+    const float d = f.scale * f.d_loss[i], a = d + (f.d_lse ? f.scale * f.d_lse[i] : 0.0f);
+    f.lse2[c] = f.lse[i] * kLog2e;
+    f.coef[c] = a;
+    f.at[c] = a * fast_exp2(-f.loss[i] * kLog2e) - d;
+}
+
+// a wave a row
+__global__ __launch_bounds__(256) void coef_top(VocabCoef f) {
+    const VocabRows& r = f.r;
+    const int c = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x & 63;
+    if (c >= *r.count) return;
+    const int64_t i = r.rows[c];
+    const float d = f.scale * f.d_loss[i], off = top_offset(r, i, lane, 64);
+    float mass = 1.0f;
+    if (r.top_lse) {
+        mass = 0.0f;
+        for (int k = lane; k < r.K; k += 64) mass += fast_exp2(top2(r, i * r.K + k) - off);
+        for (int x = 1; x < 64; x *= 2) mass += __shfl_xor(mass, x);
+    }
+    const float a = d * mass + (f.d_lse ? f.scale * f.d_lse[i] : 0.0f);
+    if (lane == 0) {
+        f.lse2[c] = f.lse[i] * kLog2e;
+        f.coef[c] = a;
+    }
+    const int32_t* ids = r.kid + (int64_t)c * r.K;
+    for (int k = lane; k < r.K; k += 64) {
+        if (ids[k] < 0) continue;
+        float p = 0.0f;  // of every entry with this id
+        for (int x = 0; x < r.K; ++x)
+            if (ids[x] == ids[k]) p += fast_exp2(top2(r, i * r.K + x) - off);
+        f.at[(int64_t)c * r.K + k] = a * fast_exp2(f.logq[i * r.K + k] * kLog2e) - d * p;
+    }
+}
+
+template <int TERMS>
+__global__ __launch_bounds__(256) void patch_ids(VocabPatch p) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int c = (int)(e / p.r.K);
+    if (c >= *p.r.count) return;
+    const int v = p.r.kid[e] - p.v0;
+    if (p.r.kid[e] < p.v0 || v >= p.P) return;
+    const int64_t at = (int64_t)c * p.P + v, at_t = (int64_t)v * p.r.Np + c, plane = (int64_t)p.r.Np * p.P;
+    if constexpr (TERMS == 1) {
+        p.g[at] = p.gt[at_t] = bf16_rne(p.at[e]);
+    } else {
+        uint16_t t[3];
+        bf16_terms(p.at[e], t);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) p.g[n * plane + at] = p.gt[n * plane + at_t] = t[n];
+    }
+}
+
+// four columns of a row of d_h
+__global__ __launch_bounds__(256) void dh_rows(VocabDh d, int pieces) {
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = x / pieces;
+    const int col = 4 * (int)(x % pieces);
+    if (i >= d.r.N) return;
+    const int c = d.r.pos[i];
+    const float fill = c == kRowBad ? __builtin_nanf("") : 0.0f;
+    float v[4] = {fill, fill, fill, fill};
+    if (c >= 0)
+        for (int s = 0; s < d.parts; ++s) {
+            const float4 a = *reinterpret_cast<const float4*>(d.acc + ((int64_t)s * d.r.Np + c) * d.Dp + col);
+            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        }
+    const int64_t at = i * d.ld + col;
+    const int left = d.r.D - col;
+    if (d.io == SSM_F32) {
+        float* to = static_cast<float*>(d.d_h) + at;
+        if (left >= 4) __builtin_memcpy(to, v, 16);
+        else
+            for (int e = 0; e < left; ++e) to[e] = v[e];
+    } else {
+        uint16_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = bf16_rne(v[e]);
+        uint16_t* to = static_cast<uint16_t*>(d.d_h) + at;
+        if (left >= 4) __builtin_memcpy(to, w, 8);
+        else
+            for (int e = 0; e < left; ++e) to[e] = w[e];
+    }
+}
+
+unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
+int launched() { return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
+
+}  // namespace
+
+int launch_vocab_rows(const VocabRows& r, uint32_t* err, hipStream_t stream) {
+    if (r.K > 1 && r.N > 0) rows_state<<<blocks(r.N, 256), 256, 0, stream>>>(r, err);
+    rows_list<<<1, 1024, 0, stream>>>(r, err);
+    if (r.K > 1 && r.N > 0) rows_ids<<<blocks((int64_t)r.N * r.K, 256), 256, 0, stream>>>(r);
+    return launched();
+}
+
+int launch_vocab_pack(const VocabPack& p, hipStream_t stream) {
+    const int pieces = (p.width + 63) / 64 * 8;
+    const unsigned grid = blocks((int64_t)p.n * pieces, 256);
+    if (p.dtype == SSM_BF16) pack_rows<1><<<grid, 256, 0, stream>>>(p, pieces, is_wide(p));
+    else pack_rows<3><<<grid, 256, 0, stream>>>(p, pieces, is_wide(p));
+    return launched();
+}
+
+int launch_vocab_turn(const VocabPack& p, hipStream_t stream) {
+    const dim3 grid(blocks(p.n, 64), blocks(p.width, 64));
+    if (p.dtype == SSM_BF16) turn_rows<1><<<grid, 256, 0, stream>>>(p, is_wide(p));
+    else turn_rows<3><<<grid, 256, 0, stream>>>(p, is_wide(p));
+    return launched();
+}
+
+int launch_vocab_join(const VocabJoin& j, hipStream_t stream) {
+    join_rows<<<blocks(j.r.N, 32), 256, 0, stream>>>(j);
+    return launched();
+}
+
+int launch_vocab_coef(const VocabCoef& c, hipStream_t stream) {
+    if (!c.r.logit) coef_target<<<blocks(c.r.N, 256), 256, 0, stream>>>(c);
+    else coef_top<<<blocks(c.r.N, 4), 256, 0, stream>>>(c);
+    return launched();
+}
+
+int launch_vocab_patch(const VocabPatch& p, hipStream_t stream) {
+    const unsigned grid = blocks((int64_t)p.r.N * p.r.K, 256);
+    if (p.r.terms == 1) patch_ids<1><<<grid, 256, 0, stream>>>(p);
+    else patch_ids<3><<<grid, 256, 0, stream>>>(p);
+    return launched();
+}
+
+int launch_vocab_dh(const VocabDh& d, hipStream_t stream) {
+    const int pieces = (d.r.D + 3) / 4;
+    dh_rows<<<blocks((int64_t)d.r.N * pieces, 256), 256, 0, stream>>>(d, pieces);
+    return launched();
+}
+
+}  // namespace ssm

@@ -566,3 +566,147 @@ def norm_residual_bwd(desc, dh, w, rstd, *, dr_out=None, r_out=None, r8=None, b=
     B.ssm_norm_residual_bwd(desc, dh, dr_out, r_out, r8, b, b8, w_post, scale, w, rstd, rstd_post,
                             d_r, d_b, d_w, d_w_post, d_scale, ws, ws.numel(), stream)
     return NormResidualGrad(d_r, d_b, d_w, d_w_post, d_scale)
+
+
+# ---- the loss over the vocabulary ----
+#
+# As above: [n_rows][width] and [n_vocab][width] matrices with a contiguous last
+# axis, everything checked here that the C ABI cannot see, on the call's device.
+
+
+def vocab_desc(*, n_rows, width, n_vocab, n_top=0, io="bf16", dw="f32", scale=1.0, top_scale=1.0,
+               ld_h=0, ld_w=0, accumulate=False) -> B.SsmVocabDesc:
+    """Descriptor of the losses over a vocabulary.  n_top: the teacher's entries
+    a row (0: cross entropy).  dw: type of d_w, f32 or io's.  ld_h, ld_w: row
+    strides in elements (0: width) of h and d_h, and of w and d_w.  accumulate:
+    the backward adds to d_w."""
+    def dtype(v):
+        return IO_DTYPES[v] if isinstance(v, str) else int(v)
+
+    return B.SsmVocabDesc(int(n_rows), int(width), int(n_vocab), int(n_top), int(ld_h) or int(width),
+                          int(ld_w) or int(width), dtype(io), dtype(dw), float(scale),
+                          float(top_scale), B.SSM_VOCAB_ACCUMULATE if accumulate else 0, 0)
+
+
+def vocab_workspace(desc: B.SsmVocabDesc, backward: bool, device="cuda", stream=None) -> torch.Tensor:
+    """Workspace of a forward, or of a backward (which serves the forward too)."""
+    n = B.ssm_vocab_workspace_bytes(desc, int(backward))
+    if n == 0:
+        raise B.SsmError(B.SSM_ERR_SHAPE, "ssm_vocab_workspace_bytes")
+    return _empty((n,), torch.uint8, device, stream)
+
+
+@dataclass
+class VocabLoss:
+    loss: torch.Tensor             # [n_rows] f32
+    lse: torch.Tensor              # [n_rows] f32
+    logq: Optional[torch.Tensor]   # [n_rows][n_top] f32 (distillation)
+
+
+@dataclass
+class VocabGrad:
+    d_h: Optional[torch.Tensor]    # [n_rows][width] io
+    d_w: Optional[torch.Tensor]    # [n_vocab][width]
+
+
+def _vocab_inputs(where, desc, h, w, dev):
+    _matrix(where, "h", h, desc.n_rows, desc.width, desc.ld_h, TORCH_IO[desc.io_dtype], dev)
+    _matrix(where, "w", w, desc.n_vocab, desc.width, desc.ld_w, TORCH_IO[desc.io_dtype], dev)
+
+
+def _vocab_entries(where, name, t, desc, dtype, dev):
+    """[n_rows][n_top], dense."""
+    if t is not None and t.shape != (desc.n_rows, desc.n_top):
+        _refuse(B.SSM_ERR_SHAPE, where, name, t)
+    _dense(where, name, t, desc.n_rows * desc.n_top, dtype, dev)
+
+
+def _vocab_fwd(where, desc, h, w, loss, lse, err, ws, dev, stream):
+    _vocab_inputs(where, desc, h, w, dev)
+    M = desc.n_rows
+    loss = _empty((M,), torch.float32, w.device, stream) if loss is None else loss
+    lse = _empty((M,), torch.float32, w.device, stream) if lse is None else lse
+    _dense(where, "loss", loss, M, torch.float32, dev)
+    _dense(where, "lse", lse, M, torch.float32, dev)
+    if err is not None:
+        _dense(where, "err", err, 1, torch.int32, dev)
+    if ws is None:
+        ws = vocab_workspace(desc, False, w.device, stream)
+    else:
+        _dense(where, "ws", ws, 0, ws.dtype, dev)
+    return loss, lse, ws
+
+
+def _vocab_bwd(where, desc, h, w, lse, d_loss, d_lse, d_h, d_w, want_h, want_w, ws, dev, stream):
+    _vocab_inputs(where, desc, h, w, dev)
+    M, io, dw = desc.n_rows, TORCH_IO[desc.io_dtype], TORCH_IO[desc.dw_dtype]
+    _dense(where, "lse", lse, M, torch.float32, dev)
+    _dense(where, "d_loss", d_loss, M, torch.float32, dev)
+    _dense(where, "d_lse", d_lse, M, torch.float32, dev)
+    if d_h is None and want_h:
+        d_h = _matrix_like(M, desc.width, desc.ld_h, io, w.device, stream)
+    _matrix(where, "d_h", d_h, M, desc.width, desc.ld_h, io, dev)
+    if d_w is None and want_w:
+        if desc.flags & B.SSM_VOCAB_ACCUMULATE:
+            raise B.SsmError(B.SSM_ERR_NULL, f"{where}: accumulate without d_w")
+        d_w = _matrix_like(desc.n_vocab, desc.width, desc.ld_w, dw, w.device, stream)
+    _matrix(where, "d_w", d_w, desc.n_vocab, desc.width, desc.ld_w, dw, dev)
+    if ws is None:
+        ws = vocab_workspace(desc, True, w.device, stream)
+    else:
+        _dense(where, "ws", ws, 0, ws.dtype, dev)
+    return d_h, d_w, ws
+
+
+def vocab_ce_fwd(desc, h, w, target, *, loss=None, lse=None, err=None, ws=None, stream=None) -> VocabLoss:
+    """Softmax cross entropy of scale * h w^T against target [n_rows] int32
+    (ssm_vocab_ce_fwd): a loss a row, 0 where the target is negative."""
+    where, dev = "vocab_ce_fwd", _device_of(stream)
+    loss, lse, ws = _vocab_fwd(where, desc, h, w, loss, lse, err, ws, dev, stream)
+    _dense(where, "target", target, desc.n_rows, torch.int32, dev)
+    B.ssm_vocab_ce_fwd(desc, h, w, target, loss, lse, err, ws, ws.numel(), stream)
+    return VocabLoss(loss, lse, None)
+
+
+def vocab_ce_bwd(desc, h, w, target, loss, lse, d_loss, *, d_lse=None, d_h=None, d_w=None, want_h=True,
+                 want_w=True, ws=None, stream=None) -> VocabGrad:
+    """Backward of ``vocab_ce_fwd`` from its loss and lse.  want_h, want_w: form
+    the gradient although no tensor is given for it."""
+    where, dev = "vocab_ce_bwd", _device_of(stream)
+    _dense(where, "target", target, desc.n_rows, torch.int32, dev)
+    _dense(where, "loss", loss, desc.n_rows, torch.float32, dev)
+    d_h, d_w, ws = _vocab_bwd(where, desc, h, w, lse, d_loss, d_lse, d_h, d_w, want_h, want_w, ws, dev,
+                              stream)
+    B.ssm_vocab_ce_bwd(desc, h, w, target, loss, lse, d_loss, d_lse, d_h, d_w, ws, ws.numel(), stream)
+    return VocabGrad(d_h, d_w)
+
+
+def vocab_kd_fwd(desc, h, w, top_id, top_logit, *, top_lse=None, loss=None, lse=None, logq=None, err=None,
+                 ws=None, stream=None) -> VocabLoss:
+    """Distillation from a teacher's top logits [n_rows][n_top] f32 at top_id
+    int32 (ssm_vocab_kd_fwd).  An id < 0 or a logit of -inf is no entry."""
+    where, dev = "vocab_kd_fwd", _device_of(stream)
+    loss, lse, ws = _vocab_fwd(where, desc, h, w, loss, lse, err, ws, dev, stream)
+    if logq is None:
+        logq = _empty((desc.n_rows, desc.n_top), torch.float32, w.device, stream)
+    _vocab_entries(where, "top_id", top_id, desc, torch.int32, dev)
+    _vocab_entries(where, "top_logit", top_logit, desc, torch.float32, dev)
+    _vocab_entries(where, "logq", logq, desc, torch.float32, dev)
+    _dense(where, "top_lse", top_lse, desc.n_rows, torch.float32, dev)
+    B.ssm_vocab_kd_fwd(desc, h, w, top_id, top_logit, top_lse, loss, lse, logq, err, ws, ws.numel(), stream)
+    return VocabLoss(loss, lse, logq)
+
+
+def vocab_kd_bwd(desc, h, w, top_id, top_logit, logq, lse, d_loss, *, top_lse=None, d_lse=None, d_h=None,
+                 d_w=None, want_h=True, want_w=True, ws=None, stream=None) -> VocabGrad:
+    """Backward of ``vocab_kd_fwd`` from its logq and lse."""
+    where, dev = "vocab_kd_bwd", _device_of(stream)
+    _vocab_entries(where, "top_id", top_id, desc, torch.int32, dev)
+    _vocab_entries(where, "top_logit", top_logit, desc, torch.float32, dev)
+    _vocab_entries(where, "logq", logq, desc, torch.float32, dev)
+    _dense(where, "top_lse", top_lse, desc.n_rows, torch.float32, dev)
+    d_h, d_w, ws = _vocab_bwd(where, desc, h, w, lse, d_loss, d_lse, d_h, d_w, want_h, want_w, ws, dev,
+                              stream)
+    B.ssm_vocab_kd_bwd(desc, h, w, top_id, top_logit, top_lse, logq, lse, d_loss, d_lse, d_h, d_w, ws,
+                       ws.numel(), stream)
+    return VocabGrad(d_h, d_w)
