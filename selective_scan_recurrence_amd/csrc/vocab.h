@@ -15,6 +15,7 @@ namespace ssm {
 // by 64 or 128 rows (m).
 constexpr int kVocabStep = 64;
 constexpr int kVocabTile = 256;  // what tensors in the workspace are padded to
+constexpr int kVocabSplits = 8;  // of d_h's sum over the vocabulary, at most
 
 // What the small kernels need of a call.  `rows` are the rows that count, in
 // order: row c of them is row rows[c] of h.
@@ -28,7 +29,7 @@ struct VocabRows {
     int32_t* count;      // rows that count
     int32_t* rows;       // [Np]
     int32_t* pos;        // [N]: place among rows, kRowOut or kRowBad
-    int32_t* kid;        // [Np][K] ids of the rows that count, -1 for an absent entry
+    int32_t* kid;        // [K][Np] ids of the rows that count, -1 for an absent entry
 };
 constexpr int32_t kRowOut = -1, kRowBad = -2;
 
@@ -56,7 +57,7 @@ struct VocabCoef {
     const float *logq, *loss, *lse, *d_loss, *d_lse;
     float scale;
     float *lse2, *coef;  // [Np]
-    float *at;           // [Np][K]: g at entry k's id
+    float *at;           // [K][Np]: g at entry k's id
 };
 int launch_vocab_coef(const VocabCoef& c, hipStream_t stream);
 
@@ -66,7 +67,7 @@ struct VocabJoin {
     int parts;
     float2* state;       // [Np] of the pieces before, or NULL
     bool first, last;
-    const float* slog;   // [Np][K] logits at the ids, times log2 e
+    const float* slog;   // [K][Np] logits at the ids, times log2 e
     float *loss, *lse, *logq;
 };
 int launch_vocab_join(const VocabJoin& j, hipStream_t stream);
@@ -75,7 +76,7 @@ int launch_vocab_join(const VocabJoin& j, hipStream_t stream);
 struct VocabPatch {
     VocabRows r;
     const float* at;
-    int v0, P;
+    int v0, P, terms;
     uint16_t *g, *gt;  // [terms][Np][P], [terms][P][Np]
 };
 int launch_vocab_patch(const VocabPatch& p, hipStream_t stream);
@@ -91,42 +92,49 @@ struct VocabDh {
 int launch_vocab_dh(const VocabDh& d, hipStream_t stream);
 
 // out[n][m] = sum_k A[m][k] B[n][k] over planes of bf16 terms, k in steps of 64.
-enum VocabMode { kLogitsFwd, kLogitsBwd, kGradH, kGradW };
 struct VocabGemm {
-    int mode, terms;
     const uint16_t *a, *b;
     int64_t a_plane, b_plane, lda, ldb;
     int m, n, k;           // rows of A and of B, and length of the sum
-    const int32_t* count;  // device: bounds n (kGradW: k)
+    const int32_t* count;  // device: bounds n (d_w: k, in whole steps)
     int64_t Np;
-    // kLogitsFwd, kLogitsBwd
+    // logits
     float scale2;          // scale * log2 e
-    int v0, K;
-    float2* part;
+    int v0, K, P;          // the piece's start, ids a row, the piece's length
+    float2* part;          // forward
     const int32_t* kid;
     float* slog;
-    const float *lse2, *coef;
+    const float *lse2, *coef;  // backward
     uint16_t *g, *gt;
-    int P;
-    // kGradH, kGradW: out row n (from row0), splits of k
+    // d_h: f32 [splits][Np][ld_out], each split a part of k; d_w: out rows of n
     void* out;
-    int64_t ld_out, split_stride;
+    int64_t ld_out;
     int splits, out_dtype;
     bool accumulate;
 };
-int vocab_parts(int m, int n);  // partials of a kLogitsFwd product, at most m / 64 + 4
-int launch_vocab_gemm(const VocabGemm& g, hipStream_t stream);
+int vocab_parts(int m, int n);  // partials of a forward's logits, at most m / 64 + 4
+int vocab_splits(const VocabGemm& d_h, const VocabGemm& d_w, int g_terms);
+int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream);
+int launch_vocab_logits_bwd(const VocabGemm& g, int terms, int g_terms, hipStream_t stream);
+// both products of the gradient (n = 0: not that one)
+int launch_vocab_grads(const VocabGemm& d_h, const VocabGemm& d_w, int terms, int g_terms, hipStream_t stream);
 
-// v as bf16 terms: exact in three, each what the ones before leave with the low
-// half cut off (no rounding passes the largest value); an infinity or a NaN is
+// v as bf16 terms.  One: v rounded.  Two: that, and the rest rounded (2^-17 of v is
+// left).  Three: v itself, each term what the ones before leave with the low half
+// cut off, so that no rounding passes the largest value.  An infinity or a NaN is
 // all in the first.
-__device__ __forceinline__ void bf16_terms(float v, uint16_t (&t)[3]) {
-    const uint32_t bits = __float_as_uint(v);
-    const bool finite = fabsf(v) < __builtin_inff();
-    t[0] = v != v ? 0x7fc0 : bits >> 16;
-    const float left = finite ? v - __uint_as_float(bits & 0xffff0000u) : 0.0f;
-    t[1] = __float_as_uint(left) >> 16;
-    t[2] = __float_as_uint(left - __uint_as_float(__float_as_uint(left) & 0xffff0000u)) >> 16;
+template <int TERMS>
+__device__ __forceinline__ void bf16_terms(float v, uint16_t (&t)[TERMS]) {
+    if constexpr (TERMS < 3) {
+        t[0] = bf16_rne(v);
+        if constexpr (TERMS == 2) t[1] = fabsf(to_f32(t[0])) < __builtin_inff() ? bf16_rne(v - to_f32(t[0])) : 0;
+    } else {
+        const uint32_t bits = __float_as_uint(v);
+        t[0] = v != v ? 0x7fc0 : bits >> 16;
+        const float left = fabsf(v) < __builtin_inff() ? v - __uint_as_float(bits & 0xffff0000u) : 0.0f;
+        t[1] = __float_as_uint(left) >> 16;
+        t[2] = __float_as_uint(left - __uint_as_float(__float_as_uint(left) & 0xffff0000u)) >> 16;
+    }
 }
 
 }  // namespace ssm

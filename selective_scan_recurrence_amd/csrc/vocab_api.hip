@@ -15,8 +15,14 @@ bool known(int32_t dtype) { return dtype == SSM_F32 || dtype == SSM_BF16; }
 size_t size_of(int32_t dtype) { return dtype == SSM_BF16 ? 2 : 4; }
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
+// With so few rows a gradient may hang on a single rounded value of g, and the
+// products wait for W's bytes: a second term of g costs little and takes its
+// rounding (2^-9 of a value) out of the result.
+constexpr int kVocabFewRows = 128;
+
 struct VocabShape {
     int N, D, V, K, top;
+    int g_terms;  // bf16 terms of g
     int64_t ld_h, ld_w;
     int io, dw, terms;
     float scale, top_scale;
@@ -38,6 +44,7 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
     if (s.ld_h < s.D || s.ld_w < s.D || s.ld_h > 1 << 22 || s.ld_w > 1 << 22) return SSM_ERR_SHAPE;
     if (!isfinite(d->scale) || !isfinite(d->top_scale)) return SSM_ERR_SHAPE;
     s.io = d->io_dtype; s.dw = d->dw_dtype; s.terms = s.io == SSM_BF16 ? 1 : 3;
+    s.g_terms = s.terms == 3 ? 3 : s.N <= kVocabFewRows ? 2 : 1;
     if (s.io == SSM_F32 && s.dw == SSM_BF16) return SSM_ERR_UNSUPPORTED;
     s.scale = d->scale; s.top_scale = d->top_scale;
     s.accumulate = d->flags & SSM_VOCAB_ACCUMULATE;
@@ -46,17 +53,29 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
 }
 
 // Where a call keeps what in its workspace, and the vocabulary's pieces.  A
-// piece's tensors take about a gigabyte: with 16384 rows in bf16 that is 16384
+// piece's tensors take up to 1.25 GiB: with 16384 rows in bf16 that is 16384
 // of the vocabulary, long enough a sum that adding to d_h once a piece costs
 // little (a piece's d_h product takes over a millisecond, the addition 0.07).
 struct Plan {
     int64_t Np, Kd, piece;
-    int pieces;
+    int pieces, splits;
     bool packed;  // W goes through the workspace
     size_t count, rows, pos, kid, h, part, state, slog, w, ht, wt, g, gt, lse2, coef, at, acc, bytes;
 };
 
-constexpr int64_t kPieceBytes = (int64_t)1 << 30;
+constexpr int64_t kPieceBytes = (int64_t)5 << 28;
+
+// of d_h's sum: for both products, or for d_h alone, whichever has more
+int splits_of(const VocabShape& s, const Plan& p) {
+    VocabGemm h = {}, w = {};
+    h.m = w.m = s.D;
+    h.n = s.N;
+    h.k = (int)p.piece;
+    const int alone = vocab_splits(h, w, s.g_terms);
+    w.n = (int)p.piece;
+    const int both = vocab_splits(h, w, s.g_terms);
+    return both > alone ? both : alone;
+}
 
 Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     Plan p;
@@ -66,7 +85,7 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     const int64_t T = s.terms, V = round_up(s.V, kVocabTile);
     // bytes a vocabulary entry of a piece
     int64_t each = packed ? T * p.Kd * 2 : 0;
-    each += backward ? T * (4 * p.Np + 2 * p.Kd) : p.Np / 8;
+    each += backward ? 4 * s.g_terms * p.Np + 2 * T * p.Kd : p.Np / 8;
     int64_t most = kPieceBytes / each / kVocabTile * kVocabTile;
     if (most < kVocabTile) most = kVocabTile;
     p.pieces = (int)((V + most - 1) / most);
@@ -88,12 +107,13 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     if (backward) {
         p.ht = take(T * s.D * p.Np * 2);
         p.wt = take(T * s.D * p.piece * 2);
-        p.g = take(T * p.Np * p.piece * 2);
-        p.gt = take(T * p.Np * p.piece * 2);
+        p.g = take(s.g_terms * p.Np * p.piece * 2);
+        p.gt = take(s.g_terms * p.Np * p.piece * 2);
         p.lse2 = take(p.Np * 4);
         p.coef = take(p.Np * 4);
         p.at = take(p.Np * s.K * 4);
-        p.acc = take(p.Np * p.Kd * 4);
+        p.splits = splits_of(s, p);
+        p.acc = take(p.splits * p.Np * p.Kd * 4);
     } else {
         p.part = take(p.piece / 64 * p.Np * 8);
         p.state = take(p.Np * 8);
@@ -152,9 +172,9 @@ VocabPack pack_w(const Call& c, int64_t v0, int n, size_t to, int64_t plane) {
     return {c.w, c.s.ld_w, c.s.io, c.s.D, n, v0, nullptr, nullptr, c.at<uint16_t>(to), c.p.piece, plane};
 }
 
-// the product of a piece's logits; W's rows where they are, or packed
-int logits(const Call& c, VocabGemm g, int64_t v0, int n) {
-    g.terms = c.s.terms;
+// the operands of a piece's logits; W's rows where they are, or packed
+int logits(const Call& c, int64_t v0, int n, VocabGemm* out) {
+    VocabGemm g = {};
     if (c.p.packed) {
         RUN(launch_vocab_pack(pack_w(c, v0, n, c.p.w, c.p.piece * c.p.Kd), c.stream));
         g.a = c.at<uint16_t>(c.p.w);
@@ -173,22 +193,22 @@ int logits(const Call& c, VocabGemm g, int64_t v0, int n) {
     g.scale2 = c.s.scale * kLog2e;
     g.v0 = (int)v0; g.K = c.s.K; g.P = (int)c.p.piece;
     g.kid = c.r.kid;
-    g.splits = 1;
-    return launch_vocab_gemm(g, c.stream);
+    *out = g;
+    return SSM_OK;
 }
 
 int forward(const Call& c, float* loss, float* lse, float* logq, uint32_t* err) {
     const Plan& p = c.p;
     RUN(launch_vocab_rows(c.r, err, c.stream));
     RUN(launch_vocab_pack(pack_h(c, p.h, p.Np * p.Kd), c.stream));
-    VocabGemm g = {};
-    g.mode = kLogitsFwd;
-    g.part = c.at<float2>(p.part);
-    g.slog = c.at<float>(p.slog);
     for (int x = 0; x < p.pieces; ++x) {
         const int64_t v0 = x * p.piece;
         const int n = (int)(c.s.V - v0 < p.piece ? c.s.V - v0 : p.piece);
-        RUN(logits(c, g, v0, n));
+        VocabGemm g;
+        RUN(logits(c, v0, n, &g));
+        g.part = c.at<float2>(p.part);
+        g.slog = c.at<float>(p.slog);
+        RUN(launch_vocab_logits_fwd(g, c.s.terms, c.stream));
         RUN(launch_vocab_join({c.r, g.part, vocab_parts(n, c.s.N), c.at<float2>(p.state), x == 0,
                                x == p.pieces - 1, g.slog, loss, lse, logq}, c.stream));
     }
@@ -199,6 +219,7 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
              const float* d_lse, void* d_h, void* d_w) {
     const Plan& p = c.p;
     const VocabShape& s = c.s;
+    if (!d_h && !d_w) return SSM_OK;
     RUN(launch_vocab_rows(c.r, nullptr, c.stream));
     if (s.N > 0) {
         RUN(launch_vocab_pack(pack_h(c, p.h, p.Np * p.Kd), c.stream));
@@ -209,42 +230,33 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
     for (int x = 0; x < p.pieces; ++x) {
         const int64_t v0 = x * p.piece;
         const int n = (int)(s.V - v0 < p.piece ? s.V - v0 : p.piece);
-        VocabGemm g = {};
+        uint16_t *g = c.at<uint16_t>(p.g), *gt = c.at<uint16_t>(p.gt);
         if (s.N > 0) {
-            g.mode = kLogitsBwd;
-            g.lse2 = c.at<float>(p.lse2);
-            g.coef = c.at<float>(p.coef);
-            g.g = c.at<uint16_t>(p.g);
-            g.gt = c.at<uint16_t>(p.gt);
-            RUN(logits(c, g, v0, n));
-            RUN(launch_vocab_patch({c.r, c.at<float>(p.at), (int)v0, (int)p.piece, g.g, g.gt}, c.stream));
+            VocabGemm l;
+            RUN(logits(c, v0, n, &l));
+            l.lse2 = c.at<float>(p.lse2);
+            l.coef = c.at<float>(p.coef);
+            l.g = g;
+            l.gt = gt;
+            RUN(launch_vocab_logits_bwd(l, s.terms, s.g_terms, c.stream));
+            RUN(launch_vocab_patch({c.r, c.at<float>(p.at), (int)v0, (int)p.piece, s.g_terms, g, gt}, c.stream));
+            if (d_h) RUN(launch_vocab_turn(pack_w(c, v0, n, p.wt, s.D * p.piece), c.stream));
         }
-        if (d_h && s.N > 0) {
-            RUN(launch_vocab_turn(pack_w(c, v0, n, p.wt, s.D * p.piece), c.stream));
-            g = {};
-            g.mode = kGradH; g.terms = s.terms;
-            g.a = c.at<uint16_t>(p.wt); g.a_plane = s.D * p.piece; g.lda = p.piece;
-            g.b = c.at<uint16_t>(p.g); g.b_plane = p.Np * p.piece; g.ldb = p.piece;
-            g.m = s.D; g.n = s.N; g.k = (int)round_up(n, kVocabStep);
-            g.count = c.r.count;
-            g.out = c.at<float>(p.acc); g.ld_out = p.Kd;
-            g.splits = 1; g.accumulate = x > 0;
-            RUN(launch_vocab_gemm(g, c.stream));
-        }
-        if (d_w) {
-            g = {};
-            g.mode = kGradW; g.terms = s.terms;
-            g.a = c.at<uint16_t>(p.ht); g.a_plane = s.D * p.Np; g.lda = p.Np;
-            g.b = c.at<uint16_t>(p.gt); g.b_plane = p.Np * p.piece; g.ldb = p.Np;
-            g.m = s.D; g.n = n;
-            g.count = c.r.count;
-            g.out = static_cast<char*>(d_w) + v0 * s.ld_w * (int64_t)size_of(s.dw); g.ld_out = s.ld_w;
-            g.out_dtype = s.dw; g.splits = 1; g.accumulate = s.accumulate;
-            RUN(launch_vocab_gemm(g, c.stream));
-        }
+        VocabGemm gh = {}, gw = {};
+        gh.a = c.at<uint16_t>(p.wt); gh.a_plane = s.D * p.piece; gh.lda = p.piece;
+        gh.b = g; gh.b_plane = p.Np * p.piece; gh.ldb = p.piece;
+        gh.m = s.D; gh.n = d_h ? s.N : 0; gh.k = (int)round_up(n, kVocabStep);
+        gh.count = c.r.count; gh.Np = p.Np;
+        gh.out = c.at<float>(p.acc); gh.ld_out = p.Kd; gh.splits = p.splits; gh.accumulate = x > 0;
+        gw.a = c.at<uint16_t>(p.ht); gw.a_plane = s.D * p.Np; gw.lda = p.Np;
+        gw.b = gt; gw.b_plane = p.Np * p.piece; gw.ldb = p.Np;
+        gw.m = s.D; gw.n = d_w ? n : 0;
+        gw.out = static_cast<char*>(d_w) + v0 * s.ld_w * (int64_t)size_of(s.dw); gw.ld_out = s.ld_w;
+        gw.out_dtype = s.dw; gw.accumulate = s.accumulate;
+        RUN(launch_vocab_grads(gh, gw, s.terms, s.g_terms, c.stream));
     }
     if (d_h && s.N > 0)
-        RUN(launch_vocab_dh({c.r, c.at<float>(p.acc), 1, (int)p.Kd, s.io, d_h, s.ld_h}, c.stream));
+        RUN(launch_vocab_dh({c.r, c.at<float>(p.acc), p.splits, (int)p.Kd, s.io, d_h, s.ld_h}, c.stream));
     return SSM_OK;
 }
 

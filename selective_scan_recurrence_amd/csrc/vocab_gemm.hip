@@ -5,28 +5,38 @@
 //            the row's ids; backward: g = coef exp2(s - lse), stored in both
 //            orders, since one product sums over the vocabulary and one over rows
 //   d_h:     A = W turned (m: width),  B = g (n: rows)
-//   d_W:     A = h turned (m: width),  B = g turned (n: vocabulary)
+//   d_w:     A = h turned (m: width),  B = g turned (n: vocabulary)
 // An f32 value is three bf16 terms, and a product the six of its nine partial
 // products that reach 2^-24 of it, the small ones first: six runs over k.
 //
-// A workgroup owns BM x BN of out and walks k in steps of 64: 128-byte rows go
-// from memory to LDS past the registers, into one of two buffers while the
-// other is multiplied.  A row's 16-byte piece c sits at c ^ f(row).  MFMA tile t of a
-// wave's rows takes rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4 (i = 0 ..
-// 15), and tile j of its 64 columns the columns 4 i + j: a lane (q = lane / 16,
-// i = lane % 16) then holds 16 neighbouring m (from 16 q) and 4 neighbouring n
-// (from 4 i), so that both orders leave in 8- to 16-byte stores.  With f = i % 8 for
-// both, any 8 neighbouring lanes of a read meet 8 different pieces.
+// A workgroup of 2 x 2 waves owns 256 x 256 (or 128 x 128) of out and walks k in
+// steps of 64: 128-byte rows go from memory to LDS past the registers, into one of
+// two buffers while the other is multiplied.  LDS holds the rows in the order of
+// MFMA tiles, row i (of 16) of tile t at 16 t + i, its 16-byte piece c at
+// c ^ (i % 8): a read of operands then meets no bank twice.  Tile t of a wave's
+// rows of A takes rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4, and tile j of
+// its TN tiles of B the rows TN i + j: a lane (q = lane / 16, i = lane % 16) ends
+// with 16 neighbouring m (from 16 q) and TN neighbouring n (from TN i), so that
+// both orders leave in stores of 8 and 16 bytes.
+//
+// The big tile has one wave a SIMD with 64 accumulators of 4 registers each, a
+// quarter fewer bytes from LDS than eight waves of 128 x 64.  That counts because
+// the card's power bounds the loop: eight waves take 2959 cycles a step at 1.9 GHz
+// and four 2775 at a lower clock, both 1.48 us, as a large library product does.
+#include <type_traits>
+
 #include "vocab.h"
 
 namespace ssm {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
+
+constexpr std::true_type yes{};
+constexpr std::false_type no{};
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0xffffffff, 0x00020000);
@@ -40,295 +50,536 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t from, uint8_t* t
 #endif
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    return (uint32_t)bf16_rne(lo) | (uint32_t)bf16_rne(hi) << 16;
+// c += A B, with c in the accumulation registers: left to itself the compiler
+// moves accumulators between the two halves of a 512-register wave.
+__device__ __forceinline__ void mfma(f32x4& c, const u32x4& a, const u32x4& b) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
-// planes of the six partial products, small ones first
-__device__ __forceinline__ int plane_a(int t) { return (0x001102 >> (4 * t)) & 15; }
-__device__ __forceinline__ int plane_b(int t) { return (0x010120 >> (4 * t)) & 15; }
-
-template <int WM, int WN, int TM, int MODE, int TERMS>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 ? 2 : 2) void vocab_gemm(VocabGemm p) {
-    constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * 64, U = TM / 4;
-    constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;
-    constexpr int kStage = (BM + BN) * 128;
-    static_assert(2 * kStage >= NW * 16384, "the logits at the ids pass through LDS");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WN, wn = wave % WN, q = lane >> 4, i16 = lane & 15;
-
-    const int count = p.count ? *p.count : 0;
-    const int n_rows = MODE == kGradW ? p.n : min(p.n, count);
-    const int k_len = MODE == kGradW ? (count + kVocabStep - 1) / kVocabStep * kVocabStep : p.k;
-    const int mt = (p.m + BM - 1) / BM, nt = (n_rows + BN - 1) / BN, total = mt * nt;
-    // workgroups are dealt to the 8 XCDs in turn: an XCD's are neighbouring
-    // tiles, 8 columns of tiles wide, that share A and B
-    const int split = blockIdx.y;
-    const int per = (total + 7) / 8, pid = blockIdx.x;
-    const int id = pid % 8 * per + pid / 8;
-    if (pid / 8 >= per || id >= total) return;
-    const int band = id / (mt * 8), in = id - band * mt * 8, wide = min(8, nt - 8 * band);
-    const int m0 = in / wide * BM, n0 = (8 * band + in % wide) * BN;
-
-    // k of this split, in steps
-    int s_begin = 0, s_end = k_len / kVocabStep;
-    if (p.splits > 1) {
-        const int all = s_end;
-        s_begin = (int)((int64_t)all * split / p.splits);
-        s_end = (int)((int64_t)all * (split + 1) / p.splits);
-    }
-    const int steps = s_end - s_begin, total_steps = TERMS == 1 ? steps : 6 * steps;
-
-    // loads: a wave's load is 8 rows of 8 pieces
-    uint32_t at_a[LA], at_b[LB];
-#pragma unroll
-    for (int x = 0; x < LA; ++x) {
-        const int row = 8 * (wave + NW * x) + lane / 8, f = (row & 3) | (row >> 4 & 1) << 2;
-        at_a[x] = (uint32_t)min(row, p.m - 1 - m0) * (uint32_t)(2 * p.lda) + 16 * ((lane & 7) ^ f);
-    }
-#pragma unroll
-    for (int x = 0; x < LB; ++x) {
-        const int row = 8 * (wave + NW * x) + lane / 8, f = row >> 2 & 7;
-        at_b[x] = (uint32_t)min(row, n_rows - 1 - n0) * (uint32_t)(2 * p.ldb) + 16 * ((lane & 7) ^ f);
-    }
-    const uint16_t* a = p.a + (int64_t)m0 * p.lda + (int64_t)s_begin * kVocabStep;
-    const uint16_t* b = p.b + (int64_t)n0 * p.ldb + (int64_t)s_begin * kVocabStep;
-    auto load = [&](int step, uint8_t* buf) {
-        const int term = TERMS == 1 ? 0 : step / steps, s = TERMS == 1 ? step : step - term * steps;
-        const auto ra = rsrc_of(TERMS == 1 ? a : a + plane_a(term) * p.a_plane);
-        const auto rb = rsrc_of(TERMS == 1 ? b : b + plane_b(term) * p.b_plane);
-#pragma unroll
-        for (int x = 0; x < LA; ++x) load_lds(ra, buf + (wave + NW * x) * 1024, at_a[x], s * (2 * kVocabStep));
-#pragma unroll
-        for (int x = 0; x < LB; ++x)
-            load_lds(rb, buf + BM * 128 + (wave + NW * x) * 1024, at_b[x], s * (2 * kVocabStep));
-    };
-
-    f32x4 acc[TM][4];
+// The waits between these and other uses of the accumulators, which the compiler
+// does not see: 18 cycles are the most that a result of this size takes.
+template <int TM, int TN>
+__device__ __forceinline__ void settle(f32x4 (&c)[TM][TN]) {
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
     for (int t = 0; t < TM; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
-    const uint32_t row_a = (wm * TM * 16 + 16 * (i16 >> 2) + (i16 & 3)) * 128;
-    const uint32_t row_b = BM * 128 + (wn * 64 + 4 * i16) * 128;
-    auto multiply = [&](const uint8_t* buf) {
+        for (int j = 0; j < TN; j += 4)
+            asm volatile("s_nop 0" : "+a"(c[t][j]), "+a"(c[t][j + 1]), "+a"(c[t][j + 2]), "+a"(c[t][j + 3]));
+    asm volatile("s_nop 15" ::: "memory");
+}
+
+// The accumulators are read where they are used, not all of them before: they take
+// half of the registers.
+__device__ __forceinline__ f32x4 take(const f32x4& c) {
+    f32x4 v;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v[0]) : "a"(c[0]));
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v[1]) : "a"(c[1]));
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v[2]) : "a"(c[2]));
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v[3]) : "a"(c[3]));
+    return v;
+}
+
+// A run's planes.  Two runs: the second term of g, then the first.  Six: the
+// partial products of three terms, small ones first.
+template <int RUNS>
+__device__ __forceinline__ int plane_a(int run) {
+    return RUNS == 6 ? (0x001102 >> (4 * run)) & 15 : 0;
+}
+template <int RUNS>
+__device__ __forceinline__ int plane_b(int run) {
+    return RUNS == 6 ? (0x010120 >> (4 * run)) & 15 : RUNS == 2 ? 1 - run : 0;
+}
+
+// Tiles of out, numbered in bands of 8 columns.
+struct Place {
+    int mt, nt;
+    __device__ __forceinline__ void of(int id, int* m, int* n) const {
+        const int band = id / (mt * 8), in = id - band * mt * 8, wide = min(8, nt - 8 * band);
+        *m = in / wide;
+        *n = 8 * band + in % wide;
+    }
+};
+
+// Workgroups are dealt to the 8 XCDs in turn: an XCD takes neighbouring tiles,
+// which share A and B.  `pid` counts from the first of these tiles' workgroups.
+// -1: no tile is left.
+__host__ __device__ __forceinline__ int64_t on_xcds(int64_t total) { return (total + 7) / 8 * 8; }
+__device__ __forceinline__ int tile_of(int pid, int total) {
+    const int per = (total + 7) / 8, id = pid % 8 * per + pid / 8;
+    return pid / 8 < per && id < total ? id : -1;
+}
+
+template <int TM_, int TN_>
+struct Tile {
+    static constexpr int WM = 2, WN = 2, NW = 4, TM = TM_, TN = TN_, BM = WM * TM * 16, BN = WN * TN * 16;
+    static constexpr int kStage = (BM + BN) * 128;
+    // two stages; the logits at the ids pass through 64 x TN 16 values a wave
+    static constexpr int kLds = 2 * kStage;
+    static_assert(NW * TN * 4096 <= kLds, "");
+    static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;
+};
+using Big = Tile<8, 8>;
+using Small = Tile<4, 4>;
+
+// acc = A[m0 ..] B[n0 ..]^T over steps [s0, s1) of every run.
+template <class T, int RUNS>
+__device__ __forceinline__ void product(const VocabGemm& p, int m0, int n0, int n_rows, int s0, int s1, uint8_t* lds,
+                                        f32x4 (&acc)[T::TM][T::TN]) {
+    constexpr int TM = T::TM, TN = T::TN, LA = T::LA, LB = T::LB, NW = T::NW, kStage = T::kStage;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / T::WN, wn = wave % T::WN, q = lane >> 4, i16 = lane & 15;
+    const int steps = s1 - s0, total = RUNS * steps;
+
+    // a wave's load is half an MFMA tile, 8 rows of 8 pieces
+    uint32_t at_a[LA], at_b[LB];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const uint32_t c = 16 * ((4 * ks + q) ^ (i16 & 7));
-            u32x4 fa[TM], fb[4];
+    for (int x = 0; x < LA; ++x) {
+        const int l = 8 * (wave + NW * x) + lane / 8, t = l / 16, i = l % 16;
+        const int row = 64 * (t / 4) + 16 * (i >> 2) + 4 * (t % 4) + (i & 3);
+        at_a[x] = (uint32_t)min(row, p.m - 1 - m0) * (uint32_t)(2 * p.lda) + 16 * ((lane & 7) ^ (i & 7));
+    }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) fb[j] = *reinterpret_cast<const u32x4*>(buf + row_b + j * 128 + c);
+    for (int x = 0; x < LB; ++x) {
+        const int l = 8 * (wave + NW * x) + lane / 8, t = l / 16, i = l % 16, row = 16 * TN * (t / TN) + TN * i + t % TN;
+        at_b[x] = (uint32_t)min(row, n_rows - 1 - n0) * (uint32_t)(2 * p.ldb) + 16 * ((lane & 7) ^ (i & 7));
+    }
+    const uint16_t* a = p.a + (int64_t)m0 * p.lda + (int64_t)s0 * kVocabStep;
+    const uint16_t* b = p.b + (int64_t)n0 * p.ldb + (int64_t)s0 * kVocabStep;
+    __amdgpu_buffer_rsrc_t ra, rb;
+    uint8_t* l_buf;
+    int l_at;
+    auto load_begin = [&](int step, uint8_t* buf) {
+        const int run = RUNS == 1 ? 0 : step / steps, s = step - run * steps;
+        ra = rsrc_of(a + plane_a<RUNS>(run) * p.a_plane);
+        rb = rsrc_of(b + plane_b<RUNS>(run) * p.b_plane);
+        l_buf = buf;
+        l_at = s * (2 * kVocabStep);
+    };
+    auto load_one = [&](int x) {
+        if (x < LA) load_lds(ra, l_buf + (wave + NW * x) * 1024, at_a[x], l_at);
+        else load_lds(rb, l_buf + T::BM * 128 + (wave + NW * (x - LA)) * 1024, at_b[x - LA], l_at);
+    };
+
 #pragma unroll
-            for (int t = 0; t < TM; ++t)
-                fa[t] = *reinterpret_cast<const u32x4*>(buf + row_a + (64 * (t / 4) + 4 * (t % 4)) * 128 + c);
+    for (int t = 0; t < TM; ++t)
 #pragma unroll
-            for (int t = 0; t < TM; ++t)
+        for (int j = 0; j < TN; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
+    settle(acc);
+
+    // Row e = ks TM + t of a step multiplies A's tile t with B's TN tiles.  A's tiles
+    // are read three rows ahead into a ring of four, B's of the next half step
+    // during the half before.  Three rows before a step's end all of it has been
+    // read: there every wave waits for the next step's loads, and begins those of
+    // the step after it, two a row.
+    const uint32_t row_a = (wm * TM * 16 + i16) * 128, row_b = (T::BM + wn * TN * 16 + i16) * 128;
+    u32x4 fa[4], fb[2][TN];
+    auto read_a = [&](int e, const uint8_t* buf) {
+        fa[e & 3] = *reinterpret_cast<const u32x4*>(buf + row_a + (e % TM) * 2048 + 16 * ((4 * (e / TM) + q) ^ (i16 & 7)));
+    };
+    auto read_b = [&](int ks, int j, const uint8_t* buf) {
+        fb[ks][j] = *reinterpret_cast<const u32x4*>(buf + row_b + j * 2048 + 16 * ((4 * ks + q) ^ (i16 & 7)));
+    };
+    constexpr int kPer = 2, kTurn = 2 * TM - 3;
+    static_assert((kTurn + 3) * kPer >= LA + LB, "every load of a step has a row");
+    auto step = [&](int s, auto more, auto next) {
+        const uint8_t* cur = lds + (s & 1) * kStage;
+        uint8_t* nxt = lds + ((s + 1) & 1) * kStage;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, fa[t]), __builtin_bit_cast(bf16x8, fb[j]), acc[t][j], 0, 0, 0);
+        for (int e = 0; e < 2 * TM; ++e) {
+            if constexpr (next.value)  // what is left of the loads that the step before began
+#pragma unroll
+                for (int x = (e + 3) * kPer; x < (e + 4) * kPer && x < LA + LB; ++x) load_one(x);
+            if (e + 3 < 2 * TM) read_a(e + 3, cur);
+            if (e < TM)
+#pragma unroll
+                for (int j = e * TN / TM; j < (e + 1) * TN / TM; ++j) read_b(1, j, cur);
+            if constexpr (next.value) {
+                if (e == kTurn) {
+                    __syncthreads();
+                    if constexpr (more.value) load_begin(s + 2, lds + (s & 1) * kStage);
+                }
+                if (e >= kTurn) {
+                    const int x = e - kTurn;
+                    if constexpr (more.value)
+#pragma unroll
+                        for (int y = x * kPer; y < (x + 1) * kPer; ++y) load_one(y);
+#pragma unroll
+                    for (int j = x * TN / 3; j < (x + 1) * TN / 3; ++j) read_b(0, j, nxt);
+                    read_a(x, nxt);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < TN; ++j) mfma(acc[e % TM][j], fa[e & 3], fb[e / TM][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-    if (total_steps > 0) load(0, lds);
-    for (int s = 0; s < total_steps; ++s) {
+    if (total > 0) {
+        load_begin(0, lds);
+#pragma unroll
+        for (int x = 0; x < LA + LB; ++x) load_one(x);
         __syncthreads();
-        if (s + 1 < total_steps) load(s + 1, lds + (s + 1 & 1) * kStage);
-        multiply(lds + (s & 1) * kStage);
+        if (total > 1) {
+            load_begin(1, lds + kStage);
+#pragma unroll
+            for (int x = 0; x < 3 * kPer; ++x) load_one(x);
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) read_b(0, j, lds);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) read_a(x, lds);
+        int s = 0;
+        for (; s + 2 < total; ++s) step(s, yes, yes);
+        if (s + 1 < total) step(s++, no, yes);
+        step(s, no, no);
     }
+    settle(acc);
+}
 
-    // lane (q, i): acc[4 u + s][j][r] is m = mb + 64 u + 4 s + r, n = nb + j
-    const int mw = m0 + wm * TM * 16, mb = mw + 16 * q, nw = n0 + wn * 64, nb = nw + 4 * i16;
-    if constexpr (MODE == kLogitsFwd) {
-        float top[4], sum[4];
+// Where a lane's values lie: acc[t][j][r] is m = mb + 64 (t / 4) + 4 (t % 4) + r,
+// n = nb + j.
+template <class T>
+struct Lane {
+    int lane, wave, q, i16, mw, mb, nw, nb;
+    __device__ __forceinline__ Lane(int m0, int n0) {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        q = lane >> 4;
+        i16 = lane & 15;
+        mw = m0 + wave / T::WN * T::TM * 16;
+        mb = mw + 16 * q;
+        nw = n0 + wave % T::WN * T::TN * 16;
+        nb = nw + T::TN * i16;
+    }
+};
+__device__ __forceinline__ constexpr int m_of(int t) { return 64 * (t / 4) + 4 * (t % 4); }
+
+template <class T, int RUNS>
+__global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_fwd(VocabGemm p) {
+    constexpr int TM = T::TM, TN = T::TN;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
+    const int n_rows = min(p.n, *p.count);
+    const Place place = {(p.m + T::BM - 1) / T::BM, (n_rows + T::BN - 1) / T::BN};
+    const int id = tile_of(blockIdx.x, place.mt * place.nt);
+    if (id < 0) return;
+    int m0, n0;
+    place.of(id, &m0, &n0);
+    m0 *= T::BM;
+    n0 *= T::BN;
+    f32x4 acc[TM][TN];
+    product<T, RUNS>(p, m0, n0, n_rows, 0, p.k / kVocabStep, lds, acc);
+    const Lane<T> l(m0, n0);
+
+    // a row's largest logit and sum of exponentials over the wave's vocabulary
+    float top[TN], sum[TN];
+    auto statistics = [&](auto whole) {
+        auto there = [&](int t, int r) { return whole.value || l.mb + m_of(t) + r < p.m; };
+        auto largest = [&](auto up) {
+            const float sign = up.value ? 1.0f : -1.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float m = -__builtin_inff();
+            for (int j = 0; j < TN; ++j) {
+                float m = -__builtin_inff();
 #pragma unroll
-            for (int t = 0; t < TM; ++t)
+                for (int t = 0; t < TM; ++t) {
+                    const f32x4 v = take(acc[t][j]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const bool there = mb + 64 * (t / 4) + 4 * (t % 4) + r < p.m;
-                    const float v = there ? acc[t][j][r] * p.scale2 : -__builtin_inff();
-                    acc[t][j][r] = v;
-                    m = fmaxf(m, v);
+                    for (int r = 0; r < 4; ++r)
+                        if (there(t, r)) m = fmaxf(m, sign * v[r]);
                 }
-            m = fmaxf(m, __shfl_xor(m, 16));
+                top[j] = m * (sign * p.scale2);
+            }
+        };
+        if (p.scale2 >= 0.0f) largest(yes);
+        else largest(no);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            float m = fmaxf(top[j], __shfl_xor(top[j], 16));
             m = fmaxf(m, __shfl_xor(m, 32));
             // nothing is taken off an infinite maximum: all -inf sum to 0, +inf to +inf
-            const bool none = m == -__builtin_inff();
+            const bool none = !(m > -__builtin_inff());
             m = fabsf(m) < __builtin_inff() ? m : 0.0f;
-            float l = 0.0f;
+            float s = 0.0f;
 #pragma unroll
-            for (int t = 0; t < TM; ++t)
+            for (int t = 0; t < TM; ++t) {
+                const f32x4 v = take(acc[t][j]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) l += fast_exp2(acc[t][j][r] - m);
-            l += __shfl_xor(l, 16);
-            l += __shfl_xor(l, 32);
+                for (int r = 0; r < 4; ++r)
+                    if (there(t, r)) s += fast_exp2(fmaf(v[r], p.scale2, -m));
+            }
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
             top[j] = none ? -0x1p127f : m;  // a sum of nothing, under every other
-            sum[j] = l;
+            sum[j] = s;
         }
-        if (q == 0) {
-            float4* to = reinterpret_cast<float4*>(p.part + (int64_t)(m0 / (TM * 16) + wm) * p.Np + nb);
-            to[0] = make_float4(top[0], sum[0], top[1], sum[1]);
-            to[1] = make_float4(top[2], sum[2], top[3], sum[3]);
+    };
+    if (l.mw + TM * 16 <= p.m) statistics(yes);
+    else statistics(no);
+    if (l.q == 0) {
+        float4* to = reinterpret_cast<float4*>(p.part + (int64_t)(l.mw / (TM * 16)) * p.Np + l.nb);
+#pragma unroll
+        for (int j = 0; j < TN; j += 2) to[j / 2] = make_float4(top[j], sum[j], top[j + 1], sum[j + 1]);
+    }
+
+    // the logits at the rows' ids: 64 of m at a time through LDS, a lane a row
+    constexpr int U = TM / 4;
+    bool any[U] = {};
+    const int left = p.m - l.mw;
+    for (int x = l.lane; x < TN * 16 && l.nw + x < n_rows; x += 64)
+        for (int k = 0; k < p.K; ++k) {
+            const int at = p.kid[k * p.Np + l.nw + x] - p.v0 - l.mw;
+#pragma unroll
+            for (int u = 0; u < U; ++u) any[u] |= at >= 64 * u && at < min(64 * u + 64, left);
         }
-        // the logits at the rows' ids: 64 of m at a time through LDS, a token a lane
-        __syncthreads();
-        float* mine = reinterpret_cast<float*>(lds + wave * 16384);
-        const int n = nw + lane;
-        const int32_t* ids = p.kid + (int64_t)min(n, n_rows - 1) * p.K;
+    __syncthreads();
+    float* mine = reinterpret_cast<float*>(lds + l.wave * (TN * 4096));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int base = p.v0 + mw + 64 * u, top_m = min(64, p.m - mw - 64 * u);
-            bool any = false;
-            for (int k = 0; k < p.K; ++k) any |= ids[k] >= base && ids[k] - base < top_m;
-            if (!__any(any && n < n_rows)) continue;
+    for (int u = 0; u < U; ++u) {
+        if (!__any(any[u])) continue;
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<f32x4*>(mine + (4 * i16 + j) * 64 + 4 * ((4 * q + s) ^ i16)) = acc[4 * u + s][j];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (n < n_rows)
-                for (int k = 0; k < p.K; ++k) {
-                    const int at = ids[k] - base;
-                    if (ids[k] >= base && at < top_m)
-                        p.slog[(int64_t)n * p.K + k] = mine[lane * 64 + 4 * ((at >> 2) ^ (lane >> 2)) + (at & 3)];
-                }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        }
-    } else if constexpr (MODE == kLogitsBwd) {
-        const float4 l4 = *reinterpret_cast<const float4*>(p.lse2 + nb), c4 = *reinterpret_cast<const float4*>(p.coef + nb);
-        const float lse2[4] = {l4.x, l4.y, l4.z, l4.w}, coef[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int t = 0; t < TM; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const bool there = nb + j < n_rows && mb + 64 * (t / 4) + 4 * (t % 4) + r < p.m;
-                    acc[t][j][r] = there ? coef[j] * fast_exp2(fmaf(acc[t][j][r], p.scale2, -lse2[j])) : 0.0f;
-                }
-#pragma unroll
-        for (int term = 0; term < TERMS; ++term) {
-            // this term of every value, and what it leaves for the next
-            uint32_t half[TM][4][2];
-#pragma unroll
-            for (int t = 0; t < TM; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (TERMS == 1) {
-                        half[t][j][0] = pack2(acc[t][j][0], acc[t][j][1]);
-                        half[t][j][1] = pack2(acc[t][j][2], acc[t][j][3]);
-                    } else {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float v = acc[t][j][r];
-                            w[r] = v != v ? 0x7fc0u : __float_as_uint(v) >> 16;
-                            acc[t][j][r] = fabsf(v) < __builtin_inff() ? v - __uint_as_float(w[r] << 16) : 0.0f;
-                        }
-                        half[t][j][0] = w[0] | w[1] << 16;
-                        half[t][j][1] = w[2] | w[3] << 16;
-                    }
-                }
-            uint16_t* g = p.g + term * (p.Np * p.P);
-            uint16_t* gt = p.gt + term * (p.Np * p.P);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int t = 4 * u + 2 * h;
-                        *reinterpret_cast<u32x4*>(g + (int64_t)(nb + j) * p.P + mb + 64 * u + 8 * h) =
-                            u32x4{half[t][j][0], half[t][j][1], half[t + 1][j][0], half[t + 1][j][1]};
-                    }
-#pragma unroll
-            for (int t = 0; t < TM; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t sel = r & 1 ? 0x07060302u : 0x05040100u;
-                    const u32x2 v = {__builtin_amdgcn_perm(half[t][1][r / 2], half[t][0][r / 2], sel),
-                                     __builtin_amdgcn_perm(half[t][3][r / 2], half[t][2][r / 2], sel)};
-                    const int m = mb + 64 * (t / 4) + 4 * (t % 4) + r;
-                    *reinterpret_cast<u32x2*>(gt + (int64_t)m * p.Np + nb) = v;
-                }
-        }
-    } else if constexpr (MODE == kGradH) {
-        float* out = static_cast<float*>(p.out) + split * p.split_stride;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int t = 0; t < TM; ++t) {
-                const int m = mb + 64 * (t / 4) + 4 * (t % 4);
-                if (nb + j >= n_rows || m >= p.ld_out) continue;  // ld_out: m's padded end
-                f32x4* to = reinterpret_cast<f32x4*>(out + (int64_t)(nb + j) * p.ld_out + m);
-                *to = p.accumulate ? *to + acc[t][j] : acc[t][j];
+            for (int j = 0; j < TN; ++j)
+                *reinterpret_cast<f32x4*>(mine + (TN * l.i16 + j) * 64 + 4 * ((4 * l.q + s) ^ l.i16)) =
+                    take(acc[4 * u + s][j]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int x = l.lane; x < TN * 16 && l.nw + x < n_rows; x += 64)
+            for (int k = 0; k < p.K; ++k) {
+                const int64_t e = k * p.Np + l.nw + x;
+                const int at = p.kid[e] - p.v0 - l.mw - 64 * u;
+                if (at >= 0 && at < min(64, left - 64 * u))
+                    p.slog[e] = p.scale2 * mine[x * 64 + 4 * ((at >> 2) ^ (x / TN)) + (at & 3)];
             }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int t = 0; t < TM; ++t) {
-                const int m = mb + 64 * (t / 4) + 4 * (t % 4), left = p.m - m;
-                if (nb + j >= n_rows || left <= 0) continue;
-                const int64_t at = (int64_t)(nb + j) * p.ld_out + m;
-                f32x4 v = acc[t][j];
-                if (p.out_dtype == SSM_F32) {
-                    float* to = static_cast<float*>(p.out) + at;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (p.accumulate && r < left) v[r] += to[r];
-                    if (left >= 4) __builtin_memcpy(to, &v, 16);
-                    else
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (r < left) to[r] = v[r];
-                } else {
-                    uint16_t* to = static_cast<uint16_t*>(p.out) + at;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (p.accumulate && r < left) v[r] += to_f32(to[r]);
-                    const u32x2 w = {pack2(v[0], v[1]), pack2(v[2], v[3])};
-                    if (left >= 4) __builtin_memcpy(to, &w, 8);
-                    else
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (r < left) to[r] = bf16_rne(v[r]);
-                }
-            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
-template <int WM, int WN, int TM, int MODE>
-int launch(const VocabGemm& g, hipStream_t stream) {
-    constexpr int BM = WM * TM * 16, BN = WN * 64;
-    const int64_t mt = (g.m + BM - 1) / BM, nt = (g.n + BN - 1) / BN, total = (mt * nt + 7) / 8 * 8;
-    const dim3 grid((unsigned)total, (unsigned)g.splits);
-    if (g.terms == 1) vocab_gemm<WM, WN, TM, MODE, 1><<<grid, 64 * WM * WN, 0, stream>>>(g);
-    else vocab_gemm<WM, WN, TM, MODE, 3><<<grid, 64 * WM * WN, 0, stream>>>(g);
-    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+// GT: g's terms
+template <class T, int RUNS, int GT>
+__global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_bwd(VocabGemm p) {
+    constexpr int TM = T::TM, TN = T::TN;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
+    const int n_rows = min(p.n, *p.count);
+    const Place place = {(p.m + T::BM - 1) / T::BM, (n_rows + T::BN - 1) / T::BN};
+    const int id = tile_of(blockIdx.x, place.mt * place.nt);
+    if (id < 0) return;
+    int m0, n0;
+    place.of(id, &m0, &n0);
+    m0 *= T::BM;
+    n0 *= T::BN;
+    f32x4 acc[TM][TN];
+    product<T, RUNS>(p, m0, n0, n_rows, 0, p.k / kVocabStep, lds, acc);
+    const Lane<T> l(m0, n0);
+
+    float lse2[TN], coef[TN];
+    __builtin_memcpy(lse2, p.lse2 + l.nb, sizeof lse2);
+    __builtin_memcpy(coef, p.coef + l.nb, sizeof coef);
+    const int64_t plane = p.Np * p.P;
+    // two tiles, 8 neighbouring m, at a time (one in f32, for its registers); zero
+    // past the vocabulary and the rows
+    constexpr int S = GT == 3 ? 1 : 2;
+    auto store = [&](int t0, auto whole) {
+        uint16_t g[S][TN][4][GT];
+#pragma unroll
+        for (int t = 0; t < S; ++t)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const f32x4 c = take(acc[t0 + t][j]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool there = whole.value || (l.nb + j < n_rows && l.mb + m_of(t0 + t) + r < p.m);
+                    const float v = coef[j] * fast_exp2(fmaf(c[r], p.scale2, -lse2[j]));
+                    bf16_terms<GT>(there ? v : 0.0f, g[t][j][r]);
+                }
+            }
+        const int m = l.mb + m_of(t0);
+#pragma unroll
+        for (int n = 0; n < GT; ++n) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                uint32_t w[2 * S];
+#pragma unroll
+                for (int x = 0; x < 2 * S; ++x)
+                    w[x] = g[x / 2][j][x % 2 * 2][n] | (uint32_t)g[x / 2][j][x % 2 * 2 + 1][n] << 16;
+                __builtin_memcpy(__builtin_assume_aligned(p.g + n * plane + (int64_t)(l.nb + j) * p.P + m, 8 * S), w,
+                                 sizeof w);
+            }
+#pragma unroll
+            for (int t = 0; t < S; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    uint32_t w[TN / 2];
+#pragma unroll
+                    for (int j = 0; j < TN; j += 2) w[j / 2] = g[t][j][r][n] | (uint32_t)g[t][j + 1][r][n] << 16;
+                    __builtin_memcpy(__builtin_assume_aligned(
+                        p.gt + n * plane + (int64_t)(m + 4 * t + r) * p.Np + l.nb, 2 * TN), w, sizeof w);
+                }
+        }
+    };
+    const bool whole = l.mw + TM * 16 <= p.m && l.nw + TN * 16 <= n_rows;
+#pragma unroll
+    for (int t = 0; t < TM; t += S)
+        if (whole) store(t, yes);
+        else store(t, no);
 }
 
-template <int MODE>
-int launch_mode(const VocabGemm& g, hipStream_t stream) {
-    return launch<2, 2, 4, MODE>(g, stream);
+template <class T, int RUNS>
+__device__ __forceinline__ void tile_d_h(const VocabGemm& p, int n_rows, const Place& place, int id, uint8_t* lds) {
+    constexpr int TM = T::TM, TN = T::TN;
+    int m0, n0;
+    const int tiles = place.mt * place.nt, split = id / tiles, all = p.k / kVocabStep;
+    place.of(id - split * tiles, &m0, &n0);
+    f32x4 acc[TM][TN];
+    product<T, RUNS>(p, m0 *= T::BM, n0 *= T::BN, n_rows, (int)((int64_t)all * split / p.splits),
+                     (int)((int64_t)all * (split + 1) / p.splits), lds, acc);
+    const Lane<T> l(m0, n0);
+    float* out = static_cast<float*>(p.out) + split * p.Np * p.ld_out;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+            const int m = l.mb + m_of(t);
+            if (l.nb + j >= n_rows || m >= p.ld_out) continue;  // ld_out: m's padded end
+            f32x4* to = reinterpret_cast<f32x4*>(out + (int64_t)(l.nb + j) * p.ld_out + m);
+            *to = p.accumulate ? *to + acc[t][j] : acc[t][j];
+        }
+}
+
+// a lane's values m .. m + 3 of a row of d_w; `left` of them are there
+template <typename E>
+__device__ __forceinline__ void store_dw(E* to, f32x4 v, int left, bool accumulate) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (accumulate && r < left) v[r] += to_f32(to[r]);
+    E w[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) store_io(&w[r], v[r]);
+    if (left >= 4) __builtin_memcpy(to, w, sizeof w);
+    else
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (r < left) to[r] = w[r];
+}
+
+template <class T, int RUNS>
+__device__ __forceinline__ void tile_d_w(const VocabGemm& p, int count, const Place& place, int id, uint8_t* lds) {
+    constexpr int TM = T::TM, TN = T::TN;
+    int m0, n0;
+    place.of(id, &m0, &n0);
+    f32x4 acc[TM][TN];
+    product<T, RUNS>(p, m0 *= T::BM, n0 *= T::BN, p.n, 0, (count + kVocabStep - 1) / kVocabStep, lds, acc);
+    const Lane<T> l(m0, n0);
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+            const int m = l.mb + m_of(t), left = p.m - m;
+            if (l.nb + j >= p.n || left <= 0) continue;
+            const int64_t at = (int64_t)(l.nb + j) * p.ld_out + m;
+            if (p.out_dtype == SSM_F32) store_dw(static_cast<float*>(p.out) + at, acc[t][j], left, p.accumulate);
+            else store_dw(static_cast<bf16_t*>(p.out) + at, acc[t][j], left, p.accumulate);
+        }
+}
+
+// Both products in one launch, so that the compute units that one's last round of
+// tiles leaves idle take the other's.
+template <class T, int RUNS>
+__global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void grads(VocabGemm h, VocabGemm w) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
+    const int count = *h.count, n_h = min(h.n, count);
+    const Place ph = {(h.m + T::BM - 1) / T::BM, (n_h + T::BN - 1) / T::BN};
+    const Place pw = {(w.m + T::BM - 1) / T::BM, (w.n + T::BN - 1) / T::BN};
+    // every XCD takes its part of d_h, whose sums are longer as a rule, then of d_w
+    const int tiles_h = ph.mt * ph.nt * h.splits, pid = blockIdx.x, first = (int)on_xcds(tiles_h);
+    if (pid < first) {
+        const int id = tile_of(pid, tiles_h);
+        if (id >= 0) tile_d_h<T, RUNS>(h, n_h, ph, id, lds);
+    } else {
+        const int id = tile_of(pid - first, pw.mt * pw.nt);
+        if (id >= 0) tile_d_w<T, RUNS>(w, count, pw, id, lds);
+    }
+}
+
+int64_t tiles(int64_t m, int64_t n, int tile) { return (m + tile - 1) / tile * ((n + tile - 1) / tile); }
+
+// Whether 256 x 256 tiles, one a compute unit, take less time than 128 x 128 tiles,
+// two a compute unit: a round of the small ones takes about 5/8 of a big one's.
+bool big_tiles(int64_t big, int64_t small) { return (big + 255) / 256 * 8 <= (small + 511) / 512 * 5; }
+
+bool big_logits(const VocabGemm& g) { return big_tiles(tiles(g.m, g.n, 256), tiles(g.m, g.n, 128)); }
+
+bool big_grads(const VocabGemm& h, const VocabGemm& w) {
+    return big_tiles(tiles(h.m, h.n, 256) + tiles(w.m, w.n, 256), tiles(h.m, h.n, 128) + tiles(w.m, w.n, 128));
+}
+
+
+int launched() { return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
+
+template <class T>
+int launch_fwd(const VocabGemm& g, int terms, hipStream_t stream) {
+    const unsigned grid = (unsigned)on_xcds(tiles(g.m, g.n, T::BM));
+    if (terms == 1) logits_fwd<T, 1><<<grid, 256, 0, stream>>>(g);
+    else logits_fwd<T, 6><<<grid, 256, 0, stream>>>(g);
+    return launched();
+}
+
+template <class T>
+int launch_bwd(const VocabGemm& g, int terms, hipStream_t stream) {
+    const unsigned grid = (unsigned)on_xcds(tiles(g.m, g.n, T::BM));
+    if (terms == 3) logits_bwd<T, 6, 3><<<grid, 256, 0, stream>>>(g);
+    else logits_bwd<T, 1, 1><<<grid, 256, 0, stream>>>(g);
+    return launched();
+}
+
+template <class T>
+unsigned grads_grid(const VocabGemm& h, const VocabGemm& w) {
+    return (unsigned)on_xcds(tiles(h.m, h.n, T::BM) * h.splits) + (unsigned)on_xcds(tiles(w.m, w.n, T::BM));
+}
+
+template <class T>
+int launch_grads(const VocabGemm& h, const VocabGemm& w, int terms, hipStream_t stream) {
+    if (terms == 3) grads<T, 6><<<grads_grid<T>(h, w), 256, 0, stream>>>(h, w);
+    else grads<T, 1><<<grads_grid<T>(h, w), 256, 0, stream>>>(h, w);
+    return launched();
 }
 
 }  // namespace
 
-int vocab_parts(int m, int) { return (m + 127) / 128 * 2; }
+int vocab_parts(int m, int n) {
+    return big_tiles(tiles(m, n, 256), tiles(m, n, 128)) ? (m + 255) / 256 * 2 : (m + 127) / 128 * 2;
+}
 
-int launch_vocab_gemm(const VocabGemm& g, hipStream_t stream) {
-    if (g.m <= 0 || g.n <= 0) return SSM_OK;
-    switch (g.mode) {
-        case kLogitsFwd: return launch_mode<kLogitsFwd>(g, stream);
-        case kLogitsBwd: return launch_mode<kLogitsBwd>(g, stream);
-        case kGradH: return launch_mode<kGradH>(g, stream);
-        default: return launch_mode<kGradW>(g, stream);
+// Splits of d_h's sum over the vocabulary: none longer than the work of a workgroup's
+// place, so that a long sum for few rows does not outlast all else.
+int vocab_splits(const VocabGemm& h, const VocabGemm& w, int g_terms) {
+    const bool big = g_terms != 2 && big_grads(h, w);
+    const int tile = big ? 256 : 128;
+    const int64_t th = tiles(h.m, h.n, tile), tw = tiles(w.m, w.n, tile), steps = (h.k + 63) / 64;
+    int64_t share = (th * steps + tw * ((h.n + 63) / 64)) / (big ? 256 : 512);
+    if (share < 8) share = 8;
+    const int64_t n = (steps + share - 1) / share;
+    return (int)(n < 1 ? 1 : n > kVocabSplits ? kVocabSplits : n);
+}
+
+int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream) {
+    return big_logits(g) ? launch_fwd<Big>(g, terms, stream) : launch_fwd<Small>(g, terms, stream);
+}
+
+// Two terms of g are taken for few rows, which no big tile is for.
+int launch_vocab_logits_bwd(const VocabGemm& g, int terms, int g_terms, hipStream_t stream) {
+    if (g_terms == 2) {
+        logits_bwd<Small, 1, 2><<<(unsigned)on_xcds(tiles(g.m, g.n, Small::BM)), 256, 0, stream>>>(g);
+        return launched();
     }
+    return big_logits(g) ? launch_bwd<Big>(g, terms, stream) : launch_bwd<Small>(g, terms, stream);
+}
+
+int launch_vocab_grads(const VocabGemm& h, const VocabGemm& w, int terms, int g_terms, hipStream_t stream) {
+    if (h.n + w.n == 0) return SSM_OK;
+    if (g_terms == 2) {
+        grads<Small, 2><<<grads_grid<Small>(h, w), 256, 0, stream>>>(h, w);
+        return launched();
+    }
+    return big_grads(h, w) ? launch_grads<Big>(h, w, terms, stream) : launch_grads<Small>(h, w, terms, stream);
 }
 
 }  // namespace ssm

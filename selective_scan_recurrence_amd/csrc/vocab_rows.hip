@@ -79,11 +79,11 @@ __global__ __launch_bounds__(1024) void rows_list(VocabRows r, uint32_t* err) {
 }
 
 __global__ __launch_bounds__(256) void rows_ids(VocabRows r) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int c = (int)(e / r.K), k = (int)(e % r.K);
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int c = (int)(x / r.K), k = (int)(x % r.K);
     if (c >= *r.count) return;
     const int64_t from = (int64_t)r.rows[c] * r.K + k;
-    r.kid[e] = present(r, from) ? r.id[from] : -1;
+    r.kid[(int64_t)k * r.Np + c] = present(r, from) ? r.id[from] : -1;
 }
 
 // ---- layouts ----------------------------------------------------------------
@@ -119,7 +119,7 @@ __device__ __forceinline__ void load8(const VocabPack& p, const char* row, int c
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             uint16_t w[3];
-            bf16_terms(v[e], w);
+            bf16_terms<3>(v[e], w);
 #pragma unroll
             for (int n = 0; n < 3; ++n) t[n][e] = w[n];
         }
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(256) void join_rows(VocabJoin j) {
     for (int k = lane; k < r.K; k += 8) {
         const int64_t e = i * r.K + k;
         const bool there = present(r, e);
-        const float q = there ? (j.slog[(int64_t)c * r.K + k] - m) - l : 0.0f, p = top2(r, e) - off;
+        const float q = there ? (j.slog[(int64_t)k * r.Np + c] - m) - l : 0.0f, p = top2(r, e) - off;
         if (j.logq) j.logq[e] = q * kLn2;
         if (there) loss += fast_exp2(p) * (p - q);
     }
@@ -287,32 +287,28 @@ __global__ __launch_bounds__(256) void coef_top(VocabCoef f) {
         f.lse2[c] = f.lse[i] * kLog2e;
         f.coef[c] = a;
     }
-    const int32_t* ids = r.kid + (int64_t)c * r.K;
+    const int32_t* ids = r.id + i * r.K;
     for (int k = lane; k < r.K; k += 64) {
-        if (ids[k] < 0) continue;
+        if (!present(r, i * r.K + k)) continue;
         float p = 0.0f;  // of every entry with this id
         for (int x = 0; x < r.K; ++x)
             if (ids[x] == ids[k]) p += fast_exp2(top2(r, i * r.K + x) - off);
-        f.at[(int64_t)c * r.K + k] = a * fast_exp2(f.logq[i * r.K + k] * kLog2e) - d * p;
+        f.at[(int64_t)k * r.Np + c] = a * fast_exp2(f.logq[i * r.K + k] * kLog2e) - d * p;
     }
 }
 
 template <int TERMS>
-__global__ __launch_bounds__(256) void patch_ids(VocabPatch p) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int c = (int)(e / p.r.K);
+__global__ __launch_bounds__(256) void patch_ids(VocabPatch p, int groups) {
+    const int k = blockIdx.x / groups, c = blockIdx.x % groups * 256 + threadIdx.x;
     if (c >= *p.r.count) return;
-    const int v = p.r.kid[e] - p.v0;
-    if (p.r.kid[e] < p.v0 || v >= p.P) return;
-    const int64_t at = (int64_t)c * p.P + v, at_t = (int64_t)v * p.r.Np + c, plane = (int64_t)p.r.Np * p.P;
-    if constexpr (TERMS == 1) {
-        p.g[at] = p.gt[at_t] = bf16_rne(p.at[e]);
-    } else {
-        uint16_t t[3];
-        bf16_terms(p.at[e], t);
+    const int64_t e = (int64_t)k * p.r.Np + c, plane = (int64_t)p.r.Np * p.P;
+    const int id = p.r.kid[e], v = id - p.v0;
+    if (id < p.v0 || v >= p.P) return;
+    uint16_t t[TERMS];
+    bf16_terms<TERMS>(p.at[e], t);
 #pragma unroll
-        for (int n = 0; n < 3; ++n) p.g[n * plane + at] = p.gt[n * plane + at_t] = t[n];
-    }
+    for (int n = 0; n < TERMS; ++n)
+        p.g[n * plane + (int64_t)c * p.P + v] = p.gt[n * plane + (int64_t)v * p.r.Np + c] = t[n];
 }
 
 // four columns of a row of d_h
@@ -386,9 +382,11 @@ int launch_vocab_coef(const VocabCoef& c, hipStream_t stream) {
 }
 
 int launch_vocab_patch(const VocabPatch& p, hipStream_t stream) {
-    const unsigned grid = blocks((int64_t)p.r.N * p.r.K, 256);
-    if (p.r.terms == 1) patch_ids<1><<<grid, 256, 0, stream>>>(p);
-    else patch_ids<3><<<grid, 256, 0, stream>>>(p);
+    const int groups = (int)blocks(p.r.N, 256);
+    const unsigned grid = (unsigned)groups * p.r.K;
+    if (p.terms == 1) patch_ids<1><<<grid, 256, 0, stream>>>(p, groups);
+    else if (p.terms == 2) patch_ids<2><<<grid, 256, 0, stream>>>(p, groups);
+    else patch_ids<3><<<grid, 256, 0, stream>>>(p, groups);
     return launched();
 }
 
