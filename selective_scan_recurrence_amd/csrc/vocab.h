@@ -28,7 +28,7 @@ struct VocabRows {
     float top_scale;
     int32_t* count;      // rows that count
     int32_t* rows;       // [Np]
-    int32_t* pos;        // [N]: place among rows, kRowOut or kRowBad
+    int32_t* pos;        // [N]: place among rows, kRowOut or kRowBad (NULL: not listed, rows keep their places)
     int32_t* kid;        // [K][Np] ids of the rows that count, -1 for an absent entry
 };
 constexpr int32_t kRowOut = -1, kRowBad = -2;
@@ -69,6 +69,7 @@ struct VocabJoin {
     bool first, last;
     const float* slog;   // [K][Np] logits at the ids, times log2 e
     float *loss, *lse, *logq;
+    uint32_t* err;       // for rows that are not listed
 };
 int launch_vocab_join(const VocabJoin& j, hipStream_t stream);
 
@@ -118,6 +119,31 @@ int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream);
 int launch_vocab_logits_bwd(const VocabGemm& g, int terms, int g_terms, hipStream_t stream);
 // both products of the gradient (n = 0: not that one)
 int launch_vocab_grads(const VocabGemm& d_h, const VocabGemm& d_w, int terms, int g_terms, hipStream_t stream);
+
+// Up to 64 rows (Np = 64), h and W read where they lie.  Rows keep their places; one
+// that is left out has pos < 0.
+constexpr int kVocabFew = 64;
+struct VocabFew {
+    VocabRows r;
+    const void *h, *w;
+    int64_t ld_h, ld_w;
+    float scale2;
+    int v0, P;             // the piece
+    float2* part;          // forward, a partial for every vocab_few_tile of the piece
+    float* slog;
+    const float *lse2, *coef, *at;  // backward, as VocabCoef
+    uint16_t *g, *gt;
+    float* acc;            // d_h: [splits][64][width rounded up to 64]
+    int splits;
+    bool first;            // the first piece: acc holds nothing yet
+};
+int vocab_few_tile(int64_t V, int terms);
+int vocab_few_splits(int64_t V, int64_t D);
+int launch_vocab_few_logits(const VocabFew& p, bool backward, hipStream_t stream);
+int launch_vocab_few_d_h(const VocabFew& p, hipStream_t stream);
+// Before the backward: pos, count, the factors, and h turned, [terms][width][64], with
+// the rows that are left out zero.
+int launch_vocab_few_begin(const VocabCoef& c, const VocabPack& turned, hipStream_t stream);
 
 // v as bf16 terms.  One: v rounded.  Two: that, and the rest rounded (2^-17 of v is
 // left).  Three: v itself, each term what the ones before leave with the low half

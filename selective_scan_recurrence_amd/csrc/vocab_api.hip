@@ -59,7 +59,7 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
 struct Plan {
     int64_t Np, Kd, piece;
     int pieces, splits;
-    bool packed;  // W goes through the workspace
+    bool few, packed;  // W goes through the workspace
     size_t count, rows, pos, kid, h, part, state, slog, w, ht, wt, g, gt, lse2, coef, at, acc, bytes;
 };
 
@@ -79,13 +79,15 @@ int splits_of(const VocabShape& s, const Plan& p) {
 
 Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     Plan p;
-    p.Np = round_up(s.N ? s.N : 1, kVocabTile);
+    p.few = s.N <= kVocabFew;
+    p.Np = p.few ? kVocabFew : round_up(s.N, kVocabTile);
     p.Kd = round_up(s.D, kVocabStep);
-    p.packed = packed;
+    p.packed = packed && !p.few;
+    packed = p.packed;
     const int64_t T = s.terms, V = round_up(s.V, kVocabTile);
     // bytes a vocabulary entry of a piece
     int64_t each = packed ? T * p.Kd * 2 : 0;
-    each += backward ? 4 * s.g_terms * p.Np + 2 * T * p.Kd : p.Np / 8;
+    each += backward ? 4 * s.g_terms * p.Np + (p.few ? 0 : 2 * T * p.Kd) : p.Np / (p.few ? 2 : 8);
     int64_t most = kPieceBytes / each / kVocabTile * kVocabTile;
     if (most < kVocabTile) most = kVocabTile;
     p.pieces = (int)((V + most - 1) / most);
@@ -102,20 +104,20 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     p.rows = take(p.Np * 4);
     p.pos = take(p.Np * 4);
     p.kid = take(p.Np * s.K * 4);
-    p.h = take(T * p.Np * p.Kd * 2);
+    p.h = p.few ? 0 : take(T * p.Np * p.Kd * 2);
     p.w = packed ? take(T * p.piece * p.Kd * 2) : 0;
     if (backward) {
         p.ht = take(T * s.D * p.Np * 2);
-        p.wt = take(T * s.D * p.piece * 2);
+        p.wt = p.few ? 0 : take(T * s.D * p.piece * 2);
         p.g = take(s.g_terms * p.Np * p.piece * 2);
         p.gt = take(s.g_terms * p.Np * p.piece * 2);
         p.lse2 = take(p.Np * 4);
         p.coef = take(p.Np * 4);
         p.at = take(p.Np * s.K * 4);
-        p.splits = splits_of(s, p);
+        p.splits = p.few ? vocab_few_splits(p.piece, s.D) : splits_of(s, p);
         p.acc = take(p.splits * p.Np * p.Kd * 4);
     } else {
-        p.part = take(p.piece / 64 * p.Np * 8);
+        p.part = take(p.piece / (p.few ? 16 : 64) * p.Np * 8);
         p.state = take(p.Np * 8);
         p.slog = take(p.Np * s.K * 4);
     }
@@ -197,8 +199,11 @@ int logits(const Call& c, int64_t v0, int n, VocabGemm* out) {
     return SSM_OK;
 }
 
+int forward_few(const Call& c, float* loss, float* lse, float* logq, uint32_t* err);
+
 int forward(const Call& c, float* loss, float* lse, float* logq, uint32_t* err) {
     const Plan& p = c.p;
+    if (p.few) return forward_few(c, loss, lse, logq, err);
     RUN(launch_vocab_rows(c.r, err, c.stream));
     RUN(launch_vocab_pack(pack_h(c, p.h, p.Np * p.Kd), c.stream));
     for (int x = 0; x < p.pieces; ++x) {
@@ -210,8 +215,81 @@ int forward(const Call& c, float* loss, float* lse, float* logq, uint32_t* err) 
         g.slog = c.at<float>(p.slog);
         RUN(launch_vocab_logits_fwd(g, c.s.terms, c.stream));
         RUN(launch_vocab_join({c.r, g.part, vocab_parts(n, c.s.N), c.at<float2>(p.state), x == 0,
-                               x == p.pieces - 1, g.slog, loss, lse, logq}, c.stream));
+                               x == p.pieces - 1, g.slog, loss, lse, logq, nullptr}, c.stream));
     }
+    return SSM_OK;
+}
+
+VocabFew few_of(const Call& c) {
+    VocabFew f = {};
+    f.r = c.r;
+    f.h = c.h; f.w = c.w;
+    f.ld_h = c.s.ld_h; f.ld_w = c.s.ld_w;
+    f.scale2 = c.s.scale * kLog2e;
+    f.P = (int)c.p.piece;
+    return f;
+}
+
+int forward_few(const Call& c, float* loss, float* lse, float* logq, uint32_t* err) {
+    const Plan& p = c.p;
+    VocabFew f = few_of(c);
+    f.r.pos = nullptr;
+    f.part = c.at<float2>(p.part);
+    f.slog = c.at<float>(p.slog);
+    const int tile = vocab_few_tile(c.s.V, c.s.terms);
+    for (int x = 0; x < p.pieces; ++x) {
+        f.v0 = (int)(x * p.piece);
+        const int n = c.s.V - f.v0 < f.P ? c.s.V - f.v0 : f.P;
+        RUN(launch_vocab_few_logits(f, false, c.stream));
+        RUN(launch_vocab_join({f.r, f.part, (n + tile - 1) / tile, c.at<float2>(p.state), x == 0, x == p.pieces - 1,
+                               f.slog, loss, lse, logq, err}, c.stream));
+    }
+    return SSM_OK;
+}
+
+// the product for d_w of a piece [v0, v0 + n)
+VocabGemm product_w(const Call& c, int64_t v0, int n, void* d_w) {
+    const Plan& p = c.p;
+    VocabGemm g = {};
+    g.a = c.at<uint16_t>(p.ht); g.a_plane = c.s.D * p.Np; g.lda = p.Np;
+    g.b = c.at<uint16_t>(p.gt); g.b_plane = p.Np * p.piece; g.ldb = p.Np;
+    g.m = c.s.D; g.n = d_w ? n : 0;
+    g.out = static_cast<char*>(d_w) + v0 * c.s.ld_w * (int64_t)size_of(c.s.dw); g.ld_out = c.s.ld_w;
+    g.out_dtype = c.s.dw; g.accumulate = c.s.accumulate;
+    return g;
+}
+
+VocabCoef factors(const Call& c, const float* logq, const float* loss, const float* lse, const float* d_loss,
+                  const float* d_lse) {
+    return {c.r, logq, loss, lse, d_loss, d_lse, c.s.scale, c.at<float>(c.p.lse2), c.at<float>(c.p.coef),
+            c.at<float>(c.p.at)};
+}
+
+int backward_few(const Call& c, const VocabCoef& f, void* d_h, void* d_w) {
+    const Plan& p = c.p;
+    const VocabShape& s = c.s;
+    VocabPack turned = pack_h(c, p.ht, s.D * p.Np);
+    turned.rows = turned.count = nullptr;
+    RUN(launch_vocab_few_begin(f, turned, c.stream));
+    VocabFew few = few_of(c);
+    few.lse2 = f.lse2; few.coef = f.coef; few.at = f.at;
+    few.g = c.at<uint16_t>(p.g); few.gt = c.at<uint16_t>(p.gt);
+    few.acc = c.at<float>(p.acc); few.splits = p.splits;
+    for (int x = 0; x < p.pieces; ++x) {
+        few.v0 = (int)(x * p.piece);
+        few.first = x == 0;
+        if (s.N > 0) RUN(launch_vocab_few_logits(few, true, c.stream));
+        if (d_h && s.N > 0) RUN(launch_vocab_few_d_h(few, c.stream));
+        if (d_w) {
+            VocabGemm none = {};
+            none.count = c.r.count;
+            none.splits = 1;
+            RUN(launch_vocab_grads(none, product_w(c, few.v0, s.V - few.v0 < few.P ? s.V - few.v0 : few.P, d_w),
+                                   s.terms, s.g_terms, c.stream));
+        }
+    }
+    if (d_h && s.N > 0)
+        RUN(launch_vocab_dh({c.r, few.acc, p.splits, (int)p.Kd, s.io, d_h, s.ld_h}, c.stream));
     return SSM_OK;
 }
 
@@ -220,43 +298,34 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
     const Plan& p = c.p;
     const VocabShape& s = c.s;
     if (!d_h && !d_w) return SSM_OK;
+    const VocabCoef f = factors(c, logq, loss, lse, d_loss, d_lse);
+    if (p.few) return backward_few(c, f, d_h, d_w);
     RUN(launch_vocab_rows(c.r, nullptr, c.stream));
-    if (s.N > 0) {
-        RUN(launch_vocab_pack(pack_h(c, p.h, p.Np * p.Kd), c.stream));
-        if (d_w) RUN(launch_vocab_turn(pack_h(c, p.ht, s.D * p.Np), c.stream));
-        RUN(launch_vocab_coef({c.r, logq, loss, lse, d_loss, d_lse, s.scale, c.at<float>(p.lse2),
-                               c.at<float>(p.coef), c.at<float>(p.at)}, c.stream));
-    }
+    RUN(launch_vocab_pack(pack_h(c, p.h, p.Np * p.Kd), c.stream));
+    if (d_w) RUN(launch_vocab_turn(pack_h(c, p.ht, s.D * p.Np), c.stream));
+    RUN(launch_vocab_coef(f, c.stream));
+    uint16_t *g = c.at<uint16_t>(p.g), *gt = c.at<uint16_t>(p.gt);
     for (int x = 0; x < p.pieces; ++x) {
         const int64_t v0 = x * p.piece;
         const int n = (int)(s.V - v0 < p.piece ? s.V - v0 : p.piece);
-        uint16_t *g = c.at<uint16_t>(p.g), *gt = c.at<uint16_t>(p.gt);
-        if (s.N > 0) {
-            VocabGemm l;
-            RUN(logits(c, v0, n, &l));
-            l.lse2 = c.at<float>(p.lse2);
-            l.coef = c.at<float>(p.coef);
-            l.g = g;
-            l.gt = gt;
-            RUN(launch_vocab_logits_bwd(l, s.terms, s.g_terms, c.stream));
-            RUN(launch_vocab_patch({c.r, c.at<float>(p.at), (int)v0, (int)p.piece, s.g_terms, g, gt}, c.stream));
-            if (d_h) RUN(launch_vocab_turn(pack_w(c, v0, n, p.wt, s.D * p.piece), c.stream));
-        }
-        VocabGemm gh = {}, gw = {};
+        VocabGemm l;
+        RUN(logits(c, v0, n, &l));
+        l.lse2 = f.lse2;
+        l.coef = f.coef;
+        l.g = g;
+        l.gt = gt;
+        RUN(launch_vocab_logits_bwd(l, s.terms, s.g_terms, c.stream));
+        RUN(launch_vocab_patch({c.r, f.at, (int)v0, (int)p.piece, s.g_terms, g, gt}, c.stream));
+        if (d_h) RUN(launch_vocab_turn(pack_w(c, v0, n, p.wt, s.D * p.piece), c.stream));
+        VocabGemm gh = {};
         gh.a = c.at<uint16_t>(p.wt); gh.a_plane = s.D * p.piece; gh.lda = p.piece;
         gh.b = g; gh.b_plane = p.Np * p.piece; gh.ldb = p.piece;
         gh.m = s.D; gh.n = d_h ? s.N : 0; gh.k = (int)round_up(n, kVocabStep);
         gh.count = c.r.count; gh.Np = p.Np;
         gh.out = c.at<float>(p.acc); gh.ld_out = p.Kd; gh.splits = p.splits; gh.accumulate = x > 0;
-        gw.a = c.at<uint16_t>(p.ht); gw.a_plane = s.D * p.Np; gw.lda = p.Np;
-        gw.b = gt; gw.b_plane = p.Np * p.piece; gw.ldb = p.Np;
-        gw.m = s.D; gw.n = d_w ? n : 0;
-        gw.out = static_cast<char*>(d_w) + v0 * s.ld_w * (int64_t)size_of(s.dw); gw.ld_out = s.ld_w;
-        gw.out_dtype = s.dw; gw.accumulate = s.accumulate;
-        RUN(launch_vocab_grads(gh, gw, s.terms, s.g_terms, c.stream));
+        RUN(launch_vocab_grads(gh, product_w(c, v0, n, d_w), s.terms, s.g_terms, c.stream));
     }
-    if (d_h && s.N > 0)
-        RUN(launch_vocab_dh({c.r, c.at<float>(p.acc), p.splits, (int)p.Kd, s.io, d_h, s.ld_h}, c.stream));
+    if (d_h) RUN(launch_vocab_dh({c.r, c.at<float>(p.acc), p.splits, (int)p.Kd, s.io, d_h, s.ld_h}, c.stream));
     return SSM_OK;
 }
 

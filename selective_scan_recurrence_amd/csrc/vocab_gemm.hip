@@ -116,7 +116,7 @@ struct Tile {
     static constexpr int kStage = (BM + BN) * 128;
     // two stages; the logits at the ids pass through 64 x TN 16 values a wave
     static constexpr int kLds = 2 * kStage;
-    static_assert(NW * TN * 4096 <= kLds, "");
+    static_assert(NW * TN * 4096 <= kLds && TN % 4 == 0, "");
     static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;
 };
 using Big = Tile<8, 8>;
@@ -320,36 +320,52 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_fwd(VocabGemm p
         for (int j = 0; j < TN; j += 2) to[j / 2] = make_float4(top[j], sum[j], top[j + 1], sum[j + 1]);
     }
 
-    // the logits at the rows' ids: 64 of m at a time through LDS, a lane a row
-    constexpr int U = TM / 4;
-    bool any[U] = {};
+    // The logits at the rows' ids, 64 ids a row at a time: which of a lane's rows' ids
+    // are in the wave's vocabulary, as bits, then 64 of m at a time through LDS.
+    constexpr int U = TM / 4, X = TN / 4;
     const int left = p.m - l.mw;
-    for (int x = l.lane; x < TN * 16 && l.nw + x < n_rows; x += 64)
-        for (int k = 0; k < p.K; ++k) {
-            const int at = p.kid[k * p.Np + l.nw + x] - p.v0 - l.mw;
-#pragma unroll
-            for (int u = 0; u < U; ++u) any[u] |= at >= 64 * u && at < min(64 * u + 64, left);
-        }
-    __syncthreads();
     float* mine = reinterpret_cast<float*>(lds + l.wave * (TN * 4096));
+    __syncthreads();
+    for (int k0 = 0; k0 < p.K; k0 += 64) {
+        uint64_t hits[U][X] = {};
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (!__any(any[u])) continue;
+        for (int x = 0; x < X; ++x) {
+            const int n = min(l.nw + 64 * x + l.lane, n_rows - 1);
+            const int32_t* ids = p.kid + k0 * p.Np + n;
+            const int base = p.v0 + l.mw, some = min(64, p.K - k0);
+            const bool row = l.nw + 64 * x + l.lane < n_rows;
+#pragma unroll 8
+            for (int k = 0; k < some; ++k) {
+                const int id = ids[k * p.Np], at = id - base;
+                // an absent entry's id is negative, and may wrap around
+                const bool in = row && id >= base && at < left;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                *reinterpret_cast<f32x4*>(mine + (TN * l.i16 + j) * 64 + 4 * ((4 * l.q + s) ^ l.i16)) =
-                    take(acc[4 * u + s][j]);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        for (int x = l.lane; x < TN * 16 && l.nw + x < n_rows; x += 64)
-            for (int k = 0; k < p.K; ++k) {
-                const int64_t e = k * p.Np + l.nw + x;
-                const int at = p.kid[e] - p.v0 - l.mw - 64 * u;
-                if (at >= 0 && at < min(64, left - 64 * u))
-                    p.slog[e] = p.scale2 * mine[x * 64 + 4 * ((at >> 2) ^ (x / TN)) + (at & 3)];
+                for (int u = 0; u < U; ++u)
+                    if (in && at / 64 == u) hits[u][x] |= 1ull << k;
             }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            bool any = false;
+#pragma unroll
+            for (int x = 0; x < X; ++x) any |= hits[u][x] != 0;
+            if (!__any(any)) continue;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    *reinterpret_cast<f32x4*>(mine + (TN * l.i16 + j) * 64 + 4 * ((4 * l.q + s) ^ l.i16)) =
+                        take(acc[4 * u + s][j]);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+                for (uint64_t left_bits = hits[u][x]; left_bits; left_bits &= left_bits - 1) {
+                    const int64_t e = (int64_t)(k0 + __builtin_ctzll(left_bits)) * p.Np + l.nw + 64 * x + l.lane;
+                    const int at = p.kid[e] - p.v0 - l.mw - 64 * u, n = 64 * x + l.lane;
+                    p.slog[e] = p.scale2 * mine[n * 64 + 4 * ((at >> 2) ^ (n / TN)) + (at & 3)];
+                }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
     }
 }
 

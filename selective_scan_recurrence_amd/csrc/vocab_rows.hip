@@ -138,13 +138,11 @@ __global__ __launch_bounds__(256) void pack_rows(VocabPack p, int pieces, bool w
         __builtin_memcpy(__builtin_assume_aligned(p.out + n * p.plane + (int64_t)r * (8 * pieces) + c, 16), t[n], 16);
 }
 
-// a tile of 64 rows x 64 columns through LDS
-template <int TERMS>
-__global__ __launch_bounds__(256) void turn_rows(VocabPack p, bool wide) {
+// a tile of 64 rows x 64 columns through LDS; zero where a row is not there
+template <int TERMS, typename There>
+__device__ __forceinline__ void turn_tile(const VocabPack& p, int r0, int c0, int n, bool wide, There there) {
     __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
-    const int n = p.count ? min(p.n, *p.count) : p.n;
-    const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64, tid = threadIdx.x;
-    if (r0 >= n) return;
+    const int tid = threadIdx.x;
     uint16_t t[2][TERMS][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -153,7 +151,7 @@ __global__ __launch_bounds__(256) void turn_rows(VocabPack p, bool wide) {
         for (int x = 0; x < TERMS; ++x)
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[h][x][e] = 0;
-        if (r < n && c < p.width) load8<TERMS>(p, row_of(p, r), c, wide, t[h]);
+        if (r < n && c < p.width && there(r)) load8<TERMS>(p, row_of(p, r), c, wide, t[h]);
     }
 #pragma unroll
     for (int x = 0; x < TERMS; ++x) {
@@ -171,6 +169,12 @@ __global__ __launch_bounds__(256) void turn_rows(VocabPack p, bool wide) {
                     *reinterpret_cast<const u32x4*>(&tile[c][r]);
         }
     }
+}
+
+template <int TERMS>
+__global__ __launch_bounds__(256) void turn_rows(VocabPack p, bool wide) {
+    const int n = p.count ? min(p.n, *p.count) : p.n, r0 = blockIdx.x * 64;
+    if (r0 < n) turn_tile<TERMS>(p, r0, blockIdx.y * 64, n, wide, [](int) { return true; });
 }
 
 bool is_wide(const VocabPack& p) {
@@ -212,7 +216,14 @@ __global__ __launch_bounds__(256) void join_rows(VocabJoin j) {
     const int lane = threadIdx.x & 7;
     const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x / 8;
     if (i >= r.N) return;
-    const int c = r.pos[i];
+    int c;
+    if (r.pos) {
+        c = r.pos[i];
+    } else {
+        const int state = row_state(r, (int)i);
+        c = state < 0 ? state : (int)i;
+        if (state == kRowBad && j.err && j.last && lane == 0) atomicOr(j.err, (uint32_t)SSM_DEVERR_TARGET);
+    }
     if (c < 0) {
         if (!j.last) return;
         const float v = c == kRowBad ? __builtin_nanf("") : 0.0f;
@@ -259,22 +270,17 @@ __global__ __launch_bounds__(256) void join_rows(VocabJoin j) {
 
 // ---- the gradient's factors ---------------------------------------------------
 
-__global__ __launch_bounds__(256) void coef_target(VocabCoef f) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= *f.r.count) return;
-    const int i = f.r.rows[c];
+// of row i, which counts as row c
+__device__ __forceinline__ void target_factors(const VocabCoef& f, int i, int c) {
     const float d = f.scale * f.d_loss[i], a = d + (f.d_lse ? f.scale * f.d_lse[i] : 0.0f);
     f.lse2[c] = f.lse[i] * kLog2e;
     f.coef[c] = a;
     f.at[c] = a * fast_exp2(-f.loss[i] * kLog2e) - d;
 }
 
-// a wave a row
-__global__ __launch_bounds__(256) void coef_top(VocabCoef f) {
+// by a wave
+__device__ __forceinline__ void top_factors(const VocabCoef& f, int64_t i, int c, int lane) {
     const VocabRows& r = f.r;
-    const int c = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x & 63;
-    if (c >= *r.count) return;
-    const int64_t i = r.rows[c];
     const float d = f.scale * f.d_loss[i], off = top_offset(r, i, lane, 64);
     float mass = 1.0f;
     if (r.top_lse) {
@@ -295,6 +301,39 @@ __global__ __launch_bounds__(256) void coef_top(VocabCoef f) {
             if (ids[x] == ids[k]) p += fast_exp2(top2(r, i * r.K + x) - off);
         f.at[(int64_t)k * r.Np + c] = a * fast_exp2(f.logq[i * r.K + k] * kLog2e) - d * p;
     }
+}
+
+__global__ __launch_bounds__(256) void coef_target(VocabCoef f) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c < *f.r.count) target_factors(f, f.r.rows[c], c);
+}
+
+__global__ __launch_bounds__(256) void coef_top(VocabCoef f) {
+    const int c = blockIdx.x * 4 + threadIdx.x / 64;
+    if (c < *f.r.count) top_factors(f, f.r.rows[c], c, threadIdx.x & 63);
+}
+
+// The first 16 workgroups take the rows' factors, a wave a row; the others turn h,
+// 64 columns each.
+template <int TERMS>
+__global__ __launch_bounds__(256) void few_begin(VocabCoef f, VocabPack p, bool wide) {
+    const VocabRows& r = f.r;
+    const int tid = threadIdx.x;
+    if (blockIdx.x < kVocabFew / 4) {
+        const int i = blockIdx.x * 4 + tid / 64;
+        if (blockIdx.x == 0 && tid == 0) *r.count = r.N;
+        if (i >= r.N) return;
+        const int state = row_state(r, i);
+        if ((tid & 63) == 0) r.pos[i] = state < 0 ? state : i;
+        if (state < 0) return;
+        if (r.logit) top_factors(f, i, i, tid & 63);
+        else if ((tid & 63) == 0) target_factors(f, i, i);
+        return;
+    }
+    __shared__ int state[kVocabFew];
+    if (tid < kVocabFew) state[tid] = tid < r.N ? row_state(r, tid) : kRowOut;
+    __syncthreads();
+    turn_tile<TERMS>(p, 0, 64 * (blockIdx.x - kVocabFew / 4), r.N, wide, [&](int row) { return state[row] >= 0; });
 }
 
 template <int TERMS>
@@ -378,6 +417,13 @@ int launch_vocab_join(const VocabJoin& j, hipStream_t stream) {
 int launch_vocab_coef(const VocabCoef& c, hipStream_t stream) {
     if (!c.r.logit) coef_target<<<blocks(c.r.N, 256), 256, 0, stream>>>(c);
     else coef_top<<<blocks(c.r.N, 4), 256, 0, stream>>>(c);
+    return launched();
+}
+
+int launch_vocab_few_begin(const VocabCoef& c, const VocabPack& p, hipStream_t stream) {
+    const unsigned grid = kVocabFew / 4 + blocks(p.width, 64);
+    if (p.dtype == SSM_BF16) few_begin<1><<<grid, 256, 0, stream>>>(c, p, is_wide(p));
+    else few_begin<3><<<grid, 256, 0, stream>>>(c, p, is_wide(p));
     return launched();
 }
 
