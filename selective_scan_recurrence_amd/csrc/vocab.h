@@ -47,8 +47,6 @@ struct VocabPack {
     uint16_t* out;
     int64_t ld_rows, plane;
 };
-int launch_vocab_pack(const VocabPack& p, hipStream_t stream);
-int launch_vocab_turn(const VocabPack& p, hipStream_t stream);
 
 // The backward's factors of a row that counts: g_v = coef exp2(s2_v - lse2) and,
 // at entry k's id, q_k - p_k (entries with the same id hold the same sum).
@@ -59,7 +57,6 @@ struct VocabCoef {
     float *lse2, *coef;  // [Np]
     float *at;           // [K][Np]: g at entry k's id
 };
-int launch_vocab_coef(const VocabCoef& c, hipStream_t stream);
 
 struct VocabJoin {
     VocabRows r;
@@ -72,6 +69,14 @@ struct VocabJoin {
     uint32_t* err;       // for rows that are not listed
 };
 int launch_vocab_join(const VocabJoin& j, hipStream_t stream);
+
+// Of the kernels before a product, those that wait for the list of rows alone, in one
+// launch: any of packing h, turning h, the factors, and packing and turning W's piece.
+struct VocabBegin {
+    const VocabPack *pack_h = nullptr, *turn_h = nullptr, *pack_w = nullptr, *turn_w = nullptr;
+    const VocabCoef* coef = nullptr;
+};
+int launch_vocab_begin(const VocabBegin& b, int dtype, hipStream_t stream);
 
 // g at the entries' ids within the piece [v0, v0 + P).
 struct VocabPatch {
@@ -127,40 +132,66 @@ struct VocabFew {
     VocabRows r;
     const void *h, *w;
     int64_t ld_h, ld_w;
+    const uint16_t* hp;    // f32: h's terms [3][64][width rounded up to 64]
     float scale2;
     int v0, P;             // the piece
     float2* part;          // forward, a partial for every vocab_few_tile of the piece
     float* slog;
     const float *lse2, *coef, *at;  // backward, as VocabCoef
     uint16_t *g, *gt;
+    const uint16_t* ht;    // h turned
+    void* d_w;             // of the piece, row stride ld_w
+    int dw_dtype;
+    bool accumulate;
     float* acc;            // d_h: [splits][64][width rounded up to 64]
     int splits;
     bool first;            // the first piece: acc holds nothing yet
 };
-int vocab_few_tile(int64_t V, int terms);
+int vocab_few_tile(int64_t V, int N, int terms);
 int vocab_few_splits(int64_t V, int64_t D);
 int launch_vocab_few_logits(const VocabFew& p, bool backward, hipStream_t stream);
 int launch_vocab_few_d_h(const VocabFew& p, hipStream_t stream);
-// Before the backward: pos, count, the factors, and h turned, [terms][width][64], with
-// the rows that are left out zero.
-int launch_vocab_few_begin(const VocabCoef& c, const VocabPack& turned, hipStream_t stream);
+int launch_vocab_few_d_w(const VocabFew& p, hipStream_t stream);
+// Before the backward: pos, the factors, and h turned, [terms][width][64], with the rows
+// that are left out zero; in f32 also h's terms, packed.
+int launch_vocab_few_begin(const VocabCoef& c, const VocabPack& turned, const VocabPack& packed, hipStream_t stream);
 
-// v as bf16 terms.  One: v rounded.  Two: that, and the rest rounded (2^-17 of v is
-// left).  Three: v itself, each term what the ones before leave with the low half
-// cut off, so that no rounding passes the largest value.  An infinity or a NaN is
-// all in the first.
+// Stores a lane's V neighbouring values of a row of d_w; `left` of them are there
+template <typename E, int V>
+__device__ __forceinline__ void store_dw(E* to, float (&v)[V], int left, bool accumulate) {
+#pragma unroll
+    for (int r = 0; r < V; ++r)
+        if (accumulate && r < left) v[r] += to_f32(to[r]);
+    E w[V];
+#pragma unroll
+    for (int r = 0; r < V; ++r) store_io(&w[r], v[r]);
+    if (left >= V) __builtin_memcpy(to, w, sizeof w);
+    else
+#pragma unroll
+        for (int r = 0; r < V; ++r)
+            if (r < left) to[r] = w[r];
+}
+
+// v's next bf16 term, of TERMS in all; v keeps the rest.  One: v rounded.  Two: that,
+// and the rest rounded (2^-17 of v is left).  Three: v itself, each term what the ones
+// before leave with the low half cut off, so that no rounding passes the largest
+// value.  An infinity or a NaN is all in the first.
+template <int TERMS>
+__device__ __forceinline__ uint16_t next_term(float& v) {
+    if constexpr (TERMS < 3) {
+        const uint16_t t = bf16_rne(v);
+        v = fabsf(to_f32(t)) < __builtin_inff() ? v - to_f32(t) : 0.0f;
+        return t;
+    } else {
+        const uint16_t t = v != v ? 0x7fc0 : __float_as_uint(v) >> 16;
+        v = fabsf(v) < __builtin_inff() ? v - to_f32(t) : 0.0f;
+        return t;
+    }
+}
 template <int TERMS>
 __device__ __forceinline__ void bf16_terms(float v, uint16_t (&t)[TERMS]) {
-    if constexpr (TERMS < 3) {
-        t[0] = bf16_rne(v);
-        if constexpr (TERMS == 2) t[1] = fabsf(to_f32(t[0])) < __builtin_inff() ? bf16_rne(v - to_f32(t[0])) : 0;
-    } else {
-        const uint32_t bits = __float_as_uint(v);
-        t[0] = v != v ? 0x7fc0 : bits >> 16;
-        const float left = fabsf(v) < __builtin_inff() ? v - __uint_as_float(bits & 0xffff0000u) : 0.0f;
-        t[1] = __float_as_uint(left) >> 16;
-        t[2] = __float_as_uint(left - __uint_as_float(__float_as_uint(left) & 0xffff0000u)) >> 16;
-    }
+#pragma unroll
+    for (int n = 0; n < TERMS; ++n) t[n] = next_term<TERMS>(v);
 }
 
 }  // namespace ssm

@@ -104,7 +104,7 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     p.rows = take(p.Np * 4);
     p.pos = take(p.Np * 4);
     p.kid = take(p.Np * s.K * 4);
-    p.h = p.few ? 0 : take(T * p.Np * p.Kd * 2);
+    p.h = p.few && T == 1 ? 0 : take(T * p.Np * p.Kd * 2);
     p.w = packed ? take(T * p.piece * p.Kd * 2) : 0;
     if (backward) {
         p.ht = take(T * s.D * p.Np * 2);
@@ -174,11 +174,21 @@ VocabPack pack_w(const Call& c, int64_t v0, int n, size_t to, int64_t plane) {
     return {c.w, c.s.ld_w, c.s.io, c.s.D, n, v0, nullptr, nullptr, c.at<uint16_t>(to), c.p.piece, plane};
 }
 
-// the operands of a piece's logits; W's rows where they are, or packed
-int logits(const Call& c, int64_t v0, int n, VocabGemm* out) {
+// What comes before a piece's logits: W's rows packed unless they are read where they
+// are, and turned for d_h; before the first piece also `first`.
+int begin_piece(const Call& c, int x, int64_t v0, int n, bool turn, const VocabBegin& first) {
+    VocabBegin b = x == 0 ? first : VocabBegin();
+    const VocabPack packed = pack_w(c, v0, n, c.p.w, c.p.piece * c.p.Kd);
+    const VocabPack turned = pack_w(c, v0, n, c.p.wt, c.s.D * c.p.piece);
+    if (c.p.packed) b.pack_w = &packed;
+    if (turn) b.turn_w = &turned;
+    return launch_vocab_begin(b, c.s.io, c.stream);
+}
+
+// the operands of a piece's logits
+VocabGemm logits(const Call& c, int64_t v0, int n) {
     VocabGemm g = {};
     if (c.p.packed) {
-        RUN(launch_vocab_pack(pack_w(c, v0, n, c.p.w, c.p.piece * c.p.Kd), c.stream));
         g.a = c.at<uint16_t>(c.p.w);
         g.a_plane = c.p.piece * c.p.Kd;
         g.lda = c.p.Kd;
@@ -195,8 +205,7 @@ int logits(const Call& c, int64_t v0, int n, VocabGemm* out) {
     g.scale2 = c.s.scale * kLog2e;
     g.v0 = (int)v0; g.K = c.s.K; g.P = (int)c.p.piece;
     g.kid = c.r.kid;
-    *out = g;
-    return SSM_OK;
+    return g;
 }
 
 int forward_few(const Call& c, float* loss, float* lse, float* logq, uint32_t* err);
@@ -205,12 +214,14 @@ int forward(const Call& c, float* loss, float* lse, float* logq, uint32_t* err) 
     const Plan& p = c.p;
     if (p.few) return forward_few(c, loss, lse, logq, err);
     RUN(launch_vocab_rows(c.r, err, c.stream));
-    RUN(launch_vocab_pack(pack_h(c, p.h, p.Np * p.Kd), c.stream));
+    const VocabPack packed = pack_h(c, p.h, p.Np * p.Kd);
+    VocabBegin first;
+    first.pack_h = &packed;
     for (int x = 0; x < p.pieces; ++x) {
         const int64_t v0 = x * p.piece;
         const int n = (int)(c.s.V - v0 < p.piece ? c.s.V - v0 : p.piece);
-        VocabGemm g;
-        RUN(logits(c, v0, n, &g));
+        RUN(begin_piece(c, x, v0, n, false, first));
+        VocabGemm g = logits(c, v0, n);
         g.part = c.at<float2>(p.part);
         g.slog = c.at<float>(p.slog);
         RUN(launch_vocab_logits_fwd(g, c.s.terms, c.stream));
@@ -227,7 +238,15 @@ VocabFew few_of(const Call& c) {
     f.ld_h = c.s.ld_h; f.ld_w = c.s.ld_w;
     f.scale2 = c.s.scale * kLog2e;
     f.P = (int)c.p.piece;
+    if (c.s.terms == 3) f.hp = c.at<uint16_t>(c.p.h);
     return f;
+}
+
+// h where rows keep their places
+VocabPack placed_h(const Call& c, size_t to, int64_t plane) {
+    VocabPack p = pack_h(c, to, plane);
+    p.rows = p.count = nullptr;
+    return p;
 }
 
 int forward_few(const Call& c, float* loss, float* lse, float* logq, uint32_t* err) {
@@ -236,7 +255,13 @@ int forward_few(const Call& c, float* loss, float* lse, float* logq, uint32_t* e
     f.r.pos = nullptr;
     f.part = c.at<float2>(p.part);
     f.slog = c.at<float>(p.slog);
-    const int tile = vocab_few_tile(c.s.V, c.s.terms);
+    const int tile = vocab_few_tile(c.s.V, c.s.N, c.s.terms);
+    if (c.s.terms == 3) {
+        const VocabPack packed = placed_h(c, p.h, p.Np * p.Kd);
+        VocabBegin b;
+        b.pack_h = &packed;
+        RUN(launch_vocab_begin(b, c.s.io, c.stream));
+    }
     for (int x = 0; x < p.pieces; ++x) {
         f.v0 = (int)(x * p.piece);
         const int n = c.s.V - f.v0 < f.P ? c.s.V - f.v0 : f.P;
@@ -268,12 +293,12 @@ VocabCoef factors(const Call& c, const float* logq, const float* loss, const flo
 int backward_few(const Call& c, const VocabCoef& f, void* d_h, void* d_w) {
     const Plan& p = c.p;
     const VocabShape& s = c.s;
-    VocabPack turned = pack_h(c, p.ht, s.D * p.Np);
-    turned.rows = turned.count = nullptr;
-    RUN(launch_vocab_few_begin(f, turned, c.stream));
+    RUN(launch_vocab_few_begin(f, placed_h(c, p.ht, s.D * p.Np), placed_h(c, p.h, p.Np * p.Kd), c.stream));
     VocabFew few = few_of(c);
     few.lse2 = f.lse2; few.coef = f.coef; few.at = f.at;
     few.g = c.at<uint16_t>(p.g); few.gt = c.at<uint16_t>(p.gt);
+    few.ht = c.at<uint16_t>(p.ht);
+    few.dw_dtype = s.dw; few.accumulate = s.accumulate;
     few.acc = c.at<float>(p.acc); few.splits = p.splits;
     for (int x = 0; x < p.pieces; ++x) {
         few.v0 = (int)(x * p.piece);
@@ -281,11 +306,8 @@ int backward_few(const Call& c, const VocabCoef& f, void* d_h, void* d_w) {
         if (s.N > 0) RUN(launch_vocab_few_logits(few, true, c.stream));
         if (d_h && s.N > 0) RUN(launch_vocab_few_d_h(few, c.stream));
         if (d_w) {
-            VocabGemm none = {};
-            none.count = c.r.count;
-            none.splits = 1;
-            RUN(launch_vocab_grads(none, product_w(c, few.v0, s.V - few.v0 < few.P ? s.V - few.v0 : few.P, d_w),
-                                   s.terms, s.g_terms, c.stream));
+            few.d_w = static_cast<char*>(d_w) + few.v0 * s.ld_w * (int64_t)size_of(s.dw);
+            RUN(launch_vocab_few_d_w(few, c.stream));
         }
     }
     if (d_h && s.N > 0)
@@ -301,22 +323,23 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
     const VocabCoef f = factors(c, logq, loss, lse, d_loss, d_lse);
     if (p.few) return backward_few(c, f, d_h, d_w);
     RUN(launch_vocab_rows(c.r, nullptr, c.stream));
-    RUN(launch_vocab_pack(pack_h(c, p.h, p.Np * p.Kd), c.stream));
-    if (d_w) RUN(launch_vocab_turn(pack_h(c, p.ht, s.D * p.Np), c.stream));
-    RUN(launch_vocab_coef(f, c.stream));
+    const VocabPack packed = pack_h(c, p.h, p.Np * p.Kd), turned = pack_h(c, p.ht, s.D * p.Np);
+    VocabBegin first;
+    first.pack_h = &packed;
+    if (d_w) first.turn_h = &turned;
+    first.coef = &f;
     uint16_t *g = c.at<uint16_t>(p.g), *gt = c.at<uint16_t>(p.gt);
     for (int x = 0; x < p.pieces; ++x) {
         const int64_t v0 = x * p.piece;
         const int n = (int)(s.V - v0 < p.piece ? s.V - v0 : p.piece);
-        VocabGemm l;
-        RUN(logits(c, v0, n, &l));
+        RUN(begin_piece(c, x, v0, n, d_h != nullptr, first));
+        VocabGemm l = logits(c, v0, n);
         l.lse2 = f.lse2;
         l.coef = f.coef;
         l.g = g;
         l.gt = gt;
         RUN(launch_vocab_logits_bwd(l, s.terms, s.g_terms, c.stream));
         RUN(launch_vocab_patch({c.r, f.at, (int)v0, (int)p.piece, s.g_terms, g, gt}, c.stream));
-        if (d_h) RUN(launch_vocab_turn(pack_w(c, v0, n, p.wt, s.D * p.piece), c.stream));
         VocabGemm gh = {};
         gh.a = c.at<uint16_t>(p.wt); gh.a_plane = s.D * p.piece; gh.lda = p.piece;
         gh.b = g; gh.b_plane = p.Np * p.piece; gh.ldb = p.piece;

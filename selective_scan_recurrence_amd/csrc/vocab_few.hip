@@ -70,6 +70,33 @@ struct Raw {
     }
 };
 
+// The same sixteen values of h: as they lie, or (f32) of its terms in the workspace,
+// which every workgroup would have to form again.
+template <typename E>
+struct Rows {
+    Raw<E> x;
+    __device__ __forceinline__ void load(const VocabFew& p, int n, int k) {
+        x.load(static_cast<const E*>(p.h) + (int64_t)n * p.ld_h, k, p.r.D);
+    }
+    __device__ __forceinline__ void operand(int h, u32x4 (&f)[1]) const { x.operand(h, f); }
+};
+template <>
+struct Rows<float> {
+    u32x4 x[2][3];
+    __device__ __forceinline__ void load(const VocabFew& p, int n, int k) {
+        const int64_t Kd = (p.r.D + 63) / 64 * 64;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+                x[h][t] = *reinterpret_cast<const u32x4*>(p.hp + (t * p.r.Np + n) * Kd + k + 8 * h);
+    }
+    __device__ __forceinline__ void operand(int h, u32x4 (&f)[3]) const {
+#pragma unroll
+        for (int t = 0; t < 3; ++t) f[t] = x[h][t];
+    }
+};
+
 // ---- the logits -----------------------------------------------------------------
 // A workgroup of 8 waves owns 16 MT of the vocabulary and all rows (16 NT of them).
 // The waves share out the width in chunks of 64, a lane reading 16 neighbouring
@@ -83,12 +110,9 @@ __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4, i16 = lane & 15;
     const int m0 = blockIdx.x * M;  // in the piece
     const E* w[MT];
-    const E* h[NT];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
         w[t] = static_cast<const E*>(p.w) + (int64_t)min(p.v0 + m0 + 16 * t + i16, r.V - 1) * p.ld_w;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) h[j] = static_cast<const E*>(p.h) + (int64_t)min(16 * j + i16, r.N - 1) * p.ld_h;
     f32x4 acc[MT][NT];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -100,9 +124,10 @@ __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) next[t].load(w[t], k, r.D);
     for (; k - 16 * q < r.D; k += 512) {
-        Raw<E> cur[MT], x[NT];
+        Raw<E> cur[MT];
+        Rows<E> x[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) x[j].load(h[j], k, r.D);
+        for (int j = 0; j < NT; ++j) x[j].load(p, min(16 * j + i16, r.N - 1), k);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             cur[t] = next[t];
@@ -230,14 +255,12 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
         for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
     struct Step {
         uint32_t w[8][kWords];
-        u32x4 g[NT][GT];
     } next;
     auto load = [&](Step& s, int step) {
-        const int v = 32 * step + 8 * q;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             // g is zero past the vocabulary
-            const E* row = w + (int64_t)min(v + j, rows - 1) * p.ld_w;
+            const E* row = w + (int64_t)min(32 * step + 8 * q + j, rows - 1) * p.ld_w;
             if (col + 4 <= r.D) {
                 __builtin_memcpy(s.w[j], row + col, sizeof s.w[j]);
             } else {
@@ -247,18 +270,20 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
                 __builtin_memcpy(s.w[j], x, sizeof x);
             }
         }
+    };
+    if (begin < end) load(next, begin);
+    for (int s = begin; s < end; ++s) {
+        const Step cur = next;
+        u32x4 g[NT][GT];
+        const int v = 32 * s + 8 * q;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int t = 0; t < GT; ++t) {
                 // written to the end of a workgroup's 16 MT of the vocabulary
                 const u32x4 x = *reinterpret_cast<const u32x4*>(p.g + t * plane + (int64_t)(16 * j + i16) * p.P + v);
-                s.g[j][t] = v < rows ? x : u32x4{0, 0, 0, 0};
+                g[j][t] = v < rows ? x : u32x4{0, 0, 0, 0};
             }
-    };
-    if (begin < end) load(next, begin);
-    for (int s = begin; s < end; ++s) {
-        const Step cur = next;
         if (s + 1 < end) load(next, s + 1);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -271,15 +296,15 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
             } else {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    uint16_t u[3], v[3];
+                    uint16_t u[3], y[3];
                     bf16_terms<3>(__uint_as_float(cur.w[2 * x][t]), u);
-                    bf16_terms<3>(__uint_as_float(cur.w[2 * x + 1][t]), v);
+                    bf16_terms<3>(__uint_as_float(cur.w[2 * x + 1][t]), y);
 #pragma unroll
-                    for (int n = 0; n < 3; ++n) a[n][x] = u[n] | (uint32_t)v[n] << 16;
+                    for (int n = 0; n < 3; ++n) a[n][x] = u[n] | (uint32_t)y[n] << 16;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < NT; ++j) acc[t][j] = products<T, GT>(a, cur.g[j], acc[t][j]);
+            for (int j = 0; j < NT; ++j) acc[t][j] = products<T, GT>(a, g[j], acc[t][j]);
         }
     }
     // tile t's row 4 q + x is column 4 (4 q + x) + t: 16 neighbours a lane
@@ -295,18 +320,79 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
         }
 }
 
+// ---- d_w ------------------------------------------------------------------------
+// A wave owns 64 columns and 128 of the vocabulary, 16 of it a step; the sum over the
+// rows is one or two MFMAs long, and d_w's bytes bound it.  Tiles take the columns in
+// the order of the big products' rows (S neighbouring groups of 4 a lane).
+template <int T, int KS, int S>
+__global__ __launch_bounds__(256, 2) void few_d_w(VocabFew p) {
+    constexpr int GT = T == 3 ? 3 : 2, kSteps = 8;
+    const VocabRows& r = p.r;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, i16 = lane & 15;
+    const int d0 = 256 * blockIdx.x + 64 * wave, rows = min(p.P, r.V - p.v0);
+    if (d0 >= r.D) return;
+    u32x4 a[4][KS][T];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int n = 0; n < T; ++n) {
+                const int d = min(d0 + 16 * S * (t / S) + 4 * S * (i16 >> 2) + 4 * (t % S) + (i16 & 3), r.D - 1);
+                a[t][k][n] = *reinterpret_cast<const u32x4*>(p.ht + ((int64_t)n * r.D + d) * r.Np + 32 * k + 8 * q);
+            }
+    const int64_t plane = (int64_t)r.Np * p.P;
+    u32x4 next[KS][GT];
+    auto load = [&](int v) {  // gt has a piece's rows, whole tiles of them
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int n = 0; n < GT; ++n)
+                next[k][n] = r.N == 0 ? u32x4{0, 0, 0, 0}  // without rows nothing wrote it
+                                      : *reinterpret_cast<const u32x4*>(p.gt + n * plane + (int64_t)(v + i16) * r.Np +
+                                                                        32 * k + 8 * q);
+    };
+    const int begin = 16 * kSteps * blockIdx.y, end = min(begin + 16 * kSteps, rows);
+    load(begin);
+    for (int v = begin; v < end; v += 16) {
+        u32x4 b[KS][GT];
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int n = 0; n < GT; ++n) b[k][n] = next[k][n];
+        if (v + 16 < end) load(v + 16);
+#pragma unroll
+        for (int t = 0; t < 4; t += S) {
+            float c[4 * S];
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) acc = products<T, GT>(a[t + s][k], b[k], acc);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) c[4 * s + x] = acc[x];
+            }
+            const int d = d0 + 16 * t + 4 * S * q, left = r.D - d;
+            if (v + i16 >= rows || left <= 0) continue;
+            const int64_t at = (int64_t)(v + i16) * p.ld_w + d;
+            if (p.dw_dtype == SSM_F32) store_dw(static_cast<float*>(p.d_w) + at, c, left, p.accumulate);
+            else store_dw(static_cast<bf16_t*>(p.d_w) + at, c, left, p.accumulate);
+        }
+    }
+}
+
 template <typename E, int MT, bool BWD>
 int launch_logits(const VocabFew& p, hipStream_t stream) {
     const int M = 16 * MT, v = p.r.V - p.v0 < p.P ? p.r.V - p.v0 : p.P, grid = (v + M - 1) / M;
     if (p.r.N <= 16) few_logits<E, MT, 1, BWD><<<grid, 512, 0, stream>>>(p);
     else if (p.r.N <= 32) few_logits<E, MT, 2, BWD><<<grid, 512, 0, stream>>>(p);
-    else few_logits<E, MT, 4, BWD><<<grid, 512, 0, stream>>>(p);
+    else if constexpr (MT < 4) few_logits<E, MT, 4, BWD><<<grid, 512, 0, stream>>>(p);  // 64 logits a workgroup are for up to 32 rows
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
 template <bool BWD>
 int launch_logits(const VocabFew& p, hipStream_t stream) {
-    const int mt = vocab_few_tile(p.r.V, p.r.terms) / 16;
+    const int mt = vocab_few_tile(p.r.V, p.r.N, p.r.terms) / 16;
     if (p.r.terms == 3)
         return mt == 1 ? launch_logits<float, 1, BWD>(p, stream) : launch_logits<float, 2, BWD>(p, stream);
     return mt == 1   ? launch_logits<bf16_t, 1, BWD>(p, stream)
@@ -318,18 +404,20 @@ int launch_logits(const VocabFew& p, hipStream_t stream) {
 
 // Of the vocabulary a workgroup: the more, the fewer times h is read, as long as
 // there is more than one workgroup a compute unit.
-int vocab_few_tile(int64_t V, int terms) {
-    const int most = terms == 3 ? 32 : 64;
+int vocab_few_tile(int64_t V, int N, int terms) {
+    const int most = terms == 3 || N > 32 ? 32 : 64;
     int m = 16;
     while (m < most && V / (2 * m) >= 400) m *= 2;
     return m;
 }
 
+// Parts of d_h's sum over the vocabulary, of 4 steps at least: two workgroups a compute
+// unit, and not many more, since every part is written and read again.
 int vocab_few_splits(int64_t V, int64_t D) {
-    const int64_t columns = (D + 255) / 256, most = (V + 255) / 256;
-    int64_t n = 768 / columns;
+    const int64_t columns = (D + 255) / 256, most = (V + 127) / 128;
+    int64_t n = 640 / columns;
     if (n > most) n = most;
-    return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+    return (int)(n < 1 ? 1 : n > 256 ? 256 : n);
 }
 
 int launch_vocab_few_logits(const VocabFew& p, bool backward, hipStream_t stream) {
@@ -347,6 +435,23 @@ int launch_vocab_few_d_h(const VocabFew& p, hipStream_t stream) {
         if (nt == 1) few_d_h<bf16_t, 1><<<grid, 256, 0, stream>>>(p);
         else if (nt == 2) few_d_h<bf16_t, 2><<<grid, 256, 0, stream>>>(p);
         else few_d_h<bf16_t, 4><<<grid, 256, 0, stream>>>(p);
+    }
+    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int launch_vocab_few_d_w(const VocabFew& p, hipStream_t stream) {
+    const int rows = p.r.V - p.v0 < p.P ? p.r.V - p.v0 : p.P;
+    const dim3 grid((p.r.D + 255) / 256, (rows + 127) / 128);
+    const bool two = p.r.N > 32, f32 = p.dw_dtype == SSM_F32;
+    if (p.r.terms == 3) {
+        if (two) few_d_w<3, 2, 1><<<grid, 256, 0, stream>>>(p);
+        else few_d_w<3, 1, 1><<<grid, 256, 0, stream>>>(p);
+    } else if (f32) {
+        if (two) few_d_w<1, 2, 1><<<grid, 256, 0, stream>>>(p);
+        else few_d_w<1, 1, 1><<<grid, 256, 0, stream>>>(p);
+    } else {
+        if (two) few_d_w<1, 2, 2><<<grid, 256, 0, stream>>>(p);
+        else few_d_w<1, 1, 2><<<grid, 256, 0, stream>>>(p);
     }
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }

@@ -13,11 +13,13 @@
 // steps of 64: 128-byte rows go from memory to LDS past the registers, into one of
 // two buffers while the other is multiplied.  LDS holds the rows in the order of
 // MFMA tiles, row i (of 16) of tile t at 16 t + i, its 16-byte piece c at
-// c ^ (i % 8): a read of operands then meets no bank twice.  Tile t of a wave's
-// rows of A takes rows 64 (t / 4) + 16 (i / 4) + 4 (t % 4) + i % 4, and tile j of
-// its TN tiles of B the rows TN i + j: a lane (q = lane / 16, i = lane % 16) ends
-// with 16 neighbouring m (from 16 q) and TN neighbouring n (from TN i), so that
-// both orders leave in stores of 8 and 16 bytes.
+// c ^ (i % 8): a read of operands then meets no bank twice.  Which row of A is row i
+// of tile t is free: S tiles share 16 S rows, so that a lane (q = lane / 16, i = lane
+// % 16) ends with 4 S neighbouring m from 4 S q.  S = 2 where they leave in bf16, 1
+// in f32: the 4 lanes of a row of out then store 64 neighbouring bytes (with 16 m a
+// lane, which leave in two stores of every second 16 bytes, the backward's logits of
+// 16384 x 16384 rows, width 2560, took 1340 us instead of 1130).  Tile j of a wave's TN
+// tiles of B takes the rows TN i + j: TN neighbouring n a lane for g's other order.
 //
 // The big tile has one wave a SIMD with 64 accumulators of 4 registers each, a
 // quarter fewer bytes from LDS than eight waves of 128 x 64.  That counts because
@@ -122,8 +124,14 @@ struct Tile {
 using Big = Tile<8, 8>;
 using Small = Tile<4, 4>;
 
+// Row i of tile t among a wave's rows of A.
+template <int S>
+__device__ __forceinline__ constexpr int row_of_a(int t, int i) {
+    return 16 * S * (t / S) + 4 * S * (i >> 2) + 4 * (t % S) + (i & 3);
+}
+
 // acc = A[m0 ..] B[n0 ..]^T over steps [s0, s1) of every run.
-template <class T, int RUNS>
+template <class T, int RUNS, int S>
 __device__ __forceinline__ void product(const VocabGemm& p, int m0, int n0, int n_rows, int s0, int s1, uint8_t* lds,
                                         f32x4 (&acc)[T::TM][T::TN]) {
     constexpr int TM = T::TM, TN = T::TN, LA = T::LA, LB = T::LB, NW = T::NW, kStage = T::kStage;
@@ -136,8 +144,7 @@ __device__ __forceinline__ void product(const VocabGemm& p, int m0, int n0, int 
 #pragma unroll
     for (int x = 0; x < LA; ++x) {
         const int l = 8 * (wave + NW * x) + lane / 8, t = l / 16, i = l % 16;
-        const int row = 64 * (t / 4) + 16 * (i >> 2) + 4 * (t % 4) + (i & 3);
-        at_a[x] = (uint32_t)min(row, p.m - 1 - m0) * (uint32_t)(2 * p.lda) + 16 * ((lane & 7) ^ (i & 7));
+        at_a[x] = (uint32_t)min(row_of_a<S>(t, i), p.m - 1 - m0) * (uint32_t)(2 * p.lda) + 16 * ((lane & 7) ^ (i & 7));
     }
 #pragma unroll
     for (int x = 0; x < LB; ++x) {
@@ -236,10 +243,10 @@ __device__ __forceinline__ void product(const VocabGemm& p, int m0, int n0, int 
     settle(acc);
 }
 
-// Where a lane's values lie: acc[t][j][r] is m = mb + 64 (t / 4) + 4 (t % 4) + r,
-// n = nb + j.
-template <class T>
+// Where a lane's values lie: acc[t][j][r] is m = mb + m_of(t) + r, n = nb + j.
+template <class T, int S>
 struct Lane {
+    static __device__ __forceinline__ constexpr int m_of(int t) { return 16 * S * (t / S) + 4 * (t % S); }
     int lane, wave, q, i16, mw, mb, nw, nb;
     __device__ __forceinline__ Lane(int m0, int n0) {
         lane = threadIdx.x & 63;
@@ -247,12 +254,11 @@ struct Lane {
         q = lane >> 4;
         i16 = lane & 15;
         mw = m0 + wave / T::WN * T::TM * 16;
-        mb = mw + 16 * q;
+        mb = mw + 4 * S * q;
         nw = n0 + wave % T::WN * T::TN * 16;
         nb = nw + T::TN * i16;
     }
 };
-__device__ __forceinline__ constexpr int m_of(int t) { return 64 * (t / 4) + 4 * (t % 4); }
 
 template <class T, int RUNS>
 __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_fwd(VocabGemm p) {
@@ -267,13 +273,13 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_fwd(VocabGemm p
     m0 *= T::BM;
     n0 *= T::BN;
     f32x4 acc[TM][TN];
-    product<T, RUNS>(p, m0, n0, n_rows, 0, p.k / kVocabStep, lds, acc);
-    const Lane<T> l(m0, n0);
+    product<T, RUNS, 1>(p, m0, n0, n_rows, 0, p.k / kVocabStep, lds, acc);
+    const Lane<T, 1> l(m0, n0);
 
     // a row's largest logit and sum of exponentials over the wave's vocabulary
     float top[TN], sum[TN];
     auto statistics = [&](auto whole) {
-        auto there = [&](int t, int r) { return whole.value || l.mb + m_of(t) + r < p.m; };
+        auto there = [&](int t, int r) { return whole.value || l.mb + l.m_of(t) + r < p.m; };
         auto largest = [&](auto up) {
             const float sign = up.value ? 1.0f : -1.0f;
 #pragma unroll
@@ -354,7 +360,7 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_fwd(VocabGemm p
             for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    *reinterpret_cast<f32x4*>(mine + (TN * l.i16 + j) * 64 + 4 * ((4 * l.q + s) ^ l.i16)) =
+                    *reinterpret_cast<f32x4*>(mine + (TN * l.i16 + j) * 64 + 4 * ((4 * s + l.q) ^ l.i16)) =
                         take(acc[4 * u + s][j]);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
@@ -383,49 +389,52 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_bwd(VocabGemm p
     m0 *= T::BM;
     n0 *= T::BN;
     f32x4 acc[TM][TN];
-    product<T, RUNS>(p, m0, n0, n_rows, 0, p.k / kVocabStep, lds, acc);
-    const Lane<T> l(m0, n0);
+    product<T, RUNS, 2>(p, m0, n0, n_rows, 0, p.k / kVocabStep, lds, acc);
+    const Lane<T, 2> l(m0, n0);
 
     float lse2[TN], coef[TN];
     __builtin_memcpy(lse2, p.lse2 + l.nb, sizeof lse2);
     __builtin_memcpy(coef, p.coef + l.nb, sizeof coef);
     const int64_t plane = p.Np * p.P;
-    // two tiles, 8 neighbouring m, at a time (one in f32, for its registers); zero
-    // past the vocabulary and the rows
-    constexpr int S = GT == 3 ? 1 : 2;
+    // two tiles, 8 neighbouring m, at a time; zero past the vocabulary and the rows
     auto store = [&](int t0, auto whole) {
-        uint16_t g[S][TN][4][GT];
+        float v[2][TN][4];
 #pragma unroll
-        for (int t = 0; t < S; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const f32x4 c = take(acc[t0 + t][j]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const bool there = whole.value || (l.nb + j < n_rows && l.mb + m_of(t0 + t) + r < p.m);
-                    const float v = coef[j] * fast_exp2(fmaf(c[r], p.scale2, -lse2[j]));
-                    bf16_terms<GT>(there ? v : 0.0f, g[t][j][r]);
+                    const bool there = whole.value || (l.nb + j < n_rows && l.mb + l.m_of(t0 + t) + r < p.m);
+                    const float x = coef[j] * fast_exp2(fmaf(c[r], p.scale2, -lse2[j]));
+                    v[t][j][r] = there ? x : 0.0f;
                 }
             }
-        const int m = l.mb + m_of(t0);
+        const int m = l.mb + l.m_of(t0);
 #pragma unroll
         for (int n = 0; n < GT; ++n) {
+            uint16_t g[2][TN][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) g[t][j][r] = next_term<GT>(v[t][j][r]);
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                uint32_t w[2 * S];
+                u32x4 w;
 #pragma unroll
-                for (int x = 0; x < 2 * S; ++x)
-                    w[x] = g[x / 2][j][x % 2 * 2][n] | (uint32_t)g[x / 2][j][x % 2 * 2 + 1][n] << 16;
-                __builtin_memcpy(__builtin_assume_aligned(p.g + n * plane + (int64_t)(l.nb + j) * p.P + m, 8 * S), w,
-                                 sizeof w);
+                for (int x = 0; x < 4; ++x) w[x] = g[x / 2][j][x % 2 * 2] | (uint32_t)g[x / 2][j][x % 2 * 2 + 1] << 16;
+                *reinterpret_cast<u32x4*>(p.g + n * plane + (int64_t)(l.nb + j) * p.P + m) = w;
             }
 #pragma unroll
-            for (int t = 0; t < S; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     uint32_t w[TN / 2];
 #pragma unroll
-                    for (int j = 0; j < TN; j += 2) w[j / 2] = g[t][j][r][n] | (uint32_t)g[t][j + 1][r][n] << 16;
+                    for (int j = 0; j < TN; j += 2) w[j / 2] = g[t][j][r] | (uint32_t)g[t][j + 1][r] << 16;
                     __builtin_memcpy(__builtin_assume_aligned(
                         p.gt + n * plane + (int64_t)(m + 4 * t + r) * p.Np + l.nb, 2 * TN), w, sizeof w);
                 }
@@ -433,7 +442,7 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_bwd(VocabGemm p
     };
     const bool whole = l.mw + TM * 16 <= p.m && l.nw + TN * 16 <= n_rows;
 #pragma unroll
-    for (int t = 0; t < TM; t += S)
+    for (int t = 0; t < TM; t += 2)
         if (whole) store(t, yes);
         else store(t, no);
 }
@@ -445,54 +454,46 @@ __device__ __forceinline__ void tile_d_h(const VocabGemm& p, int n_rows, const P
     const int tiles = place.mt * place.nt, split = id / tiles, all = p.k / kVocabStep;
     place.of(id - split * tiles, &m0, &n0);
     f32x4 acc[TM][TN];
-    product<T, RUNS>(p, m0 *= T::BM, n0 *= T::BN, n_rows, (int)((int64_t)all * split / p.splits),
-                     (int)((int64_t)all * (split + 1) / p.splits), lds, acc);
-    const Lane<T> l(m0, n0);
+    product<T, RUNS, 1>(p, m0 *= T::BM, n0 *= T::BN, n_rows, (int)((int64_t)all * split / p.splits),
+                        (int)((int64_t)all * (split + 1) / p.splits), lds, acc);
+    const Lane<T, 1> l(m0, n0);
     float* out = static_cast<float*>(p.out) + split * p.Np * p.ld_out;
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int t = 0; t < TM; ++t) {
-            const int m = l.mb + m_of(t);
+            const int m = l.mb + l.m_of(t);
             if (l.nb + j >= n_rows || m >= p.ld_out) continue;  // ld_out: m's padded end
             f32x4* to = reinterpret_cast<f32x4*>(out + (int64_t)(l.nb + j) * p.ld_out + m);
-            *to = p.accumulate ? *to + acc[t][j] : acc[t][j];
+            const f32x4 v = take(acc[t][j]);
+            *to = p.accumulate ? *to + v : v;
         }
-}
-
-// a lane's values m .. m + 3 of a row of d_w; `left` of them are there
-template <typename E>
-__device__ __forceinline__ void store_dw(E* to, f32x4 v, int left, bool accumulate) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        if (accumulate && r < left) v[r] += to_f32(to[r]);
-    E w[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) store_io(&w[r], v[r]);
-    if (left >= 4) __builtin_memcpy(to, w, sizeof w);
-    else
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r < left) to[r] = w[r];
 }
 
 template <class T, int RUNS>
 __device__ __forceinline__ void tile_d_w(const VocabGemm& p, int count, const Place& place, int id, uint8_t* lds) {
-    constexpr int TM = T::TM, TN = T::TN;
+    constexpr int TM = T::TM, TN = T::TN, S = RUNS == 6 ? 1 : 2;
     int m0, n0;
     place.of(id, &m0, &n0);
     f32x4 acc[TM][TN];
-    product<T, RUNS>(p, m0 *= T::BM, n0 *= T::BN, p.n, 0, (count + kVocabStep - 1) / kVocabStep, lds, acc);
-    const Lane<T> l(m0, n0);
+    product<T, RUNS, S>(p, m0 *= T::BM, n0 *= T::BN, p.n, 0, (count + kVocabStep - 1) / kVocabStep, lds, acc);
+    const Lane<T, S> l(m0, n0);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int t = 0; t < TM; ++t) {
-            const int m = l.mb + m_of(t), left = p.m - m;
+        for (int t = 0; t < TM; t += S) {
+            const int m = l.mb + l.m_of(t), left = p.m - m;
             if (l.nb + j >= p.n || left <= 0) continue;
+            float v[4 * S];
+#pragma unroll
+            for (int x = 0; x < S; ++x) {
+                const f32x4 c = take(acc[t + x][j]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[4 * x + r] = c[r];
+            }
             const int64_t at = (int64_t)(l.nb + j) * p.ld_out + m;
-            if (p.out_dtype == SSM_F32) store_dw(static_cast<float*>(p.out) + at, acc[t][j], left, p.accumulate);
-            else store_dw(static_cast<bf16_t*>(p.out) + at, acc[t][j], left, p.accumulate);
+            if (p.out_dtype == SSM_F32) store_dw(static_cast<float*>(p.out) + at, v, left, p.accumulate);
+            else store_dw(static_cast<bf16_t*>(p.out) + at, v, left, p.accumulate);
         }
 }
 

@@ -27,52 +27,81 @@ __device__ __forceinline__ int row_state(const VocabRows& r, int i) {
     return state;
 }
 
+// the same by a group of LANES neighbouring lanes
+template <int LANES>
+__device__ __forceinline__ int row_state_by(const VocabRows& r, int i, int lane) {
+    int best = 0;  // 1: an entry that counts, 2: one past the vocabulary
+    for (int k = lane; k < r.K; k += LANES) {
+        const int64_t e = (int64_t)i * r.K + k;
+        if (present(r, e)) best = max(best, r.id[e] >= r.V ? 2 : 1);
+    }
+#pragma unroll
+    for (int d = 1; d < LANES; d *= 2) best = max(best, __shfl_xor(best, d));
+    return best == 0 ? kRowOut : best == 1 ? 0 : kRowBad;
+}
+
 __global__ __launch_bounds__(256) void rows_state(VocabRows r, uint32_t* err) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
+    const int i = blockIdx.x * 16 + threadIdx.x / 16, lane = threadIdx.x & 15;
     if (i >= r.N) return;
-    const int state = row_state(r, i);
+    const int state = row_state_by<16>(r, i, lane);
+    if (lane) return;
     r.pos[i] = state;
     if (state == kRowBad && err) atomicOr(err, (uint32_t)SSM_DEVERR_TARGET);
 }
 
-// The rows that count, in order, by one workgroup: 4096 rows a round.  With
-// one entry a row (a target) the states are found here.
+// The rows that count, in order, by one workgroup, 1024 X in a round.  With one entry a
+// row (a target) the states are found here.
+template <int X>
 __global__ __launch_bounds__(1024) void rows_list(VocabRows r, uint32_t* err) {
-    __shared__ int wave_sum[16];
+    __shared__ int before[X * 16], total;  // rows that count before a 64 of them (x, wave), and in all
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int done = 0;
-    for (int64_t base = 0; base < r.N; base += 4096) {
-        int state[4], mine = 0;
-        const int i0 = (int)base + 4 * tid;
+    for (int64_t base = 0; base < r.N; base += 1024 * X) {
+        int state[X];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            state[x] = i0 + x >= r.N ? kRowOut : r.K > 1 ? r.pos[i0 + x] : row_state(r, i0 + x);
+        for (int x = 0; x < X; ++x) {
+            const int i = (int)min(base + 1024 * x + tid, (int64_t)r.N - 1);
+            state[x] = r.K > 1 ? r.pos[i] : row_state(r, i);
+        }
+        uint64_t mask[X];
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+            if (base + 1024 * x + tid >= r.N) state[x] = kRowOut;
             if (r.K == 1 && state[x] == kRowBad && err) atomicOr(err, (uint32_t)SSM_DEVERR_TARGET);
-            mine += state[x] >= 0;
+            mask[x] = __ballot(state[x] >= 0);
+            if (lane == 0) before[x * 16 + wave] = __popcll(mask[x]);
         }
-        int before = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int v = __shfl_up(before, d);
-            if (lane >= d) before += v;
-        }
-        if (lane == 63) wave_sum[wave] = before;
         __syncthreads();
-        int c = done + before - mine, all = 0;
-        for (int w = 0; w < 16; ++w) {
-            if (w < wave) c += wave_sum[w];
-            all += wave_sum[w];
-        }
+        if (wave == 0) {
+            constexpr int Y = X / 4;  // of `before` a lane
+            int v[Y], sum = 0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (i0 + x >= r.N) break;
-            r.pos[i0 + x] = state[x] >= 0 ? c : state[x];
-            if (state[x] < 0) continue;
-            r.rows[c] = i0 + x;
-            if (r.K == 1) r.kid[c] = r.id[i0 + x];
-            ++c;
+            for (int y = 0; y < Y; ++y) {
+                v[y] = sum;
+                sum += before[lane * Y + y];
+            }
+            int up = sum;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int w = __shfl_up(up, d);
+                if (lane >= d) up += w;
+            }
+#pragma unroll
+            for (int y = 0; y < Y; ++y) before[lane * Y + y] = done + up - sum + v[y];
+            if (lane == 63) total = done + up;
         }
-        done += all;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+            const int64_t i = base + 1024 * x + tid;
+            if (i >= r.N) break;
+            const int c = before[x * 16 + wave] + __popcll(mask[x] & ((1ull << lane) - 1));
+            r.pos[i] = state[x] >= 0 ? c : state[x];
+            if (state[x] < 0) continue;
+            r.rows[c] = (int)i;
+            if (r.K == 1) r.kid[c] = r.id[i];
+        }
+        done = total;
         __syncthreads();
     }
     if (tid == 0) *r.count = done;
@@ -127,8 +156,8 @@ __device__ __forceinline__ void load8(const VocabPack& p, const char* row, int c
 }
 
 template <int TERMS>
-__global__ __launch_bounds__(256) void pack_rows(VocabPack p, int pieces, bool wide) {
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void pack_piece(const VocabPack& p, bool wide, int64_t x) {
+    const int pieces = (p.width + 63) / 64 * 8;
     const int r = (int)(x / pieces), c = 8 * (int)(x % pieces);
     if (r >= (p.count ? min(p.n, *p.count) : p.n)) return;
     uint16_t t[TERMS][8];
@@ -171,12 +200,6 @@ __device__ __forceinline__ void turn_tile(const VocabPack& p, int r0, int c0, in
     }
 }
 
-template <int TERMS>
-__global__ __launch_bounds__(256) void turn_rows(VocabPack p, bool wide) {
-    const int n = p.count ? min(p.n, *p.count) : p.n, r0 = blockIdx.x * 64;
-    if (r0 < n) turn_tile<TERMS>(p, r0, blockIdx.y * 64, n, wide, [](int) { return true; });
-}
-
 bool is_wide(const VocabPack& p) {
     const int64_t es = p.dtype == SSM_BF16 ? 2 : 4;
     return reinterpret_cast<uintptr_t>(p.src) % 16 == 0 && p.ld * es % 16 == 0;
@@ -210,17 +233,35 @@ __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2) {
     m = top;
 }
 
-// 32 rows a workgroup, 8 lanes a row: a wave is 8 rows by 8 lanes
+// sums over the LANES lanes of a row, 8, 64 or a whole workgroup
+template <int LANES, typename Combine>
+__device__ __forceinline__ void combine_lanes(float& m, float& s, Combine combine) {
+#pragma unroll
+    for (int d = 1; d < (LANES < 64 ? LANES : 64); d *= 2) combine(m, s, __shfl_xor(m, d), __shfl_xor(s, d));
+    if constexpr (LANES == 256) {
+        __shared__ float2 waves[4];
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = make_float2(m, s);
+        __syncthreads();
+        m = waves[0].x;
+        s = waves[0].y;
+#pragma unroll
+        for (int w = 1; w < 4; ++w) combine(m, s, waves[w].x, waves[w].y);
+    }
+}
+
+// Few rows have many partials each: then a wave or a workgroup takes a row.
+template <int LANES>
 __global__ __launch_bounds__(256) void join_rows(VocabJoin j) {
     const VocabRows& r = j.r;
-    const int lane = threadIdx.x & 7;
-    const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x / 8;
+    const int lane = threadIdx.x % LANES;
+    const int64_t i = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
     if (i >= r.N) return;
     int c;
     if (r.pos) {
         c = r.pos[i];
     } else {
-        const int state = row_state(r, (int)i);
+        const int state = row_state_by<(LANES < 64 ? LANES : 64)>(r, (int)i, lane & 63);
         c = state < 0 ? state : (int)i;
         if (state == kRowBad && j.err && j.last && lane == 0) atomicOr(j.err, (uint32_t)SSM_DEVERR_TARGET);
     }
@@ -232,19 +273,24 @@ __global__ __launch_bounds__(256) void join_rows(VocabJoin j) {
             if (j.lse) j.lse[i] = v;
         }
         if (j.logq)
-            for (int k = lane; k < r.K; k += 8) j.logq[i * r.K + k] = v;
+            for (int k = lane; k < r.K; k += LANES) j.logq[i * r.K + k] = v;
         return;
     }
     // a lane without a part holds a sum of nothing
     float m = -0x1p127f, s = 0.0f;
-    for (int x = lane; x < j.parts; x += 8) {
-        const float2 v = j.part[(int64_t)x * r.Np + c];
-        merge(m, s, v.x, v.y);
-    }
+    for (int x = lane; x < j.parts; x += 4 * LANES) {
+        float2 v[4];
 #pragma unroll
-    for (int d = 1; d < 8; d *= 2) merge(m, s, __shfl_xor(m, d), __shfl_xor(s, d));
+        for (int y = 0; y < 4; ++y)
+            v[y] = j.part[(int64_t)min(x + y * LANES, j.parts - 1) * r.Np + c];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            if (x + y * LANES < j.parts) merge(m, s, v[y].x, v[y].y);
+    }
+    combine_lanes<LANES>(m, s, merge);
     if (!j.first) merge(m, s, j.state[c].x, j.state[c].y);
     if (!j.last) {
+        if (LANES == 256) __syncthreads();  // every lane has read the state
         if (lane == 0) j.state[c] = make_float2(m, s);
         return;
     }
@@ -254,17 +300,16 @@ __global__ __launch_bounds__(256) void join_rows(VocabJoin j) {
         if (lane == 0 && j.loss) j.loss[i] = ((m - j.slog[c]) + l) * kLn2;
         return;
     }
-    const float off = top_offset(r, i, lane, 8);
-    float loss = 0.0f;
-    for (int k = lane; k < r.K; k += 8) {
+    const float off = top_offset(r, i, lane & 63, LANES < 64 ? LANES : 64);
+    float loss = 0.0f, none = 0.0f;
+    for (int k = lane; k < r.K; k += LANES) {
         const int64_t e = i * r.K + k;
         const bool there = present(r, e);
         const float q = there ? (j.slog[(int64_t)k * r.Np + c] - m) - l : 0.0f, p = top2(r, e) - off;
         if (j.logq) j.logq[e] = q * kLn2;
         if (there) loss += fast_exp2(p) * (p - q);
     }
-#pragma unroll
-    for (int d = 1; d < 8; d *= 2) loss += __shfl_xor(loss, d);
+    combine_lanes<LANES>(none, loss, [](float&, float& a, float, float b) { a += b; });
     if (lane == 0 && j.loss) j.loss[i] = loss * kLn2;
 }
 
@@ -303,37 +348,62 @@ __device__ __forceinline__ void top_factors(const VocabCoef& f, int64_t i, int c
     }
 }
 
-__global__ __launch_bounds__(256) void coef_target(VocabCoef f) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c < *f.r.count) target_factors(f, f.r.rows[c], c);
-}
+// workgroups of each kind, in this order
+struct Begin {
+    VocabPack pack_h, pack_w, turn_h, turn_w;
+    VocabCoef coef;
+    unsigned pack_h_end, pack_w_end, turn_h_end, turn_w_end;
+    bool wide_h, wide_w;
+};
 
-__global__ __launch_bounds__(256) void coef_top(VocabCoef f) {
-    const int c = blockIdx.x * 4 + threadIdx.x / 64;
-    if (c < *f.r.count) top_factors(f, f.r.rows[c], c, threadIdx.x & 63);
-}
-
-// The first 16 workgroups take the rows' factors, a wave a row; the others turn h,
-// 64 columns each.
 template <int TERMS>
-__global__ __launch_bounds__(256) void few_begin(VocabCoef f, VocabPack p, bool wide) {
-    const VocabRows& r = f.r;
+__global__ __launch_bounds__(256) void begin(Begin b) {
+    const unsigned id = blockIdx.x;
     const int tid = threadIdx.x;
-    if (blockIdx.x < kVocabFew / 4) {
+    if (id < b.pack_h_end) {
+        pack_piece<TERMS>(b.pack_h, b.wide_h, (int64_t)id * 256 + tid);
+    } else if (id < b.pack_w_end) {
+        pack_piece<TERMS>(b.pack_w, b.wide_w, (int64_t)(id - b.pack_h_end) * 256 + tid);
+    } else if (id < b.turn_w_end) {
+        const bool w = id >= b.turn_h_end;
+        const VocabPack& p = w ? b.turn_w : b.turn_h;
+        const int x = (int)(id - (w ? b.turn_h_end : b.pack_w_end)), columns = (p.width + 63) / 64;
+        const int n = p.count ? min(p.n, *p.count) : p.n, r0 = x / columns * 64;
+        if (r0 < n) turn_tile<TERMS>(p, r0, x % columns * 64, n, w ? b.wide_w : b.wide_h, [](int) { return true; });
+    } else if (b.coef.r.logit) {
+        const int c = (int)(id - b.turn_w_end) * 4 + tid / 64;
+        if (c < *b.coef.r.count) top_factors(b.coef, b.coef.r.rows[c], c, tid & 63);
+    } else {
+        const int c = (int)(id - b.turn_w_end) * 256 + tid;
+        if (c < *b.coef.r.count) target_factors(b.coef, b.coef.r.rows[c], c);
+    }
+}
+
+// The first 16 workgroups take the rows' factors, a wave a row; the next turn h, 64
+// columns each; in f32 the last pack it.
+template <int TERMS>
+__global__ __launch_bounds__(256) void few_begin(VocabCoef f, VocabPack turned, VocabPack packed, bool wide) {
+    constexpr int kRows = kVocabFew / 4;
+    const VocabRows& r = f.r;
+    const int tid = threadIdx.x, columns = (r.D + 63) / 64;
+    if (blockIdx.x < kRows) {
         const int i = blockIdx.x * 4 + tid / 64;
-        if (blockIdx.x == 0 && tid == 0) *r.count = r.N;
         if (i >= r.N) return;
-        const int state = row_state(r, i);
+        const int state = row_state_by<64>(r, i, tid & 63);
         if ((tid & 63) == 0) r.pos[i] = state < 0 ? state : i;
         if (state < 0) return;
         if (r.logit) top_factors(f, i, i, tid & 63);
         else if ((tid & 63) == 0) target_factors(f, i, i);
         return;
     }
+    if ((int)blockIdx.x >= kRows + columns) {
+        pack_piece<TERMS>(packed, wide, (int64_t)(blockIdx.x - kRows - columns) * 256 + tid);
+        return;
+    }
     __shared__ int state[kVocabFew];
-    if (tid < kVocabFew) state[tid] = tid < r.N ? row_state(r, tid) : kRowOut;
+    for (int i = tid / 4; i < r.N; i += 64) state[i] = row_state_by<4>(r, i, tid & 3);
     __syncthreads();
-    turn_tile<TERMS>(p, 0, 64 * (blockIdx.x - kVocabFew / 4), r.N, wide, [&](int row) { return state[row] >= 0; });
+    turn_tile<TERMS>(turned, 0, 64 * (blockIdx.x - kRows), r.N, wide, [&](int row) { return state[row] >= 0; });
 }
 
 template <int TERMS>
@@ -359,11 +429,21 @@ __global__ __launch_bounds__(256) void dh_rows(VocabDh d, int pieces) {
     const int c = d.r.pos[i];
     const float fill = c == kRowBad ? __builtin_nanf("") : 0.0f;
     float v[4] = {fill, fill, fill, fill};
-    if (c >= 0)
-        for (int s = 0; s < d.parts; ++s) {
-            const float4 a = *reinterpret_cast<const float4*>(d.acc + ((int64_t)s * d.r.Np + c) * d.Dp + col);
-            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    if (c >= 0) {
+        const float* from = d.acc + (int64_t)c * d.Dp + col;
+        const int64_t part = (int64_t)d.r.Np * d.Dp;
+        for (int s = 0; s < d.parts; s += 8) {
+            float4 a[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                a[y] = *reinterpret_cast<const float4*>(from + min(s + y, d.parts - 1) * part);
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                if (s + y < d.parts) {
+                    v[0] += a[y].x; v[1] += a[y].y; v[2] += a[y].z; v[3] += a[y].w;
+                }
         }
+    }
     const int64_t at = i * d.ld + col;
     const int left = d.r.D - col;
     if (d.io == SSM_F32) {
@@ -383,47 +463,55 @@ __global__ __launch_bounds__(256) void dh_rows(VocabDh d, int pieces) {
 }
 
 unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
+unsigned pack_blocks(const VocabPack& p) { return blocks((int64_t)p.n * ((p.width + 63) / 64 * 8), 256); }
 int launched() { return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 
 }  // namespace
 
 int launch_vocab_rows(const VocabRows& r, uint32_t* err, hipStream_t stream) {
-    if (r.K > 1 && r.N > 0) rows_state<<<blocks(r.N, 256), 256, 0, stream>>>(r, err);
-    rows_list<<<1, 1024, 0, stream>>>(r, err);
+    if (r.K > 1 && r.N > 0) rows_state<<<blocks(r.N, 16), 256, 0, stream>>>(r, err);
+    if (r.N <= 4096) rows_list<4><<<1, 1024, 0, stream>>>(r, err);
+    else rows_list<16><<<1, 1024, 0, stream>>>(r, err);
     if (r.K > 1 && r.N > 0) rows_ids<<<blocks((int64_t)r.N * r.K, 256), 256, 0, stream>>>(r);
     return launched();
 }
 
-int launch_vocab_pack(const VocabPack& p, hipStream_t stream) {
-    const int pieces = (p.width + 63) / 64 * 8;
-    const unsigned grid = blocks((int64_t)p.n * pieces, 256);
-    if (p.dtype == SSM_BF16) pack_rows<1><<<grid, 256, 0, stream>>>(p, pieces, is_wide(p));
-    else pack_rows<3><<<grid, 256, 0, stream>>>(p, pieces, is_wide(p));
-    return launched();
-}
-
-int launch_vocab_turn(const VocabPack& p, hipStream_t stream) {
-    const dim3 grid(blocks(p.n, 64), blocks(p.width, 64));
-    if (p.dtype == SSM_BF16) turn_rows<1><<<grid, 256, 0, stream>>>(p, is_wide(p));
-    else turn_rows<3><<<grid, 256, 0, stream>>>(p, is_wide(p));
+int launch_vocab_begin(const VocabBegin& v, int dtype, hipStream_t stream) {
+    Begin b = {};
+    auto turn_blocks = [](const VocabPack* p) { return p ? blocks(p->n, 64) * blocks(p->width, 64) : 0; };
+    if (v.pack_h) b.pack_h = *v.pack_h;
+    if (v.turn_h) b.turn_h = *v.turn_h;
+    if (v.pack_w) b.pack_w = *v.pack_w;
+    if (v.turn_w) b.turn_w = *v.turn_w;
+    if (v.coef) b.coef = *v.coef;
+    b.wide_h = is_wide(v.pack_h ? b.pack_h : b.turn_h);
+    b.wide_w = is_wide(v.pack_w ? b.pack_w : b.turn_w);
+    b.pack_h_end = v.pack_h ? pack_blocks(b.pack_h) : 0;
+    b.pack_w_end = b.pack_h_end + (v.pack_w ? pack_blocks(b.pack_w) : 0);
+    b.turn_h_end = b.pack_w_end + turn_blocks(v.turn_h);
+    b.turn_w_end = b.turn_h_end + turn_blocks(v.turn_w);
+    const unsigned grid = b.turn_w_end + (!v.coef ? 0 : blocks(b.coef.r.N, b.coef.r.logit ? 4 : 256));
+    if (!grid) return SSM_OK;
+    if (dtype == SSM_BF16) begin<1><<<grid, 256, 0, stream>>>(b);
+    else begin<3><<<grid, 256, 0, stream>>>(b);
     return launched();
 }
 
 int launch_vocab_join(const VocabJoin& j, hipStream_t stream) {
-    join_rows<<<blocks(j.r.N, 32), 256, 0, stream>>>(j);
+    if (j.r.N <= 512) join_rows<256><<<j.r.N, 256, 0, stream>>>(j);
+    else if (j.r.N <= 4096) join_rows<64><<<blocks(j.r.N, 4), 256, 0, stream>>>(j);
+    else join_rows<8><<<blocks(j.r.N, 32), 256, 0, stream>>>(j);
     return launched();
 }
 
-int launch_vocab_coef(const VocabCoef& c, hipStream_t stream) {
-    if (!c.r.logit) coef_target<<<blocks(c.r.N, 256), 256, 0, stream>>>(c);
-    else coef_top<<<blocks(c.r.N, 4), 256, 0, stream>>>(c);
-    return launched();
-}
-
-int launch_vocab_few_begin(const VocabCoef& c, const VocabPack& p, hipStream_t stream) {
-    const unsigned grid = kVocabFew / 4 + blocks(p.width, 64);
-    if (p.dtype == SSM_BF16) few_begin<1><<<grid, 256, 0, stream>>>(c, p, is_wide(p));
-    else few_begin<3><<<grid, 256, 0, stream>>>(c, p, is_wide(p));
+int launch_vocab_few_begin(const VocabCoef& c, const VocabPack& turned, const VocabPack& packed, hipStream_t stream) {
+    unsigned grid = kVocabFew / 4 + blocks(c.r.D, 64);
+    if (c.r.terms == 1) {
+        few_begin<1><<<grid, 256, 0, stream>>>(c, turned, packed, is_wide(turned));
+    } else {
+        grid += pack_blocks(packed);
+        few_begin<3><<<grid, 256, 0, stream>>>(c, turned, packed, is_wide(turned));
+    }
     return launched();
 }
 
