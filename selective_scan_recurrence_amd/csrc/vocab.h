@@ -119,11 +119,11 @@ struct VocabGemm {
     bool accumulate;
 };
 int vocab_parts(int m, int n);  // partials of a forward's logits, at most m / 64 + 4
-int vocab_splits(const VocabGemm& d_h, const VocabGemm& d_w, int g_terms);
+int vocab_splits(const VocabGemm& d_h, const VocabGemm& d_w);
 int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream);
-int launch_vocab_logits_bwd(const VocabGemm& g, int terms, int g_terms, hipStream_t stream);
+int launch_vocab_logits_bwd(const VocabGemm& g, int terms, hipStream_t stream);
 // both products of the gradient (n = 0: not that one)
-int launch_vocab_grads(const VocabGemm& d_h, const VocabGemm& d_w, int terms, int g_terms, hipStream_t stream);
+int launch_vocab_grads(const VocabGemm& d_h, const VocabGemm& d_w, int terms, hipStream_t stream);
 
 // Up to 64 rows (Np = 64), h and W read where they lie.  Rows keep their places; one
 // that is left out has pos < 0.
@@ -132,10 +132,10 @@ struct VocabFew {
     VocabRows r;
     const void *h, *w;
     int64_t ld_h, ld_w;
-    const uint16_t* hp;    // f32: h's terms [3][64][width rounded up to 64]
+    const uint16_t* hp;    // f32: h's terms [3][Np][width rounded up to 64]
     float scale2;
     int v0, P;             // the piece
-    float2* part;          // forward, a partial for every vocab_few_tile of the piece
+    float2* part;          // forward, a partial for every vocab_few_part of the piece
     float* slog;
     const float *lse2, *coef, *at;  // backward, as VocabCoef
     uint16_t *g, *gt;
@@ -143,16 +143,16 @@ struct VocabFew {
     void* d_w;             // of the piece, row stride ld_w
     int dw_dtype;
     bool accumulate;
-    float* acc;            // d_h: [splits][64][width rounded up to 64]
+    float* acc;            // d_h: [splits][Np][width rounded up to 64]
     int splits;
     bool first;            // the first piece: acc holds nothing yet
 };
-int vocab_few_tile(int64_t V, int N, int terms);
+int vocab_few_part(const VocabRows& r);  // of the vocabulary a partial stands for
 int vocab_few_splits(int64_t V, int64_t D);
 int launch_vocab_few_logits(const VocabFew& p, bool backward, hipStream_t stream);
 int launch_vocab_few_d_h(const VocabFew& p, hipStream_t stream);
 int launch_vocab_few_d_w(const VocabFew& p, hipStream_t stream);
-// Before the backward: pos, the factors, and h turned, [terms][width][64], with the rows
+// Before the backward: pos, the factors, and h turned, [terms][width][Np], with the rows
 // that are left out zero; in f32 also h's terms, packed.
 int launch_vocab_few_begin(const VocabCoef& c, const VocabPack& turned, const VocabPack& packed, hipStream_t stream);
 
@@ -175,7 +175,7 @@ __device__ __forceinline__ void store_dw(E* to, float (&v)[V], int left, bool ac
 // v's next bf16 term, of TERMS in all; v keeps the rest.  One: v rounded.  Two: that,
 // and the rest rounded (2^-17 of v is left).  Three: v itself, each term what the ones
 // before leave with the low half cut off, so that no rounding passes the largest
-// value.  An infinity or a NaN is all in the first.
+// value; an infinity leaves a NaN.
 template <int TERMS>
 __device__ __forceinline__ uint16_t next_term(float& v) {
     if constexpr (TERMS < 3) {
@@ -183,9 +183,9 @@ __device__ __forceinline__ uint16_t next_term(float& v) {
         v = fabsf(to_f32(t)) < __builtin_inff() ? v - to_f32(t) : 0.0f;
         return t;
     } else {
-        const uint16_t t = v != v ? 0x7fc0 : __float_as_uint(v) >> 16;
-        v = fabsf(v) < __builtin_inff() ? v - to_f32(t) : 0.0f;
-        return t;
+        const uint32_t bits = __float_as_uint(v);
+        v -= __uint_as_float(bits & 0xffff0000u);
+        return bits >> 16;
     }
 }
 template <int TERMS>

@@ -15,14 +15,9 @@ bool known(int32_t dtype) { return dtype == SSM_F32 || dtype == SSM_BF16; }
 size_t size_of(int32_t dtype) { return dtype == SSM_BF16 ? 2 : 4; }
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-// With so few rows a gradient may hang on a single rounded value of g, and the
-// products wait for W's bytes: a second term of g costs little and takes its
-// rounding (2^-9 of a value) out of the result.
-constexpr int kVocabFewRows = 128;
-
 struct VocabShape {
     int N, D, V, K, top;
-    int g_terms;  // bf16 terms of g
+    int g_terms;  // bf16 terms of g: see few rows
     int64_t ld_h, ld_w;
     int io, dw, terms;
     float scale, top_scale;
@@ -44,7 +39,7 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
     if (s.ld_h < s.D || s.ld_w < s.D || s.ld_h > 1 << 22 || s.ld_w > 1 << 22) return SSM_ERR_SHAPE;
     if (!isfinite(d->scale) || !isfinite(d->top_scale)) return SSM_ERR_SHAPE;
     s.io = d->io_dtype; s.dw = d->dw_dtype; s.terms = s.io == SSM_BF16 ? 1 : 3;
-    s.g_terms = s.terms == 3 ? 3 : s.N <= kVocabFewRows ? 2 : 1;
+    s.g_terms = s.terms == 3 ? 3 : s.N <= kVocabFew ? 2 : 1;
     if (s.io == SSM_F32 && s.dw == SSM_BF16) return SSM_ERR_UNSUPPORTED;
     s.scale = d->scale; s.top_scale = d->top_scale;
     s.accumulate = d->flags & SSM_VOCAB_ACCUMULATE;
@@ -71,9 +66,9 @@ int splits_of(const VocabShape& s, const Plan& p) {
     h.m = w.m = s.D;
     h.n = s.N;
     h.k = (int)p.piece;
-    const int alone = vocab_splits(h, w, s.g_terms);
+    const int alone = vocab_splits(h, w);
     w.n = (int)p.piece;
-    const int both = vocab_splits(h, w, s.g_terms);
+    const int both = vocab_splits(h, w);
     return both > alone ? both : alone;
 }
 
@@ -255,7 +250,7 @@ int forward_few(const Call& c, float* loss, float* lse, float* logq, uint32_t* e
     f.r.pos = nullptr;
     f.part = c.at<float2>(p.part);
     f.slog = c.at<float>(p.slog);
-    const int tile = vocab_few_tile(c.s.V, c.s.N, c.s.terms);
+    const int tile = vocab_few_part(c.r);
     if (c.s.terms == 3) {
         const VocabPack packed = placed_h(c, p.h, p.Np * p.Kd);
         VocabBegin b;
@@ -338,7 +333,7 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
         l.coef = f.coef;
         l.g = g;
         l.gt = gt;
-        RUN(launch_vocab_logits_bwd(l, s.terms, s.g_terms, c.stream));
+        RUN(launch_vocab_logits_bwd(l, s.terms, c.stream));
         RUN(launch_vocab_patch({c.r, f.at, (int)v0, (int)p.piece, s.g_terms, g, gt}, c.stream));
         VocabGemm gh = {};
         gh.a = c.at<uint16_t>(p.wt); gh.a_plane = s.D * p.piece; gh.lda = p.piece;
@@ -346,7 +341,7 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
         gh.m = s.D; gh.n = d_h ? s.N : 0; gh.k = (int)round_up(n, kVocabStep);
         gh.count = c.r.count; gh.Np = p.Np;
         gh.out = c.at<float>(p.acc); gh.ld_out = p.Kd; gh.splits = p.splits; gh.accumulate = x > 0;
-        RUN(launch_vocab_grads(gh, product_w(c, v0, n, d_w), s.terms, s.g_terms, c.stream));
+        RUN(launch_vocab_grads(gh, product_w(c, v0, n, d_w), s.terms, c.stream));
     }
     if (d_h) RUN(launch_vocab_dh({c.r, c.at<float>(p.acc), p.splits, (int)p.Kd, s.io, d_h, s.ld_h}, c.stream));
     return SSM_OK;

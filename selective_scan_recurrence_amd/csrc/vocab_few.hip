@@ -1,7 +1,9 @@
 // The losses over a vocabulary for up to 64 rows (decoded tokens, a short batch):
 // bound by W's bytes, so W goes from memory to registers as it lies, once for the
 // logits and once for d_h, in its own type and alignment, and nothing of it is
-// laid out again.
+// laid out again.  With so few rows a gradient may hang on a single rounded value of
+// g, and the products wait for W's bytes: g has a second bf16 term, which takes its
+// rounding (2^-9 of a value) out of the result.
 #include <type_traits>
 
 #include "vocab.h"
@@ -70,45 +72,43 @@ struct Raw {
     }
 };
 
-// The same sixteen values of h: as they lie, or (f32) of its terms in the workspace,
+// Eight of the same values of h: as they lie, or (f32) of its terms in the workspace,
 // which every workgroup would have to form again.
 template <typename E>
-struct Rows {
-    Raw<E> x;
-    __device__ __forceinline__ void load(const VocabFew& p, int n, int k) {
-        x.load(static_cast<const E*>(p.h) + (int64_t)n * p.ld_h, k, p.r.D);
-    }
-    __device__ __forceinline__ void operand(int h, u32x4 (&f)[1]) const { x.operand(h, f); }
-};
-template <>
-struct Rows<float> {
-    u32x4 x[2][3];
-    __device__ __forceinline__ void load(const VocabFew& p, int n, int k) {
+__device__ __forceinline__ void load_h(const VocabFew& p, int n, int k, u32x4 (&f)[kTerms<E>]) {
+    if constexpr (kTerms<E> == 1) {
+        const bf16_t* row = static_cast<const bf16_t*>(p.h) + (int64_t)n * p.ld_h;
+        if (k + 8 <= p.r.D) {
+            __builtin_memcpy(&f[0], row + k, 16);
+        } else {
+            bf16_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = k + e < p.r.D ? row[k + e] : 0;
+            __builtin_memcpy(&f[0], v, 16);
+        }
+    } else {
         const int64_t Kd = (p.r.D + 63) / 64 * 64;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-                x[h][t] = *reinterpret_cast<const u32x4*>(p.hp + (t * p.r.Np + n) * Kd + k + 8 * h);
+        for (int t = 0; t < 3; ++t) f[t] = *reinterpret_cast<const u32x4*>(p.hp + (t * p.r.Np + n) * Kd + k);
     }
-    __device__ __forceinline__ void operand(int h, u32x4 (&f)[3]) const {
-#pragma unroll
-        for (int t = 0; t < 3; ++t) f[t] = x[h][t];
-    }
-};
+}
 
 // ---- the logits -----------------------------------------------------------------
-// A workgroup of 8 waves owns 16 MT of the vocabulary and all rows (16 NT of them).
-// The waves share out the width in chunks of 64, a lane reading 16 neighbouring
-// values of a row, so that four lanes take a 128-byte line (bf16), and add up
-// through LDS.
-template <typename E, int MT, int NT, bool BWD>
+// A workgroup of 8 waves owns 8 / KW groups of M = 16 MT of the vocabulary and all rows
+// (16 NT of them).  The KW waves of a group share out the width in chunks of 64, a lane
+// reading 16 neighbouring values of a row, so that four lanes take a 128-byte line
+// (bf16), and add up through LDS.  Eight waves a group read h least often; two are for
+// widths of a few chunks, where the adding up would take longer than the reading.
+template <typename E, int MT, int NT, int KW, bool BWD>
 __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
-    constexpr int T = kTerms<E>, M = 16 * MT, N = 16 * NT, LPT = 512 / N < M ? 512 / N : M, VPT = M / LPT, kRow = M + 4;
-    __shared__ __attribute__((aligned(16))) float red[8][N][kRow];
+    constexpr int T = kTerms<E>, M = 16 * MT, N = 16 * NT, kLanes = 64 * KW / N, LPT = kLanes < M ? kLanes : M;
+    constexpr int VPT = M / LPT, kRow = M + 4;
+    __shared__ __attribute__((aligned(16))) float sums[8 / KW][KW][N][kRow];
     const VocabRows& r = p.r;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4, i16 = lane & 15;
-    const int m0 = blockIdx.x * M;  // in the piece
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, i16 = lane & 15;
+    const int group = wave / KW, part = wave % KW, tid = threadIdx.x % (64 * KW);  // in the group
+    float (&red)[KW][N][kRow] = sums[group];
+    const int block = blockIdx.x * (8 / KW) + group, m0 = block * M;  // in the piece
     const E* w[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -119,31 +119,35 @@ __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
     Raw<E> next[MT];
-    int k = 64 * wave + 16 * q;
-    if (64 * wave < r.D)
+    int k = 64 * part + 16 * q;
+    if (64 * part < r.D)
 #pragma unroll
         for (int t = 0; t < MT; ++t) next[t].load(w[t], k, r.D);
-    for (; k - 16 * q < r.D; k += 512) {
+    for (; k - 16 * q < r.D; k += 64 * KW) {
         Raw<E> cur[MT];
-        Rows<E> x[NT];
+        // in f32 half of h at a time, for its registers
+        constexpr int H = T == 3 ? 1 : 2;
+        u32x4 x[H][NT][T];
+        auto load_x = [&](int half) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) x[j].load(p, min(16 * j + i16, r.N - 1), k);
+            for (int j = 0; j < NT; ++j) load_h<E>(p, min(16 * j + i16, r.N - 1), k + 8 * half, x[half % H][j]);
+        };
+        load_x(0);
+        if constexpr (H == 2) load_x(1);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             cur[t] = next[t];
-            if (k - 16 * q + 512 < r.D) next[t].load(w[t], k + 512, r.D);
+            if (k - 16 * q + 64 * KW < r.D) next[t].load(w[t], k + 64 * KW, r.D);
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            u32x4 b[NT][T];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) x[j].operand(half, b[j]);
+            if (half >= H) load_x(half);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 u32x4 a[T];
                 cur[t].operand(half, a);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) acc[t][j] = products<T, T>(a, b[j], acc[t][j]);
+                for (int j = 0; j < NT; ++j) acc[t][j] = products<T, T>(a, x[half % H][j], acc[t][j]);
             }
         }
     }
@@ -151,19 +155,20 @@ __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<f32x4*>(&red[wave][16 * j + i16][16 * t + 4 * q]) = acc[t][j];
+            *reinterpret_cast<f32x4*>(&red[part][16 * j + i16][16 * t + 4 * q]) = acc[t][j];
     __syncthreads();
 
     // LPT lanes of a wave share a row, with every LPT-th of its logits each
     const int n = tid / LPT, l = tid % LPT;
-    const int there = min(M, r.V - p.v0 - m0);  // of the vocabulary
-    if (n < N) {  // whole waves
+    const int there = min(M, r.V - p.v0 - m0);  // of the vocabulary: none or less past its end
+    const bool work = n < N && m0 < p.P;  // whole waves; a group may lie past the piece
+    if (work) {
         float s2[VPT];
 #pragma unroll
         for (int x = 0; x < VPT; ++x) {
             float s = 0.0f;
 #pragma unroll
-            for (int y = 0; y < 8; ++y) s += red[y][n][l + LPT * x];
+            for (int y = 0; y < KW; ++y) s += red[y][n][l + LPT * x];
             s2[x] = s * p.scale2;
         }
         if constexpr (!BWD) {
@@ -183,7 +188,7 @@ __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
             for (int x = 0; x < VPT; ++x) s += fast_exp2(s2[x] - m);
 #pragma unroll
             for (int d = 1; d < LPT; d *= 2) s += __shfl_xor(s, d);
-            if (l == 0) p.part[(int64_t)blockIdx.x * r.Np + n] = make_float2(none ? -0x1p127f : m, s);
+            if (l == 0) p.part[(int64_t)block * r.Np + n] = make_float2(none ? -0x1p127f : m, s);
         } else {
             const bool out = n >= r.N || r.pos[n] < 0;
             const float a = out ? 0.0f : p.coef[n], lse2 = out ? 0.0f : p.lse2[n];
@@ -208,16 +213,20 @@ __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
         __syncthreads();
         constexpr int GT = T == 3 ? 3 : 2;
         const int64_t plane = (int64_t)r.Np * p.P;
-        if (n < N) {
+        if (work) {
             uint16_t g[VPT][GT];
 #pragma unroll
             for (int x = 0; x < VPT; ++x) bf16_terms<GT>(red[0][n][VPT * l + x], g[x]);
 #pragma unroll
             for (int t = 0; t < GT; ++t)
+                __builtin_memcpy(p.g + t * plane + (int64_t)n * p.P + m0 + VPT * l, [&] {
+                    struct { uint16_t v[VPT]; } o;
 #pragma unroll
-                for (int x = 0; x < VPT; ++x) p.g[t * plane + (int64_t)n * p.P + m0 + VPT * l + x] = g[x][t];
+                    for (int x = 0; x < VPT; ++x) o.v[x] = g[x][t];
+                    return o;
+                }().v, 2 * VPT);
         }
-        for (int x = tid; x < M * 8; x += 512) {  // 8 rows of one column
+        for (int x = tid; x < M * 8 && m0 < p.P; x += 64 * KW) {  // 8 rows of a column
             const int m = x / 8, n0 = x % 8 * 8;
             uint16_t v[8][GT];
 #pragma unroll
@@ -321,17 +330,18 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
 }
 
 // ---- d_w ------------------------------------------------------------------------
-// A wave owns 64 columns and 128 of the vocabulary, 16 of it a step; the sum over the
-// rows is one or two MFMAs long, and d_w's bytes bound it.  Tiles take the columns in
-// the order of the big products' rows (S neighbouring groups of 4 a lane).
+// A wave owns 64 columns and 64 of the vocabulary, 16 of it a step; the sum over the
+// rows is one or two MFMAs long, and d_w's bytes bound it.  Every load is made before
+// the first store: a load's wait also waits for the stores before it.  Tiles take the
+// columns in the order of the big products' rows (S neighbouring groups of 4 a lane).
 template <int T, int KS, int S>
 __global__ __launch_bounds__(256, 2) void few_d_w(VocabFew p) {
-    constexpr int GT = T == 3 ? 3 : 2, kSteps = 8;
+    constexpr int GT = T == 3 ? 3 : 2, kSteps = 4;
     const VocabRows& r = p.r;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, i16 = lane & 15;
-    const int d0 = 256 * blockIdx.x + 64 * wave, rows = min(p.P, r.V - p.v0);
+    const int d0 = 256 * blockIdx.x + 64 * wave, v0 = 16 * kSteps * blockIdx.y, rows = min(p.P, r.V - p.v0);
     if (d0 >= r.D) return;
-    u32x4 a[4][KS][T];
+    u32x4 a[4][KS][T], b[kSteps][KS][GT];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -342,74 +352,107 @@ __global__ __launch_bounds__(256, 2) void few_d_w(VocabFew p) {
                 a[t][k][n] = *reinterpret_cast<const u32x4*>(p.ht + ((int64_t)n * r.D + d) * r.Np + 32 * k + 8 * q);
             }
     const int64_t plane = (int64_t)r.Np * p.P;
-    u32x4 next[KS][GT];
-    auto load = [&](int v) {  // gt has a piece's rows, whole tiles of them
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
             for (int n = 0; n < GT; ++n)
-                next[k][n] = r.N == 0 ? u32x4{0, 0, 0, 0}  // without rows nothing wrote it
-                                      : *reinterpret_cast<const u32x4*>(p.gt + n * plane + (int64_t)(v + i16) * r.Np +
-                                                                        32 * k + 8 * q);
-    };
-    const int begin = 16 * kSteps * blockIdx.y, end = min(begin + 16 * kSteps, rows);
-    load(begin);
-    for (int v = begin; v < end; v += 16) {
-        u32x4 b[KS][GT];
+                b[s][k][n] = r.N == 0 ? u32x4{0, 0, 0, 0}  // without rows nothing wrote it
+                                      : *reinterpret_cast<const u32x4*>(
+                                            p.gt + n * plane + (int64_t)min(v0 + 16 * s + i16, rows - 1) * r.Np +
+                                            32 * k + 8 * q);
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int n = 0; n < GT; ++n) b[k][n] = next[k][n];
-        if (v + 16 < end) load(v + 16);
+    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
         for (int t = 0; t < 4; t += S) {
             float c[4 * S];
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
+            for (int x = 0; x < S; ++x) {
                 f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < KS; ++k) acc = products<T, GT>(a[t + s][k], b[k], acc);
+                for (int k = 0; k < KS; ++k) acc = products<T, GT>(a[t + x][k], b[s][k], acc);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) c[4 * s + x] = acc[x];
+                for (int y = 0; y < 4; ++y) c[4 * x + y] = acc[y];
             }
-            const int d = d0 + 16 * t + 4 * S * q, left = r.D - d;
-            if (v + i16 >= rows || left <= 0) continue;
-            const int64_t at = (int64_t)(v + i16) * p.ld_w + d;
+            const int v = v0 + 16 * s + i16, d = d0 + 16 * t + 4 * S * q, left = r.D - d;
+            if (v >= rows || left <= 0) continue;
+            const int64_t at = (int64_t)v * p.ld_w + d;
             if (p.dw_dtype == SSM_F32) store_dw(static_cast<float*>(p.d_w) + at, c, left, p.accumulate);
             else store_dw(static_cast<bf16_t*>(p.d_w) + at, c, left, p.accumulate);
         }
+}
+
+// How the logits are shared out: 16 mt of the vocabulary a group, the more the fewer
+// times h is read, as long as there are enough workgroups; and kw waves a group.
+struct FewTile {
+    int mt, nt, kw;
+};
+FewTile few_tile(const VocabRows& r) {
+    FewTile f;
+    f.nt = r.N <= 16 ? 1 : r.N <= 32 ? 2 : 4;
+    const int most = r.terms == 3 || f.nt > 2 ? 2 : 4;
+    f.mt = 1;
+    while (f.mt < most && r.V / (32 * f.mt) >= 400) f.mt *= 2;
+    f.kw = 8;
+    if (r.D <= 1024 && r.V / (64 * f.mt) >= 400) f.kw = 2;
+    return f;
+}
+
+template <typename E, int MT, int NT, bool BWD>
+void start(const VocabFew& p, int kw, int v, hipStream_t stream) {
+    constexpr int M = 16 * MT;
+    if (kw == 8) few_logits<E, MT, NT, 8, BWD><<<(v + M - 1) / M, 512, 0, stream>>>(p);
+    else few_logits<E, MT, NT, 2, BWD><<<(v + 4 * M - 1) / (4 * M), 512, 0, stream>>>(p);
+}
+
+template <typename E, int NT, bool BWD>
+void start(const VocabFew& p, const FewTile& f, int v, hipStream_t stream) {
+    if (f.mt == 1) start<E, 1, NT, BWD>(p, f.kw, v, stream);
+    else if (f.mt == 4) {
+        if constexpr (sizeof(E) == 2 && NT <= 2) start<E, 4, NT, BWD>(p, f.kw, v, stream);
+    } else {
+        start<E, 2, NT, BWD>(p, f.kw, v, stream);
     }
 }
 
-template <typename E, int MT, bool BWD>
+template <typename E, bool BWD>
 int launch_logits(const VocabFew& p, hipStream_t stream) {
-    const int M = 16 * MT, v = p.r.V - p.v0 < p.P ? p.r.V - p.v0 : p.P, grid = (v + M - 1) / M;
-    if (p.r.N <= 16) few_logits<E, MT, 1, BWD><<<grid, 512, 0, stream>>>(p);
-    else if (p.r.N <= 32) few_logits<E, MT, 2, BWD><<<grid, 512, 0, stream>>>(p);
-    else if constexpr (MT < 4) few_logits<E, MT, 4, BWD><<<grid, 512, 0, stream>>>(p);  // 64 logits a workgroup are for up to 32 rows
+    const FewTile f = few_tile(p.r);
+    const int v = p.r.V - p.v0 < p.P ? p.r.V - p.v0 : p.P;
+    if (f.nt == 1) start<E, 1, BWD>(p, f, v, stream);
+    else if (f.nt == 2) start<E, 2, BWD>(p, f, v, stream);
+    else start<E, 4, BWD>(p, f, v, stream);
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
 template <bool BWD>
 int launch_logits(const VocabFew& p, hipStream_t stream) {
-    const int mt = vocab_few_tile(p.r.V, p.r.N, p.r.terms) / 16;
-    if (p.r.terms == 3)
-        return mt == 1 ? launch_logits<float, 1, BWD>(p, stream) : launch_logits<float, 2, BWD>(p, stream);
-    return mt == 1   ? launch_logits<bf16_t, 1, BWD>(p, stream)
-           : mt == 2 ? launch_logits<bf16_t, 2, BWD>(p, stream)
-                     : launch_logits<bf16_t, 4, BWD>(p, stream);
+    return p.r.terms == 3 ? launch_logits<float, BWD>(p, stream) : launch_logits<bf16_t, BWD>(p, stream);
+}
+
+template <typename E>
+int launch_d_h(const VocabFew& p, hipStream_t stream) {
+    const dim3 grid((p.r.D + 255) / 256, p.splits);
+    const int nt = few_tile(p.r).nt;
+    if (nt == 1) few_d_h<E, 1><<<grid, 256, 0, stream>>>(p);
+    else if (nt == 2) few_d_h<E, 2><<<grid, 256, 0, stream>>>(p);
+    else few_d_h<E, 4><<<grid, 256, 0, stream>>>(p);
+    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+template <int T, int S>
+int launch_d_w(const VocabFew& p, hipStream_t stream) {
+    const int rows = p.r.V - p.v0 < p.P ? p.r.V - p.v0 : p.P;
+    const dim3 grid((p.r.D + 255) / 256, (rows + 63) / 64);
+    if (p.r.N <= 32) few_d_w<T, 1, S><<<grid, 256, 0, stream>>>(p);
+    else few_d_w<T, 2, S><<<grid, 256, 0, stream>>>(p);
+    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
 }  // namespace
 
-// Of the vocabulary a workgroup: the more, the fewer times h is read, as long as
-// there is more than one workgroup a compute unit.
-int vocab_few_tile(int64_t V, int N, int terms) {
-    const int most = terms == 3 || N > 32 ? 32 : 64;
-    int m = 16;
-    while (m < most && V / (2 * m) >= 400) m *= 2;
-    return m;
-}
+int vocab_few_part(const VocabRows& r) { return 16 * few_tile(r).mt; }
 
 // Parts of d_h's sum over the vocabulary, of 4 steps at least: two workgroups a compute
 // unit, and not many more, since every part is written and read again.
@@ -425,35 +468,12 @@ int launch_vocab_few_logits(const VocabFew& p, bool backward, hipStream_t stream
 }
 
 int launch_vocab_few_d_h(const VocabFew& p, hipStream_t stream) {
-    const dim3 grid((p.r.D + 255) / 256, p.splits);
-    const int nt = p.r.N <= 16 ? 1 : p.r.N <= 32 ? 2 : 4;
-    if (p.r.terms == 3) {
-        if (nt == 1) few_d_h<float, 1><<<grid, 256, 0, stream>>>(p);
-        else if (nt == 2) few_d_h<float, 2><<<grid, 256, 0, stream>>>(p);
-        else few_d_h<float, 4><<<grid, 256, 0, stream>>>(p);
-    } else {
-        if (nt == 1) few_d_h<bf16_t, 1><<<grid, 256, 0, stream>>>(p);
-        else if (nt == 2) few_d_h<bf16_t, 2><<<grid, 256, 0, stream>>>(p);
-        else few_d_h<bf16_t, 4><<<grid, 256, 0, stream>>>(p);
-    }
-    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+    return p.r.terms == 3 ? launch_d_h<float>(p, stream) : launch_d_h<bf16_t>(p, stream);
 }
 
 int launch_vocab_few_d_w(const VocabFew& p, hipStream_t stream) {
-    const int rows = p.r.V - p.v0 < p.P ? p.r.V - p.v0 : p.P;
-    const dim3 grid((p.r.D + 255) / 256, (rows + 127) / 128);
-    const bool two = p.r.N > 32, f32 = p.dw_dtype == SSM_F32;
-    if (p.r.terms == 3) {
-        if (two) few_d_w<3, 2, 1><<<grid, 256, 0, stream>>>(p);
-        else few_d_w<3, 1, 1><<<grid, 256, 0, stream>>>(p);
-    } else if (f32) {
-        if (two) few_d_w<1, 2, 1><<<grid, 256, 0, stream>>>(p);
-        else few_d_w<1, 1, 1><<<grid, 256, 0, stream>>>(p);
-    } else {
-        if (two) few_d_w<1, 2, 2><<<grid, 256, 0, stream>>>(p);
-        else few_d_w<1, 1, 2><<<grid, 256, 0, stream>>>(p);
-    }
-    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+    if (p.r.terms == 3) return launch_d_w<3, 1>(p, stream);
+    return p.dw_dtype == SSM_F32 ? launch_d_w<1, 1>(p, stream) : launch_d_w<1, 2>(p, stream);
 }
 
 }  // namespace ssm

@@ -82,15 +82,14 @@ __device__ __forceinline__ f32x4 take(const f32x4& c) {
     return v;
 }
 
-// A run's planes.  Two runs: the second term of g, then the first.  Six: the
-// partial products of three terms, small ones first.
+// A run's planes.  Six runs: the partial products of three terms, small ones first.
 template <int RUNS>
 __device__ __forceinline__ int plane_a(int run) {
     return RUNS == 6 ? (0x001102 >> (4 * run)) & 15 : 0;
 }
 template <int RUNS>
 __device__ __forceinline__ int plane_b(int run) {
-    return RUNS == 6 ? (0x010120 >> (4 * run)) & 15 : RUNS == 2 ? 1 - run : 0;
+    return RUNS == 6 ? (0x010120 >> (4 * run)) & 15 : 0;
 }
 
 // Tiles of out, numbered in bands of 8 columns.
@@ -567,8 +566,8 @@ int vocab_parts(int m, int n) {
 
 // Splits of d_h's sum over the vocabulary: none longer than the work of a workgroup's
 // place, so that a long sum for few rows does not outlast all else.
-int vocab_splits(const VocabGemm& h, const VocabGemm& w, int g_terms) {
-    const bool big = g_terms != 2 && big_grads(h, w);
+int vocab_splits(const VocabGemm& h, const VocabGemm& w) {
+    const bool big = big_grads(h, w);
     const int tile = big ? 256 : 128;
     const int64_t th = tiles(h.m, h.n, tile), tw = tiles(w.m, w.n, tile), steps = (h.k + 63) / 64;
     int64_t share = (th * steps + tw * ((h.n + 63) / 64)) / (big ? 256 : 512);
@@ -581,21 +580,11 @@ int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream) {
     return big_logits(g) ? launch_fwd<Big>(g, terms, stream) : launch_fwd<Small>(g, terms, stream);
 }
 
-// Two terms of g are taken for few rows, which no big tile is for.
-int launch_vocab_logits_bwd(const VocabGemm& g, int terms, int g_terms, hipStream_t stream) {
-    if (g_terms == 2) {
-        logits_bwd<Small, 1, 2><<<(unsigned)on_xcds(tiles(g.m, g.n, Small::BM)), 256, 0, stream>>>(g);
-        return launched();
-    }
+int launch_vocab_logits_bwd(const VocabGemm& g, int terms, hipStream_t stream) {
     return big_logits(g) ? launch_bwd<Big>(g, terms, stream) : launch_bwd<Small>(g, terms, stream);
 }
 
-int launch_vocab_grads(const VocabGemm& h, const VocabGemm& w, int terms, int g_terms, hipStream_t stream) {
-    if (h.n + w.n == 0) return SSM_OK;
-    if (g_terms == 2) {
-        grads<Small, 2><<<grads_grid<Small>(h, w), 256, 0, stream>>>(h, w);
-        return launched();
-    }
+int launch_vocab_grads(const VocabGemm& h, const VocabGemm& w, int terms, hipStream_t stream) {
     return big_grads(h, w) ? launch_grads<Big>(h, w, terms, stream) : launch_grads<Small>(h, w, terms, stream);
 }
 

@@ -383,11 +383,12 @@ __global__ __launch_bounds__(256) void begin(Begin b) {
 // columns each; in f32 the last pack it.
 template <int TERMS>
 __global__ __launch_bounds__(256) void few_begin(VocabCoef f, VocabPack turned, VocabPack packed, bool wide) {
-    constexpr int kRows = kVocabFew / 4;
     const VocabRows& r = f.r;
-    const int tid = threadIdx.x, columns = (r.D + 63) / 64;
-    if (blockIdx.x < kRows) {
-        const int i = blockIdx.x * 4 + tid / 64;
+    const int tid = threadIdx.x, columns = (r.D + 63) / 64, id = blockIdx.x;
+    constexpr int first = kVocabFew / 4;
+    const int packs = first + columns;
+    if (id < first) {
+        const int i = id * 4 + tid / 64;
         if (i >= r.N) return;
         const int state = row_state_by<64>(r, i, tid & 63);
         if ((tid & 63) == 0) r.pos[i] = state < 0 ? state : i;
@@ -396,14 +397,17 @@ __global__ __launch_bounds__(256) void few_begin(VocabCoef f, VocabPack turned, 
         else if ((tid & 63) == 0) target_factors(f, i, i);
         return;
     }
-    if ((int)blockIdx.x >= kRows + columns) {
-        pack_piece<TERMS>(packed, wide, (int64_t)(blockIdx.x - kRows - columns) * 256 + tid);
+    if (id >= packs) {
+        pack_piece<TERMS>(packed, wide, (int64_t)(id - packs) * 256 + tid);
         return;
     }
     __shared__ int state[kVocabFew];
-    for (int i = tid / 4; i < r.N; i += 64) state[i] = row_state_by<4>(r, i, tid & 3);
+    if (tid / 4 < r.N) {
+        const int of = row_state_by<4>(r, tid / 4, tid & 3);
+        state[tid / 4] = of;
+    }
     __syncthreads();
-    turn_tile<TERMS>(turned, 0, 64 * (blockIdx.x - kRows), r.N, wide, [&](int row) { return state[row] >= 0; });
+    turn_tile<TERMS>(turned, 0, (id - first) * 64, r.N, wide, [&](int row) { return state[row] >= 0; });
 }
 
 template <int TERMS>
@@ -420,12 +424,11 @@ __global__ __launch_bounds__(256) void patch_ids(VocabPatch p, int groups) {
         p.g[n * plane + (int64_t)c * p.P + v] = p.gt[n * plane + (int64_t)v * p.r.Np + c] = t[n];
 }
 
-// four columns of a row of d_h
-__global__ __launch_bounds__(256) void dh_rows(VocabDh d, int pieces) {
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t i = x / pieces;
-    const int col = 4 * (int)(x % pieces);
-    if (i >= d.r.N) return;
+// four rows of d_h, four columns a lane
+__global__ __launch_bounds__(256) void dh_rows(VocabDh d) {
+    const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    const int col = 4 * (64 * (int)blockIdx.y + (threadIdx.x & 63));
+    if (i >= d.r.N || col >= d.r.D) return;
     const int c = d.r.pos[i];
     const float fill = c == kRowBad ? __builtin_nanf("") : 0.0f;
     float v[4] = {fill, fill, fill, fill};
@@ -450,7 +453,9 @@ __global__ __launch_bounds__(256) void dh_rows(VocabDh d, int pieces) {
         float* to = static_cast<float*>(d.d_h) + at;
         if (left >= 4) __builtin_memcpy(to, v, 16);
         else
-            for (int e = 0; e < left; ++e) to[e] = v[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) to[e] = v[e];
     } else {
         uint16_t w[4];
 #pragma unroll
@@ -458,7 +463,9 @@ __global__ __launch_bounds__(256) void dh_rows(VocabDh d, int pieces) {
         uint16_t* to = static_cast<uint16_t*>(d.d_h) + at;
         if (left >= 4) __builtin_memcpy(to, w, 8);
         else
-            for (int e = 0; e < left; ++e) to[e] = w[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) to[e] = w[e];
     }
 }
 
@@ -519,14 +526,12 @@ int launch_vocab_patch(const VocabPatch& p, hipStream_t stream) {
     const int groups = (int)blocks(p.r.N, 256);
     const unsigned grid = (unsigned)groups * p.r.K;
     if (p.terms == 1) patch_ids<1><<<grid, 256, 0, stream>>>(p, groups);
-    else if (p.terms == 2) patch_ids<2><<<grid, 256, 0, stream>>>(p, groups);
     else patch_ids<3><<<grid, 256, 0, stream>>>(p, groups);
     return launched();
 }
 
 int launch_vocab_dh(const VocabDh& d, hipStream_t stream) {
-    const int pieces = (d.r.D + 3) / 4;
-    dh_rows<<<blocks((int64_t)d.r.N * pieces, 256), 256, 0, stream>>>(d, pieces);
+    dh_rows<<<dim3(blocks(d.r.N, 4), blocks(d.r.D, 256)), 256, 0, stream>>>(d);
     return launched();
 }
 

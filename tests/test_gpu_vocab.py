@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 # rows, width, vocabulary
 SIZES = [(1, 64, 1), (1, 1, 5), (1, 64, 300), (3, 40, 77), (16, 128, 1000), (17, 130, 513), (33, 2560, 1030),
          (64, 64, 256), (65, 72, 4097), (130, 192, 700), (257, 100, 515), (300, 515, 640), (520, 64, 130),
-         (70, 320, 9001), (20, 72, 26001), (40, 100, 13001), (64, 33, 30001), (32, 200, 12801), (128, 128, 1000)]
+         (70, 320, 9001), (20, 72, 26001), (40, 100, 13001), (64, 33, 30001), (32, 200, 12801), (128, 128, 1000), (9, 65, 26000),
+         (100, 1100, 7000), (3, 1500, 26003)]
 
 
 def run(t, io, *, dw="f32", scale=1.0, top_scale=1.0, pad_h=0, pad_w=0, d_lse=None, top_lse=None, d_w0=None,
