@@ -78,12 +78,13 @@ struct VocabBegin {
 };
 int launch_vocab_begin(const VocabBegin& b, int dtype, hipStream_t stream);
 
-// g at the entries' ids within the piece [v0, v0 + P).
+// g at the entries' ids within the piece [v0, v0 + n).
 struct VocabPatch {
     VocabRows r;
     const float* at;
-    int v0, P, terms;
-    uint16_t *g, *gt;  // [terms][Np][P], [terms][P][Np]
+    int v0, n, terms;
+    int64_t ld_g, plane;
+    uint16_t *g, *gt;  // [terms][Np][ld_g], [terms][piece][Np]
 };
 int launch_vocab_patch(const VocabPatch& p, hipStream_t stream);
 
@@ -101,12 +102,14 @@ int launch_vocab_dh(const VocabDh& d, hipStream_t stream);
 struct VocabGemm {
     const uint16_t *a, *b;
     int64_t a_plane, b_plane, lda, ldb;
-    int m, n, k;           // rows of A and of B, and length of the sum
+    int m, n, k;           // rows of A and of B, and length of the sum (d_w: count's)
+    int rows;              // d_h: all rows, for a plan of both sums
     const int32_t* count;  // device: bounds n (d_w: k, in whole steps)
     int64_t Np;
     // logits
     float scale2;          // scale * log2 e
-    int v0, K, P;          // the piece's start, ids a row, the piece's length
+    int v0, K;             // the piece's start, ids a row
+    int64_t ld_g;          // g [terms][Np][ld_g], gt [terms][piece][Np]
     float2* part;          // forward
     const int32_t* kid;
     float* slog;
@@ -118,8 +121,8 @@ struct VocabGemm {
     int splits, out_dtype;
     bool accumulate;
 };
-int vocab_parts(int m, int n);  // partials of a forward's logits, at most m / 64 + 4
-int vocab_splits(const VocabGemm& d_h, const VocabGemm& d_w);
+int vocab_parts(const VocabGemm& g, int terms);  // partials of a forward's logits, at most m / 64 + 4
+int vocab_splits(const VocabGemm& d_h, const VocabGemm& d_w, int terms);
 int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream);
 int launch_vocab_logits_bwd(const VocabGemm& g, int terms, hipStream_t stream);
 // both products of the gradient (n = 0: not that one)
@@ -156,7 +159,22 @@ int launch_vocab_few_d_w(const VocabFew& p, hipStream_t stream);
 // that are left out zero; in f32 also h's terms, packed.
 int launch_vocab_few_begin(const VocabCoef& c, const VocabPack& turned, const VocabPack& packed, hipStream_t stream);
 
-// Stores a lane's V neighbouring values of a row of d_w; `left` of them are there
+// Stores what no kernel of this launch reads again past the caches: the operands that
+// its workgroups share stay there (the backward's logits of 16384 x 16384 rows, width
+// 2560, take 1095 us, with plain stores 1220).  V may be aligned to its elements only.
+template <typename E, typename V>
+__device__ __forceinline__ void stream_out(E* to, const V& v) {
+    constexpr int N = sizeof(V);
+    static_assert(N == 8 || N == 16 || N == 32, "");
+    typedef uint32_t Piece __attribute__((ext_vector_type(N == 8 ? 2 : 4), aligned(sizeof(E) < 4 ? 2 : 4)));
+    constexpr int K = N == 32 ? 2 : 1;
+    Piece w[K];
+    __builtin_memcpy(w, &v, N);
+#pragma unroll
+    for (int x = 0; x < K; ++x) __builtin_nontemporal_store(w[x], reinterpret_cast<Piece*>(to) + x);
+}
+
+// Stores a lane's V neighbouring values of a row of d_w; `left` of them are there.
 template <typename E, int V>
 __device__ __forceinline__ void store_dw(E* to, float (&v)[V], int left, bool accumulate) {
 #pragma unroll
@@ -165,7 +183,7 @@ __device__ __forceinline__ void store_dw(E* to, float (&v)[V], int left, bool ac
     E w[V];
 #pragma unroll
     for (int r = 0; r < V; ++r) store_io(&w[r], v[r]);
-    if (left >= V) __builtin_memcpy(to, w, sizeof w);
+    if (left >= V) stream_out(to, w);
     else
 #pragma unroll
         for (int r = 0; r < V; ++r)

@@ -15,6 +15,11 @@ bool known(int32_t dtype) { return dtype == SSM_F32 || dtype == SSM_BF16; }
 size_t size_of(int32_t dtype) { return dtype == SSM_BF16 ? 2 : 4; }
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
+// A row of bf16 values whose length is a multiple of 4 KB gets 512 bytes more: such
+// rows start in the same channels of the caches (a gradient's products of 16384 x 16384
+// rows, width 2560: 2070 us, without 2140).
+int64_t off_channels(int64_t v) { return v % 2048 ? v : v + 256; }
+
 struct VocabShape {
     int N, D, V, K, top;
     int g_terms;  // bf16 terms of g: see few rows
@@ -52,7 +57,7 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
 // of the vocabulary, long enough a sum that adding to d_h once a piece costs
 // little (a piece's d_h product takes over a millisecond, the addition 0.07).
 struct Plan {
-    int64_t Np, Kd, piece;
+    int64_t Np, Kd, piece, ld;  // ld: row stride of what has the piece as columns
     int pieces, splits;
     bool few, packed;  // W goes through the workspace
     size_t count, rows, pos, kid, h, part, state, slog, w, ht, wt, g, gt, lse2, coef, at, acc, bytes;
@@ -64,18 +69,18 @@ constexpr int64_t kPieceBytes = (int64_t)5 << 28;
 int splits_of(const VocabShape& s, const Plan& p) {
     VocabGemm h = {}, w = {};
     h.m = w.m = s.D;
-    h.n = s.N;
+    h.n = h.rows = s.N;
     h.k = (int)p.piece;
-    const int alone = vocab_splits(h, w);
+    const int alone = vocab_splits(h, w, s.terms);
     w.n = (int)p.piece;
-    const int both = vocab_splits(h, w);
+    const int both = vocab_splits(h, w, s.terms);
     return both > alone ? both : alone;
 }
 
 Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     Plan p;
     p.few = s.N <= kVocabFew;
-    p.Np = p.few ? kVocabFew : round_up(s.N, kVocabTile);
+    p.Np = p.few ? kVocabFew : off_channels(round_up(s.N, kVocabTile));
     p.Kd = round_up(s.D, kVocabStep);
     p.packed = packed && !p.few;
     packed = p.packed;
@@ -88,6 +93,7 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     p.pieces = (int)((V + most - 1) / most);
     p.piece = round_up((V + p.pieces - 1) / p.pieces, kVocabTile);
     p.pieces = (int)((V + p.piece - 1) / p.piece);
+    p.ld = p.few ? p.piece : off_channels(p.piece);
 
     size_t at = 0;
     auto take = [&](int64_t n) {
@@ -103,9 +109,9 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     p.w = packed ? take(T * p.piece * p.Kd * 2) : 0;
     if (backward) {
         p.ht = take(T * s.D * p.Np * 2);
-        p.wt = p.few ? 0 : take(T * s.D * p.piece * 2);
-        p.g = take(s.g_terms * p.Np * p.piece * 2);
-        p.gt = take(s.g_terms * p.Np * p.piece * 2);
+        p.wt = p.few ? 0 : take(T * s.D * p.ld * 2);
+        p.g = take(s.g_terms * p.Np * p.ld * 2);
+        p.gt = take(s.g_terms * p.Np * p.ld * 2);
         p.lse2 = take(p.Np * 4);
         p.coef = take(p.Np * 4);
         p.at = take(p.Np * s.K * 4);
@@ -166,7 +172,7 @@ VocabPack pack_h(const Call& c, size_t to, int64_t plane) {
 }
 
 VocabPack pack_w(const Call& c, int64_t v0, int n, size_t to, int64_t plane) {
-    return {c.w, c.s.ld_w, c.s.io, c.s.D, n, v0, nullptr, nullptr, c.at<uint16_t>(to), c.p.piece, plane};
+    return {c.w, c.s.ld_w, c.s.io, c.s.D, n, v0, nullptr, nullptr, c.at<uint16_t>(to), c.p.ld, plane};
 }
 
 // What comes before a piece's logits: W's rows packed unless they are read where they
@@ -174,7 +180,7 @@ VocabPack pack_w(const Call& c, int64_t v0, int n, size_t to, int64_t plane) {
 int begin_piece(const Call& c, int x, int64_t v0, int n, bool turn, const VocabBegin& first) {
     VocabBegin b = x == 0 ? first : VocabBegin();
     const VocabPack packed = pack_w(c, v0, n, c.p.w, c.p.piece * c.p.Kd);
-    const VocabPack turned = pack_w(c, v0, n, c.p.wt, c.s.D * c.p.piece);
+    const VocabPack turned = pack_w(c, v0, n, c.p.wt, c.s.D * c.p.ld);
     if (c.p.packed) b.pack_w = &packed;
     if (turn) b.turn_w = &turned;
     return launch_vocab_begin(b, c.s.io, c.stream);
@@ -198,7 +204,7 @@ VocabGemm logits(const Call& c, int64_t v0, int n) {
     g.count = c.r.count;
     g.Np = c.p.Np;
     g.scale2 = c.s.scale * kLog2e;
-    g.v0 = (int)v0; g.K = c.s.K; g.P = (int)c.p.piece;
+    g.v0 = (int)v0; g.K = c.s.K; g.ld_g = c.p.ld;
     g.kid = c.r.kid;
     return g;
 }
@@ -220,7 +226,7 @@ int forward(const Call& c, float* loss, float* lse, float* logq, uint32_t* err) 
         g.part = c.at<float2>(p.part);
         g.slog = c.at<float>(p.slog);
         RUN(launch_vocab_logits_fwd(g, c.s.terms, c.stream));
-        RUN(launch_vocab_join({c.r, g.part, vocab_parts(n, c.s.N), c.at<float2>(p.state), x == 0,
+        RUN(launch_vocab_join({c.r, g.part, vocab_parts(g, c.s.terms), c.at<float2>(p.state), x == 0,
                                x == p.pieces - 1, g.slog, loss, lse, logq, nullptr}, c.stream));
     }
     return SSM_OK;
@@ -272,7 +278,7 @@ VocabGemm product_w(const Call& c, int64_t v0, int n, void* d_w) {
     const Plan& p = c.p;
     VocabGemm g = {};
     g.a = c.at<uint16_t>(p.ht); g.a_plane = c.s.D * p.Np; g.lda = p.Np;
-    g.b = c.at<uint16_t>(p.gt); g.b_plane = p.Np * p.piece; g.ldb = p.Np;
+    g.b = c.at<uint16_t>(p.gt); g.b_plane = p.Np * p.ld; g.ldb = p.Np;
     g.m = c.s.D; g.n = d_w ? n : 0;
     g.out = static_cast<char*>(d_w) + v0 * c.s.ld_w * (int64_t)size_of(c.s.dw); g.ld_out = c.s.ld_w;
     g.out_dtype = c.s.dw; g.accumulate = c.s.accumulate;
@@ -334,11 +340,11 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
         l.g = g;
         l.gt = gt;
         RUN(launch_vocab_logits_bwd(l, s.terms, c.stream));
-        RUN(launch_vocab_patch({c.r, f.at, (int)v0, (int)p.piece, s.g_terms, g, gt}, c.stream));
+        RUN(launch_vocab_patch({c.r, f.at, (int)v0, n, s.g_terms, p.ld, p.Np * p.ld, g, gt}, c.stream));
         VocabGemm gh = {};
-        gh.a = c.at<uint16_t>(p.wt); gh.a_plane = s.D * p.piece; gh.lda = p.piece;
-        gh.b = g; gh.b_plane = p.Np * p.piece; gh.ldb = p.piece;
-        gh.m = s.D; gh.n = d_h ? s.N : 0; gh.k = (int)round_up(n, kVocabStep);
+        gh.a = c.at<uint16_t>(p.wt); gh.a_plane = s.D * p.ld; gh.lda = p.ld;
+        gh.b = g; gh.b_plane = p.Np * p.ld; gh.ldb = p.ld;
+        gh.m = s.D; gh.n = d_h ? s.N : 0; gh.rows = s.N; gh.k = (int)round_up(n, kVocabStep);
         gh.count = c.r.count; gh.Np = p.Np;
         gh.out = c.at<float>(p.acc); gh.ld_out = p.Kd; gh.splits = p.splits; gh.accumulate = x > 0;
         RUN(launch_vocab_grads(gh, product_w(c, v0, n, d_w), s.terms, c.stream));

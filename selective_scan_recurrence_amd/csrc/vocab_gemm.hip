@@ -394,7 +394,7 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_bwd(VocabGemm p
     float lse2[TN], coef[TN];
     __builtin_memcpy(lse2, p.lse2 + l.nb, sizeof lse2);
     __builtin_memcpy(coef, p.coef + l.nb, sizeof coef);
-    const int64_t plane = p.Np * p.P;
+    const int64_t plane = p.Np * p.ld_g;
     // two tiles, 8 neighbouring m, at a time; zero past the vocabulary and the rows
     auto store = [&](int t0, auto whole) {
         float v[2][TN][4];
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_bwd(VocabGemm p
                 u32x4 w;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) w[x] = g[x / 2][j][x % 2 * 2] | (uint32_t)g[x / 2][j][x % 2 * 2 + 1] << 16;
-                *reinterpret_cast<u32x4*>(p.g + n * plane + (int64_t)(l.nb + j) * p.P + m) = w;
+                stream_out(p.g + n * plane + (int64_t)(l.nb + j) * p.ld_g + m, w);
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -434,8 +434,7 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_bwd(VocabGemm p
                     uint32_t w[TN / 2];
 #pragma unroll
                     for (int j = 0; j < TN; j += 2) w[j / 2] = g[t][j][r] | (uint32_t)g[t][j + 1][r] << 16;
-                    __builtin_memcpy(__builtin_assume_aligned(
-                        p.gt + n * plane + (int64_t)(m + 4 * t + r) * p.Np + l.nb, 2 * TN), w, sizeof w);
+                    stream_out(p.gt + n * plane + (int64_t)(m + 4 * t + r) * p.Np + l.nb, w);
                 }
         }
     };
@@ -465,7 +464,7 @@ __device__ __forceinline__ void tile_d_h(const VocabGemm& p, int n_rows, const P
             if (l.nb + j >= n_rows || m >= p.ld_out) continue;  // ld_out: m's padded end
             f32x4* to = reinterpret_cast<f32x4*>(out + (int64_t)(l.nb + j) * p.ld_out + m);
             const f32x4 v = take(acc[t][j]);
-            *to = p.accumulate ? *to + v : v;
+            stream_out(to, p.accumulate ? *to + v : v);
         }
 }
 
@@ -517,16 +516,32 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void grads(VocabGemm h, Voc
 
 int64_t tiles(int64_t m, int64_t n, int tile) { return (m + tile - 1) / tile * ((n + tile - 1) / tile); }
 
-// Whether 256 x 256 tiles, one a compute unit, take less time than 128 x 128 tiles,
-// two a compute unit: a round of the small ones takes about 5/8 of a big one's.
-bool big_tiles(int64_t big, int64_t small) { return (big + 255) / 256 * 8 <= (small + 511) / 512 * 5; }
+// Whether 256 x 256 tiles, one a compute unit, take less time than 128 x 128 tiles, two a
+// compute unit.  A round of tiles takes `steps` steps of k, 1.48 us each (a big tile's)
+// or 0.88, and its results: `big` or `small` us, measured with sums of 5 and of 40
+// steps.  (16384 x 32768 logits: width 2560 1946 us in big tiles, 2313 in small ones;
+// width 320 440 and 423 us.)
+struct Results {
+    double big, small;
+};
+constexpr Results kStatistics = {5.0, 2.0}, kBothOrders = {13.0, 8.0}, kSums = {10.0, 6.0};
 
-bool big_logits(const VocabGemm& g) { return big_tiles(tiles(g.m, g.n, 256), tiles(g.m, g.n, 128)); }
-
-bool big_grads(const VocabGemm& h, const VocabGemm& w) {
-    return big_tiles(tiles(h.m, h.n, 256) + tiles(w.m, w.n, 256), tiles(h.m, h.n, 128) + tiles(w.m, w.n, 128));
+bool big_tiles(int64_t big, int64_t small, double steps, Results r) {
+    return ((big + 255) / 256) * (1.48 * steps + r.big) <= ((small + 511) / 512) * (0.88 * steps + r.small);
 }
 
+bool big_logits(const VocabGemm& g, int terms, Results r) {
+    const double steps = (terms == 3 ? 6 : 1) * (g.k / kVocabStep);
+    return big_tiles(tiles(g.m, g.n, 256), tiles(g.m, g.n, 128), steps, {r.big * terms, r.small * terms});
+}
+
+bool big_grads(const VocabGemm& h, const VocabGemm& w, int terms) {
+    const int64_t bh = tiles(h.m, h.n, 256), bw = tiles(w.m, w.n, 256);
+    // the mean of both sums' lengths
+    const double steps_h = h.k / kVocabStep, steps_w = (double)((h.rows + kVocabStep - 1) / kVocabStep);
+    const double steps = (terms == 3 ? 6 : 1) * (bh * steps_h + bw * steps_w) / (bh + bw);
+    return big_tiles(bh + bw, tiles(h.m, h.n, 128) + tiles(w.m, w.n, 128), steps, kSums);
+}
 
 int launched() { return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 
@@ -560,32 +575,32 @@ int launch_grads(const VocabGemm& h, const VocabGemm& w, int terms, hipStream_t 
 
 }  // namespace
 
-int vocab_parts(int m, int n) {
-    return big_tiles(tiles(m, n, 256), tiles(m, n, 128)) ? (m + 255) / 256 * 2 : (m + 127) / 128 * 2;
+int vocab_parts(const VocabGemm& g, int terms) {
+    return big_logits(g, terms, kStatistics) ? (g.m + 255) / 256 * 2 : (g.m + 127) / 128 * 2;
 }
 
 // Splits of d_h's sum over the vocabulary: none longer than the work of a workgroup's
 // place, so that a long sum for few rows does not outlast all else.
-int vocab_splits(const VocabGemm& h, const VocabGemm& w) {
-    const bool big = big_grads(h, w);
+int vocab_splits(const VocabGemm& h, const VocabGemm& w, int terms) {
+    const bool big = big_grads(h, w, terms);
     const int tile = big ? 256 : 128;
     const int64_t th = tiles(h.m, h.n, tile), tw = tiles(w.m, w.n, tile), steps = (h.k + 63) / 64;
-    int64_t share = (th * steps + tw * ((h.n + 63) / 64)) / (big ? 256 : 512);
+    int64_t share = (th * steps + tw * ((h.rows + 63) / 64)) / (big ? 256 : 512);
     if (share < 8) share = 8;
     const int64_t n = (steps + share - 1) / share;
     return (int)(n < 1 ? 1 : n > kVocabSplits ? kVocabSplits : n);
 }
 
 int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream) {
-    return big_logits(g) ? launch_fwd<Big>(g, terms, stream) : launch_fwd<Small>(g, terms, stream);
+    return big_logits(g, terms, kStatistics) ? launch_fwd<Big>(g, terms, stream) : launch_fwd<Small>(g, terms, stream);
 }
 
 int launch_vocab_logits_bwd(const VocabGemm& g, int terms, hipStream_t stream) {
-    return big_logits(g) ? launch_bwd<Big>(g, terms, stream) : launch_bwd<Small>(g, terms, stream);
+    return big_logits(g, terms, kBothOrders) ? launch_bwd<Big>(g, terms, stream) : launch_bwd<Small>(g, terms, stream);
 }
 
 int launch_vocab_grads(const VocabGemm& h, const VocabGemm& w, int terms, hipStream_t stream) {
-    return big_grads(h, w) ? launch_grads<Big>(h, w, terms, stream) : launch_grads<Small>(h, w, terms, stream);
+    return big_grads(h, w, terms) ? launch_grads<Big>(h, w, terms, stream) : launch_grads<Small>(h, w, terms, stream);
 }
 
 }  // namespace ssm

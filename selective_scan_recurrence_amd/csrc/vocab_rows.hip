@@ -414,14 +414,14 @@ template <int TERMS>
 __global__ __launch_bounds__(256) void patch_ids(VocabPatch p, int groups) {
     const int k = blockIdx.x / groups, c = blockIdx.x % groups * 256 + threadIdx.x;
     if (c >= *p.r.count) return;
-    const int64_t e = (int64_t)k * p.r.Np + c, plane = (int64_t)p.r.Np * p.P;
+    const int64_t e = (int64_t)k * p.r.Np + c;
     const int id = p.r.kid[e], v = id - p.v0;
-    if (id < p.v0 || v >= p.P) return;
+    if (id < p.v0 || v >= p.n) return;
     uint16_t t[TERMS];
     bf16_terms<TERMS>(p.at[e], t);
 #pragma unroll
     for (int n = 0; n < TERMS; ++n)
-        p.g[n * plane + (int64_t)c * p.P + v] = p.gt[n * plane + (int64_t)v * p.r.Np + c] = t[n];
+        p.g[n * p.plane + (int64_t)c * p.ld_g + v] = p.gt[n * p.plane + (int64_t)v * p.r.Np + c] = t[n];
 }
 
 // four rows of d_h, four columns a lane
