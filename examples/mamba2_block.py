@@ -15,6 +15,10 @@ run and their backwards read them; the scan's operands are packed and unpacked;
 the projections' weight gradients are formed from the checkpoints of their
 inputs.  Only dt, which sits in an exponent, is kept as it is.
 
+With a head, the stack answers with tokens: the vocabulary's weights and the loss of
+the softmax over them, against the next tokens (vocab_ce_fwd, vocab_ce_bwd) or against
+a teacher's top logits (vocab_kd_fwd, vocab_kd_bwd), without the logits.
+
     python examples/mamba2_block.py [steps]
 """
 import os
@@ -168,6 +172,88 @@ class Decoder:
         return ops.norm_residual_fwd(self.norm, b, r, st.norm_out).h
 
 
+class Head:
+    """A vocabulary's weights W [n_vocab][d_model] (f32 masters) over rows of the stack's
+    output: losses a row and their gradients."""
+
+    def __init__(self, sz: Sizes, n_vocab: int, rows: int, seed=0, temperature=1.0, device="cuda"):
+        gen = torch.Generator().manual_seed(seed)
+        self.sz, self.rows, self.temperature = sz, rows, temperature
+        self.W = (torch.randn(n_vocab, sz.d_model, generator=gen) * sz.d_model ** -0.5).to(device)
+        self.n_vocab, self.ws = n_vocab, {}
+
+    def _desc(self, n_top):
+        t = 1.0 / self.temperature if n_top else 1.0
+        desc = ops.vocab_desc(n_rows=self.rows, width=self.sz.d_model, n_vocab=self.n_vocab, n_top=n_top,
+                              io=self.sz.io, scale=t, top_scale=t)
+        if n_top not in self.ws:
+            self.ws[n_top] = ops.vocab_workspace(desc, True, self.W.device)
+        return desc, self.ws[n_top]
+
+    def score(self, h, target):
+        """Losses [rows] of target [rows] int32 after h [rows][d_model]: minus the targets'
+        log-probabilities, 0 where a target is negative."""
+        desc, ws = self._desc(0)
+        return ops.vocab_ce_fwd(desc, h, self.W.to(self.sz.dtype), target, ws=ws).loss
+
+    def tokens(self, h, target, d_loss):
+        """Losses against target, and the gradients d_h, d_W of (d_loss loss).sum()."""
+        desc, ws = self._desc(0)
+        w = self.W.to(self.sz.dtype)
+        f = ops.vocab_ce_fwd(desc, h, w, target, ws=ws)
+        return f.loss, ops.vocab_ce_bwd(desc, h, w, target, f.loss, f.lse, d_loss, ws=ws)
+
+    def teacher(self, h, top_id, top_logit, d_loss):
+        """The same against a teacher's top logits [rows][n_top] f32 at top_id int32, both
+        divided by the temperature."""
+        desc, ws = self._desc(top_id.shape[1])
+        w = self.W.to(self.sz.dtype)
+        f = ops.vocab_kd_fwd(desc, h, w, top_id, top_logit, ws=ws)
+        return f.loss, ops.vocab_kd_bwd(desc, h, w, top_id, top_logit, f.logq, f.lse, d_loss, ws=ws)
+
+
+def _descend(w, grads, lr):
+    """A step of a fixed size along each weight's gradient."""
+    for name, v in grads.items():
+        w[name] -= lr * v.view_as(w[name]) * (w[name].norm() / v.norm().clamp(min=1e-20))
+
+
+def train_tokens(steps=20, n_blocks=2, n_seqs=4, n_tokens=128, n_vocab=1000, sz=None, lr=0.03, seed=0, teacher=None,
+                 n_top=8):
+    """Fits embedding, stack and head to the next tokens of fixed random sequences, or with
+    a teacher (an embedding, a stack and a head as this returns) to its top logits.  The
+    last token of a sequence has no next one.  Returns the mean losses and the three."""
+    sz = sz or Sizes()
+    stack = Stack(sz, [make_block(sz, seed + k) for k in range(n_blocks)], n_seqs, n_tokens)
+    head = Head(sz, n_vocab, stack.rows, seed + 50, temperature=2.0)
+    gen = torch.Generator().manual_seed(seed + 200)
+    embedding = torch.randn(n_vocab, sz.d_model, generator=gen).cuda()
+    tokens = torch.randint(n_vocab, (n_seqs, n_tokens), generator=torch.Generator().manual_seed(7)).cuda()
+    target = torch.cat([tokens[:, 1:], torch.full_like(tokens[:, :1], -1)], 1).reshape(-1).int()
+    tokens = tokens.view(-1)
+    d_loss = torch.full((stack.rows,), 1.0 / (n_seqs * (n_tokens - 1)), device="cuda")
+    if teacher is not None:
+        t_embedding, t_stack, t_head = teacher
+        out = t_stack.forward(t_embedding[tokens], train=False)[0]
+        top_logit, top_id = (out.float() @ t_head.W.t()).topk(n_top, 1)
+        top_id = torch.where(target[:, None] >= 0, top_id, -1).int()
+    losses = []
+    for _ in range(steps):
+        h, _, _, kept = stack.forward(embedding[tokens])
+        if teacher is None:
+            loss, g = head.tokens(h, target, d_loss)
+        else:
+            loss, g = head.teacher(h, top_id, top_logit, d_loss)
+        losses.append(float((loss * d_loss).sum()))
+        grads, d_r = stack.backward(g.d_h, kept)
+        for w, v in zip(stack.blocks, grads):
+            _descend(w, v, lr)
+        _descend({"W": head.W}, {"W": g.d_w}, lr)
+        d_embedding = torch.zeros_like(embedding).index_add_(0, tokens, d_r.float())
+        _descend({"E": embedding}, {"E": d_embedding}, lr)
+    return losses, (embedding, stack, head)
+
+
 def train(steps=40, n_blocks=2, n_seqs=4, n_tokens=128, sz=None, lr=0.05, seed=0):
     """Fits the stack to a fixed random target; returns the losses and the stack."""
     sz = sz or Sizes()
@@ -182,9 +268,7 @@ def train(steps=40, n_blocks=2, n_seqs=4, n_tokens=128, sz=None, lr=0.05, seed=0
         losses.append(float(diff.square().mean()))
         grads, _ = stack.backward((2.0 / diff.numel() * diff).to(sz.dtype), kept)
         for w, g in zip(stack.blocks, grads):
-            for name, v in g.items():
-                # a step of a fixed size along each weight's gradient
-                w[name] -= lr * v.view_as(w[name]) * (w[name].norm() / v.norm().clamp(min=1e-20))
+            _descend(w, g, lr)
     return losses, stack, r
 
 
@@ -195,3 +279,7 @@ if __name__ == "__main__":
     out, _, states, _ = stack.forward(r, train=False)
     token = Decoder(stack, states).step(torch.zeros(stack.n_seqs, stack.sz.d_model, device="cuda"))
     print("next token's output:", tuple(token.shape), token.dtype)
+    losses, model = train_tokens(n)
+    print(f"next tokens: loss {losses[0]:.4f} -> {losses[-1]:.4f}")
+    losses, _ = train_tokens(n, seed=10, teacher=model)
+    print(f"a teacher's 8 top logits: loss {losses[0]:.4f} -> {losses[-1]:.4f}")

@@ -120,6 +120,7 @@ class Reference:
 
 
 def check(what, got, want, err):
+    want, err = want.cpu(), err.cpu()
     got = got.detach().double().cpu().reshape(want.shape)
     assert torch.equal(got.isnan(), want.isnan()), f"{what}: NaN in other places"
     off = torch.where(want.isnan(), 0.0, (got - want).abs() - err.expand_as(want))
