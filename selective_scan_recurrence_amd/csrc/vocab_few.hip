@@ -262,10 +262,26 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
     for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
+    // in bf16 g is read with W, a step ahead; in f32, where it takes more registers, ahead
+    // of the splitting of W
+    constexpr bool kAhead = T == 1;
     struct Step {
         uint32_t w[8][kWords];
+        u32x4 g[NT][GT];
     } next;
+    auto load_g = [&](Step& s, int step) {
+        const int v = 32 * step + 8 * q;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int t = 0; t < GT; ++t) {
+                // written to the end of a workgroup's 16 MT of the vocabulary
+                const u32x4 x = *reinterpret_cast<const u32x4*>(p.g + t * plane + (int64_t)(16 * j + i16) * p.P + v);
+                s.g[j][t] = v < rows ? x : u32x4{0, 0, 0, 0};
+            }
+    };
     auto load = [&](Step& s, int step) {
+        if constexpr (kAhead) load_g(s, step);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             // g is zero past the vocabulary
@@ -282,17 +298,8 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
     };
     if (begin < end) load(next, begin);
     for (int s = begin; s < end; ++s) {
-        const Step cur = next;
-        u32x4 g[NT][GT];
-        const int v = 32 * s + 8 * q;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int t = 0; t < GT; ++t) {
-                // written to the end of a workgroup's 16 MT of the vocabulary
-                const u32x4 x = *reinterpret_cast<const u32x4*>(p.g + t * plane + (int64_t)(16 * j + i16) * p.P + v);
-                g[j][t] = v < rows ? x : u32x4{0, 0, 0, 0};
-            }
+        Step cur = next;
+        if constexpr (!kAhead) load_g(cur, s);
         if (s + 1 < end) load(next, s + 1);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -313,7 +320,7 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
                 }
             }
 #pragma unroll
-            for (int j = 0; j < NT; ++j) acc[t][j] = products<T, GT>(a, g[j], acc[t][j]);
+            for (int j = 0; j < NT; ++j) acc[t][j] = products<T, GT>(a, cur.g[j], acc[t][j]);
         }
     }
     // tile t's row 4 q + x is column 4 (4 q + x) + t: 16 neighbours a lane
@@ -330,30 +337,30 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
 }
 
 // ---- d_w ------------------------------------------------------------------------
-// A wave owns 64 columns and 64 of the vocabulary, 16 of it a step; the sum over the
-// rows is one or two MFMAs long, and d_w's bytes bound it.  Every load is made before
-// the first store: a load's wait also waits for the stores before it.  Tiles take the
-// columns in the order of the big products' rows (S neighbouring groups of 4 a lane).
-template <int T, int KS, int S>
+// A workgroup owns 256 columns and 64 of the vocabulary; the sum over the rows is one
+// or two MFMAs long, and d_w's bytes bound it.  A wave forms 64 columns, 16 of the
+// vocabulary at a time, and the results leave through LDS, so that a wave stores whole
+// runs of a row: 2 rows, width 1314, vocabulary 86475: 207 us with 64-byte pieces of 16
+// rows a store, 73 so.
+template <typename E, int T, int KS>
 __global__ __launch_bounds__(256, 2) void few_d_w(VocabFew p) {
-    constexpr int GT = T == 3 ? 3 : 2, kSteps = 4;
+    constexpr int GT = T == 3 ? 3 : 2, kV = 64, kD = 256, kChunk = 16 / sizeof(E);
+    __shared__ __attribute__((aligned(16))) E tile[kV][kD + kChunk];
     const VocabRows& r = p.r;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, i16 = lane & 15;
-    const int d0 = 256 * blockIdx.x + 64 * wave, v0 = 16 * kSteps * blockIdx.y, rows = min(p.P, r.V - p.v0);
-    if (d0 >= r.D) return;
-    u32x4 a[4][KS][T], b[kSteps][KS][GT];
+    const int d0 = kD * blockIdx.x, v0 = kV * blockIdx.y, rows = min(p.P, r.V - p.v0);
+    u32x4 a[4][KS][T], b[kV / 16][KS][GT];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int n = 0; n < T; ++n) {
-                const int d = min(d0 + 16 * S * (t / S) + 4 * S * (i16 >> 2) + 4 * (t % S) + (i16 & 3), r.D - 1);
-                a[t][k][n] = *reinterpret_cast<const u32x4*>(p.ht + ((int64_t)n * r.D + d) * r.Np + 32 * k + 8 * q);
-            }
+            for (int n = 0; n < T; ++n)
+                a[t][k][n] = *reinterpret_cast<const u32x4*>(
+                    p.ht + ((int64_t)n * r.D + min(d0 + 64 * wave + 16 * t + i16, r.D - 1)) * r.Np + 32 * k + 8 * q);
     const int64_t plane = (int64_t)r.Np * p.P;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+    for (int s = 0; s < kV / 16; ++s)
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -363,24 +370,42 @@ __global__ __launch_bounds__(256, 2) void few_d_w(VocabFew p) {
                                             p.gt + n * plane + (int64_t)min(v0 + 16 * s + i16, rows - 1) * r.Np +
                                             32 * k + 8 * q);
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+    for (int s = 0; s < kV / 16; ++s)
 #pragma unroll
-        for (int t = 0; t < 4; t += S) {
-            float c[4 * S];
+        for (int t = 0; t < 4; ++t) {
+            f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-            for (int x = 0; x < S; ++x) {
-                f32x4 acc = {0, 0, 0, 0};
+            for (int k = 0; k < KS; ++k) acc = products<T, GT>(a[t][k], b[s][k], acc);
+            E o[4];
+            // what is added to is added to in f32
+            E* at = &tile[16 * s + i16][64 * wave + 16 * t + 4 * q];
+            if (p.accumulate && v0 + 16 * s + i16 < rows) {
+                const E* old = static_cast<const E*>(p.d_w) + (int64_t)(v0 + 16 * s + i16) * p.ld_w;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) acc = products<T, GT>(a[t + x][k], b[s][k], acc);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) c[4 * x + y] = acc[y];
+                for (int x = 0; x < 4; ++x) {
+                    const int d = d0 + 64 * wave + 16 * t + 4 * q + x;
+                    if (d < r.D) acc[x] += to_f32(old[d]);
+                }
             }
-            const int v = v0 + 16 * s + i16, d = d0 + 16 * t + 4 * S * q, left = r.D - d;
-            if (v >= rows || left <= 0) continue;
-            const int64_t at = (int64_t)v * p.ld_w + d;
-            if (p.dw_dtype == SSM_F32) store_dw(static_cast<float*>(p.d_w) + at, c, left, p.accumulate);
-            else store_dw(static_cast<bf16_t*>(p.d_w) + at, c, left, p.accumulate);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) store_io(&o[x], acc[x]);
+            __builtin_memcpy(at, o, sizeof o);
         }
+    __syncthreads();
+    constexpr int kChunks = kD / kChunk;  // of a row
+    for (int x = threadIdx.x; x < kV * kChunks; x += 256) {
+        const int v = x / kChunks, c = x % kChunks * kChunk, left = r.D - d0 - c;
+        if (v0 + v >= rows || left <= 0) continue;
+        E* to = static_cast<E*>(p.d_w) + (int64_t)(v0 + v) * p.ld_w + d0 + c;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(&tile[v][c]);
+        if (left >= kChunk) {
+            stream_out(to, w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e)
+                if (e < left) to[e] = tile[v][c + e];
+        }
+    }
 }
 
 // How the logits are shared out: 16 mt of the vocabulary a group, the more the fewer
@@ -392,10 +417,9 @@ FewTile few_tile(const VocabRows& r) {
     FewTile f;
     f.nt = r.N <= 16 ? 1 : r.N <= 32 ? 2 : 4;
     const int most = r.terms == 3 || f.nt > 2 ? 2 : 4;
+    f.kw = r.D <= 1024 && r.V >= 64 * 256 ? 2 : 8;
     f.mt = 1;
-    while (f.mt < most && r.V / (32 * f.mt) >= 400) f.mt *= 2;
-    f.kw = 8;
-    if (r.D <= 1024 && r.V / (64 * f.mt) >= 400) f.kw = 2;
+    while (f.mt < most && r.V / (32 * f.mt * (8 / f.kw)) >= 400) f.mt *= 2;
     return f;
 }
 
@@ -441,12 +465,12 @@ int launch_d_h(const VocabFew& p, hipStream_t stream) {
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
-template <int T, int S>
+template <typename E, int T>
 int launch_d_w(const VocabFew& p, hipStream_t stream) {
     const int rows = p.r.V - p.v0 < p.P ? p.r.V - p.v0 : p.P;
     const dim3 grid((p.r.D + 255) / 256, (rows + 63) / 64);
-    if (p.r.N <= 32) few_d_w<T, 1, S><<<grid, 256, 0, stream>>>(p);
-    else few_d_w<T, 2, S><<<grid, 256, 0, stream>>>(p);
+    if (p.r.N <= 32) few_d_w<E, T, 1><<<grid, 256, 0, stream>>>(p);
+    else few_d_w<E, T, 2><<<grid, 256, 0, stream>>>(p);
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
@@ -454,11 +478,11 @@ int launch_d_w(const VocabFew& p, hipStream_t stream) {
 
 int vocab_few_part(const VocabRows& r) { return 16 * few_tile(r).mt; }
 
-// Parts of d_h's sum over the vocabulary, of 4 steps at least: two workgroups a compute
+// Parts of d_h's sum over the vocabulary, of 4 steps at least: four workgroups a compute
 // unit, and not many more, since every part is written and read again.
 int vocab_few_splits(int64_t V, int64_t D) {
     const int64_t columns = (D + 255) / 256, most = (V + 127) / 128;
-    int64_t n = 640 / columns;
+    int64_t n = 1024 / columns;
     if (n > most) n = most;
     return (int)(n < 1 ? 1 : n > 256 ? 256 : n);
 }
@@ -472,8 +496,8 @@ int launch_vocab_few_d_h(const VocabFew& p, hipStream_t stream) {
 }
 
 int launch_vocab_few_d_w(const VocabFew& p, hipStream_t stream) {
-    if (p.r.terms == 3) return launch_d_w<3, 1>(p, stream);
-    return p.dw_dtype == SSM_F32 ? launch_d_w<1, 1>(p, stream) : launch_d_w<1, 2>(p, stream);
+    if (p.r.terms == 3) return launch_d_w<float, 3>(p, stream);
+    return p.dw_dtype == SSM_F32 ? launch_d_w<float, 1>(p, stream) : launch_d_w<bf16_t, 1>(p, stream);
 }
 
 }  // namespace ssm

@@ -424,27 +424,43 @@ __global__ __launch_bounds__(256) void patch_ids(VocabPatch p, int groups) {
         p.g[n * p.plane + (int64_t)c * p.ld_g + v] = p.gt[n * p.plane + (int64_t)v * p.r.Np + c] = t[n];
 }
 
-// four rows of d_h, four columns a lane
-__global__ __launch_bounds__(256) void dh_rows(VocabDh d) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+// Rows of d_h, four columns a lane; with many parts (few rows) LANES lanes share out a
+// column's, else a workgroup takes four rows.
+template <int LANES>
+__global__ __launch_bounds__(LANES > 1 ? 64 * LANES : 256) void dh_rows(VocabDh d) {
+    constexpr int kRows = LANES > 1 ? 1 : 4;
+    const int x = threadIdx.x / 64, lane = LANES > 1 ? x : 0;
+    const int64_t i = (int64_t)blockIdx.x * kRows + (LANES > 1 ? 0 : x);
     const int col = 4 * (64 * (int)blockIdx.y + (threadIdx.x & 63));
-    if (i >= d.r.N || col >= d.r.D) return;
-    const int c = d.r.pos[i];
+    const bool mine = i < d.r.N && col < d.r.D;
+    if (LANES == 1 && !mine) return;
+    const int c = mine ? d.r.pos[i] : kRowOut;
     const float fill = c == kRowBad ? __builtin_nanf("") : 0.0f;
     float v[4] = {fill, fill, fill, fill};
     if (c >= 0) {
         const float* from = d.acc + (int64_t)c * d.Dp + col;
         const int64_t part = (int64_t)d.r.Np * d.Dp;
-        for (int s = 0; s < d.parts; s += 8) {
+        for (int s = lane; s < d.parts; s += 8 * LANES) {
             float4 a[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-                a[y] = *reinterpret_cast<const float4*>(from + min(s + y, d.parts - 1) * part);
+                a[y] = *reinterpret_cast<const float4*>(from + min(s + y * LANES, d.parts - 1) * part);
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-                if (s + y < d.parts) {
+                if (s + y * LANES < d.parts) {
                     v[0] += a[y].x; v[1] += a[y].y; v[2] += a[y].z; v[3] += a[y].w;
                 }
+        }
+    }
+    if constexpr (LANES > 1) {
+        __shared__ float4 sums[LANES][64];
+        sums[lane][threadIdx.x & 63] = make_float4(v[0], v[1], v[2], v[3]);
+        __syncthreads();
+        if (lane > 0 || !mine) return;
+#pragma unroll
+        for (int y = 1; y < LANES; ++y) {
+            const float4 a = sums[y][threadIdx.x];
+            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
         }
     }
     const int64_t at = i * d.ld + col;
@@ -531,7 +547,8 @@ int launch_vocab_patch(const VocabPatch& p, hipStream_t stream) {
 }
 
 int launch_vocab_dh(const VocabDh& d, hipStream_t stream) {
-    dh_rows<<<dim3(blocks(d.r.N, 4), blocks(d.r.D, 256)), 256, 0, stream>>>(d);
+    if (d.parts > 16) dh_rows<16><<<dim3(d.r.N, blocks(d.r.D, 256)), 1024, 0, stream>>>(d);
+    else dh_rows<1><<<dim3(blocks(d.r.N, 4), blocks(d.r.D, 256)), 256, 0, stream>>>(d);
     return launched();
 }
 
