@@ -15,7 +15,7 @@ namespace ssm {
 // by 64 or 128 rows (m).
 constexpr int kVocabStep = 64;
 constexpr int kVocabTile = 256;  // what tensors in the workspace are padded to
-constexpr int kVocabSplits = 8;  // of d_h's sum over the vocabulary, at most
+constexpr int kVocabSplits = 64;  // parts of a gradient's sum, at most
 
 // What the small kernels need of a call.  `rows` are the rows that count, in
 // order: row c of them is row rows[c] of h.
@@ -88,15 +88,19 @@ struct VocabPatch {
 };
 int launch_vocab_patch(const VocabPatch& p, hipStream_t stream);
 
-// d_h from the sum over parts of the rows that count [parts][Np][Dp].
-struct VocabDh {
-    VocabRows r;
+// The sum over parts [parts][part / Dp][Dp], in the caller's tensor.
+struct VocabSum {
     const float* acc;
-    int parts, Dp, io;
-    void* d_h;
+    int64_t part;
+    int parts, Dp;
+    const int32_t* pos;  // d_h: where row i's sum is, kRowOut (zero) or kRowBad (NaN); NULL: at i
+    int n, D;            // of out
+    int dtype;
+    void* out;
     int64_t ld;
+    bool accumulate;
 };
-int launch_vocab_dh(const VocabDh& d, hipStream_t stream);
+int launch_vocab_sum(const VocabSum& d, hipStream_t stream);
 
 // out[n][m] = sum_k A[m][k] B[n][k] over planes of bf16 terms, k in steps of 64.
 struct VocabGemm {
@@ -115,14 +119,17 @@ struct VocabGemm {
     float* slog;
     const float *lse2, *coef;  // backward
     uint16_t *g, *gt;
-    // d_h: f32 [splits][Np][ld_out], each split a part of k; d_w: out rows of n
+    // gradients: [splits] parts of k (d_h: f32 always), out_part values apart
     void* out;
-    int64_t ld_out;
+    int64_t ld_out, out_part;
     int splits, out_dtype;
     bool accumulate;
 };
 int vocab_parts(const VocabGemm& g, int terms);  // partials of a forward's logits, at most m / 64 + 4
-int vocab_splits(const VocabGemm& d_h, const VocabGemm& d_w, int terms);
+struct VocabParts {
+    int d_h, d_w;
+};
+VocabParts vocab_grads_parts(const VocabGemm& d_h, const VocabGemm& d_w, int terms);
 int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream);
 int launch_vocab_logits_bwd(const VocabGemm& g, int terms, hipStream_t stream);
 // both products of the gradient (n = 0: not that one)

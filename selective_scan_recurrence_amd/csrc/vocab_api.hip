@@ -58,23 +58,26 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
 // little (a piece's d_h product takes over a millisecond, the addition 0.07).
 struct Plan {
     int64_t Np, Kd, piece, ld;  // ld: row stride of what has the piece as columns
-    int pieces, splits;
+    int pieces;
+    VocabParts parts;  // of the gradients' sums
     bool few, packed;  // W goes through the workspace
-    size_t count, rows, pos, kid, h, part, state, slog, w, ht, wt, g, gt, lse2, coef, at, acc, bytes;
+    size_t count, rows, pos, kid, h, part, state, slog, w, ht, wt, g, gt, lse2, coef, at, acc, acc_w, bytes;
 };
 
 constexpr int64_t kPieceBytes = (int64_t)5 << 28;
 
-// of d_h's sum: for both products, or for d_h alone, whichever has more
-int splits_of(const VocabShape& s, const Plan& p) {
+// for both products, d_h's also for d_h alone, whichever has more
+VocabParts parts_of(const VocabShape& s, const Plan& p) {
+    if (p.few) return {vocab_few_splits(p.piece, s.D), 1};
     VocabGemm h = {}, w = {};
     h.m = w.m = s.D;
     h.n = h.rows = s.N;
     h.k = (int)p.piece;
-    const int alone = vocab_splits(h, w, s.terms);
+    const int alone = vocab_grads_parts(h, w, s.terms).d_h;
     w.n = (int)p.piece;
-    const int both = vocab_splits(h, w, s.terms);
-    return both > alone ? both : alone;
+    VocabParts n = vocab_grads_parts(h, w, s.terms);
+    n.d_h = n.d_h > alone ? n.d_h : alone;
+    return n;
 }
 
 Plan plan_of(const VocabShape& s, bool backward, bool packed) {
@@ -115,8 +118,9 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
         p.lse2 = take(p.Np * 4);
         p.coef = take(p.Np * 4);
         p.at = take(p.Np * s.K * 4);
-        p.splits = p.few ? vocab_few_splits(p.piece, s.D) : splits_of(s, p);
-        p.acc = take(p.splits * p.Np * p.Kd * 4);
+        p.parts = parts_of(s, p);
+        p.acc = take(p.parts.d_h * p.Np * p.Kd * 4);
+        p.acc_w = p.parts.d_w > 1 ? take(p.parts.d_w * p.piece * p.Kd * 4) : 0;
     } else {
         p.part = take(p.piece / (p.few ? 16 : 64) * p.Np * 8);
         p.state = take(p.Np * 8);
@@ -273,16 +277,35 @@ int forward_few(const Call& c, float* loss, float* lse, float* logq, uint32_t* e
     return SSM_OK;
 }
 
-// the product for d_w of a piece [v0, v0 + n)
+// the product for d_w of a piece [v0, v0 + n), or of its sum's parts
 VocabGemm product_w(const Call& c, int64_t v0, int n, void* d_w) {
     const Plan& p = c.p;
     VocabGemm g = {};
     g.a = c.at<uint16_t>(p.ht); g.a_plane = c.s.D * p.Np; g.lda = p.Np;
     g.b = c.at<uint16_t>(p.gt); g.b_plane = p.Np * p.ld; g.ldb = p.Np;
     g.m = c.s.D; g.n = d_w ? n : 0;
-    g.out = static_cast<char*>(d_w) + v0 * c.s.ld_w * (int64_t)size_of(c.s.dw); g.ld_out = c.s.ld_w;
-    g.out_dtype = c.s.dw; g.accumulate = c.s.accumulate;
+    g.splits = p.parts.d_w;
+    if (p.parts.d_w > 1) {
+        g.out = c.at<float>(p.acc_w); g.ld_out = p.Kd; g.out_part = p.piece * p.Kd;
+        g.out_dtype = SSM_F32;
+    } else {
+        g.out = static_cast<char*>(d_w) + v0 * c.s.ld_w * (int64_t)size_of(c.s.dw); g.ld_out = c.s.ld_w;
+        g.out_dtype = c.s.dw; g.accumulate = c.s.accumulate;
+    }
     return g;
+}
+
+int join_d_w(const Call& c, int64_t v0, int n, void* d_w) {
+    const Plan& p = c.p;
+    return launch_vocab_sum({c.at<float>(p.acc_w), p.piece * p.Kd, p.parts.d_w, (int)p.Kd, nullptr, n, c.s.D, c.s.dw,
+                             static_cast<char*>(d_w) + v0 * c.s.ld_w * (int64_t)size_of(c.s.dw), c.s.ld_w,
+                             c.s.accumulate}, c.stream);
+}
+
+int join_d_h(const Call& c, void* d_h) {
+    const Plan& p = c.p;
+    return launch_vocab_sum({c.at<float>(p.acc), p.Np * p.Kd, p.parts.d_h, (int)p.Kd, c.r.pos, c.s.N, c.s.D, c.s.io,
+                             d_h, c.s.ld_h, false}, c.stream);
 }
 
 VocabCoef factors(const Call& c, const float* logq, const float* loss, const float* lse, const float* d_loss,
@@ -300,7 +323,7 @@ int backward_few(const Call& c, const VocabCoef& f, void* d_h, void* d_w) {
     few.g = c.at<uint16_t>(p.g); few.gt = c.at<uint16_t>(p.gt);
     few.ht = c.at<uint16_t>(p.ht);
     few.dw_dtype = s.dw; few.accumulate = s.accumulate;
-    few.acc = c.at<float>(p.acc); few.splits = p.splits;
+    few.acc = c.at<float>(p.acc); few.splits = p.parts.d_h;
     for (int x = 0; x < p.pieces; ++x) {
         few.v0 = (int)(x * p.piece);
         few.first = x == 0;
@@ -311,9 +334,7 @@ int backward_few(const Call& c, const VocabCoef& f, void* d_h, void* d_w) {
             RUN(launch_vocab_few_d_w(few, c.stream));
         }
     }
-    if (d_h && s.N > 0)
-        RUN(launch_vocab_dh({c.r, few.acc, p.splits, (int)p.Kd, s.io, d_h, s.ld_h}, c.stream));
-    return SSM_OK;
+    return d_h && s.N > 0 ? join_d_h(c, d_h) : SSM_OK;
 }
 
 int backward(const Call& c, const float* logq, const float* loss, const float* lse, const float* d_loss,
@@ -346,11 +367,12 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
         gh.b = g; gh.b_plane = p.Np * p.ld; gh.ldb = p.ld;
         gh.m = s.D; gh.n = d_h ? s.N : 0; gh.rows = s.N; gh.k = (int)round_up(n, kVocabStep);
         gh.count = c.r.count; gh.Np = p.Np;
-        gh.out = c.at<float>(p.acc); gh.ld_out = p.Kd; gh.splits = p.splits; gh.accumulate = x > 0;
+        gh.out = c.at<float>(p.acc); gh.ld_out = p.Kd; gh.out_part = p.Np * p.Kd; gh.splits = p.parts.d_h;
+        gh.accumulate = x > 0;
         RUN(launch_vocab_grads(gh, product_w(c, v0, n, d_w), s.terms, c.stream));
+        if (d_w && p.parts.d_w > 1) RUN(join_d_w(c, v0, n, d_w));
     }
-    if (d_h) RUN(launch_vocab_dh({c.r, c.at<float>(p.acc), p.splits, (int)p.Kd, s.io, d_h, s.ld_h}, c.stream));
-    return SSM_OK;
+    return d_h ? join_d_h(c, d_h) : SSM_OK;
 }
 
 // what every call checks of its tensors

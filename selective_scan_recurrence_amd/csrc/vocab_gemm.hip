@@ -327,27 +327,41 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_fwd(VocabGemm p
 
     // The logits at the rows' ids, 64 ids a row at a time: which of a lane's rows' ids
     // are in the wave's vocabulary, as bits, then 64 of m at a time through LDS.
-    constexpr int U = TM / 4, X = TN / 4;
-    const int left = p.m - l.mw;
+    constexpr int U = TM / 4, X = TN / 4, kIds = 16;
+    const int base = p.v0 + l.mw, left = max(min(p.m - l.mw, 16 * TM), 0);
+    uint32_t window[X];  // of the vocabulary, for the lane's rows
+#pragma unroll
+    for (int x = 0; x < X; ++x) window[x] = l.nw + 64 * x + l.lane < n_rows ? left : 0;
     float* mine = reinterpret_cast<float*>(lds + l.wave * (TN * 4096));
     __syncthreads();
     for (int k0 = 0; k0 < p.K; k0 += 64) {
-        uint64_t hits[U][X] = {};
+        // `ats` holds where a row's last ten are, 6 bits each
+        uint64_t hits[U][X] = {}, ats[U][X] = {};
+        const int some = min(64, p.K - k0);
+        for (int k1 = 0; k1 < some; k1 += kIds) {
+            int id[kIds][X];
 #pragma unroll
-        for (int x = 0; x < X; ++x) {
-            const int n = min(l.nw + 64 * x + l.lane, n_rows - 1);
-            const int32_t* ids = p.kid + k0 * p.Np + n;
-            const int base = p.v0 + l.mw, some = min(64, p.K - k0);
-            const bool row = l.nw + 64 * x + l.lane < n_rows;
-#pragma unroll 8
-            for (int k = 0; k < some; ++k) {
-                const int id = ids[k * p.Np], at = id - base;
-                // an absent entry's id is negative, and may wrap around
-                const bool in = row && id >= base && at < left;
+            for (int k = 0; k < kIds; ++k)
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (in && at / 64 == u) hits[u][x] |= 1ull << k;
-            }
+                for (int x = 0; x < X; ++x)
+                    if (k1 + k < some)
+                        id[k][x] = p.kid[(k0 + k1 + k) * p.Np + min(l.nw + 64 * x + l.lane, n_rows - 1)];
+#pragma unroll
+            for (int k = 0; k < kIds; ++k)
+                if (k1 + k < some)
+#pragma unroll
+                    for (int x = 0; x < X; ++x) {
+                        // an absent entry's id is -1
+                        const uint32_t at = id[k][x] - base;
+                        if (at < window[x]) {
+#pragma unroll
+                            for (int u = 0; u < U; ++u)
+                                if (at / 64 == u) {
+                                    hits[u][x] |= 1ull << (k1 + k);
+                                    ats[u][x] = ats[u][x] << 6 | (at & 63);
+                                }
+                        }
+                    }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -364,9 +378,12 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_fwd(VocabGemm p
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
             for (int x = 0; x < X; ++x)
-                for (uint64_t left_bits = hits[u][x]; left_bits; left_bits &= left_bits - 1) {
-                    const int64_t e = (int64_t)(k0 + __builtin_ctzll(left_bits)) * p.Np + l.nw + 64 * x + l.lane;
-                    const int at = p.kid[e] - p.v0 - l.mw - 64 * u, n = 64 * x + l.lane;
+                for (int y = 0; hits[u][x]; ++y) {
+                    const int k = 63 - __builtin_clzll(hits[u][x]), n = 64 * x + l.lane;
+                    hits[u][x] &= ~(1ull << k);
+                    const int64_t e = (int64_t)(k0 + k) * p.Np + l.nw + n;
+                    const int at = y < 10 ? (int)(ats[u][x] & 63) : p.kid[e] - base - 64 * u;
+                    ats[u][x] >>= 6;
                     p.slog[e] = p.scale2 * mine[n * 64 + 4 * ((at >> 2) ^ (n / TN)) + (at & 3)];
                 }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -455,7 +472,7 @@ __device__ __forceinline__ void tile_d_h(const VocabGemm& p, int n_rows, const P
     product<T, RUNS, 1>(p, m0 *= T::BM, n0 *= T::BN, n_rows, (int)((int64_t)all * split / p.splits),
                         (int)((int64_t)all * (split + 1) / p.splits), lds, acc);
     const Lane<T, 1> l(m0, n0);
-    float* out = static_cast<float*>(p.out) + split * p.Np * p.ld_out;
+    float* out = static_cast<float*>(p.out) + split * p.out_part;
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -472,9 +489,11 @@ template <class T, int RUNS>
 __device__ __forceinline__ void tile_d_w(const VocabGemm& p, int count, const Place& place, int id, uint8_t* lds) {
     constexpr int TM = T::TM, TN = T::TN, S = RUNS == 6 ? 1 : 2;
     int m0, n0;
-    place.of(id, &m0, &n0);
+    const int tiles = place.mt * place.nt, split = id / tiles, all = (count + kVocabStep - 1) / kVocabStep;
+    place.of(id - split * tiles, &m0, &n0);
     f32x4 acc[TM][TN];
-    product<T, RUNS, S>(p, m0 *= T::BM, n0 *= T::BN, p.n, 0, (count + kVocabStep - 1) / kVocabStep, lds, acc);
+    product<T, RUNS, S>(p, m0 *= T::BM, n0 *= T::BN, p.n, (int)((int64_t)all * split / p.splits),
+                        (int)((int64_t)all * (split + 1) / p.splits), lds, acc);
     const Lane<T, S> l(m0, n0);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
@@ -489,7 +508,7 @@ __device__ __forceinline__ void tile_d_w(const VocabGemm& p, int count, const Pl
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[4 * x + r] = c[r];
             }
-            const int64_t at = (int64_t)(l.nb + j) * p.ld_out + m;
+            const int64_t at = split * p.out_part + (int64_t)(l.nb + j) * p.ld_out + m;
             if (p.out_dtype == SSM_F32) store_dw(static_cast<float*>(p.out) + at, v, left, p.accumulate);
             else store_dw(static_cast<bf16_t*>(p.out) + at, v, left, p.accumulate);
         }
@@ -509,7 +528,7 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void grads(VocabGemm h, Voc
         const int id = tile_of(pid, tiles_h);
         if (id >= 0) tile_d_h<T, RUNS>(h, n_h, ph, id, lds);
     } else {
-        const int id = tile_of(pid - first, pw.mt * pw.nt);
+        const int id = tile_of(pid - first, pw.mt * pw.nt * w.splits);
         if (id >= 0) tile_d_w<T, RUNS>(w, count, pw, id, lds);
     }
 }
@@ -563,7 +582,7 @@ int launch_bwd(const VocabGemm& g, int terms, hipStream_t stream) {
 
 template <class T>
 unsigned grads_grid(const VocabGemm& h, const VocabGemm& w) {
-    return (unsigned)on_xcds(tiles(h.m, h.n, T::BM) * h.splits) + (unsigned)on_xcds(tiles(w.m, w.n, T::BM));
+    return (unsigned)on_xcds(tiles(h.m, h.n, T::BM) * h.splits) + (unsigned)on_xcds(tiles(w.m, w.n, T::BM) * w.splits);
 }
 
 template <class T>
@@ -579,16 +598,19 @@ int vocab_parts(const VocabGemm& g, int terms) {
     return big_logits(g, terms, kStatistics) ? (g.m + 255) / 256 * 2 : (g.m + 127) / 128 * 2;
 }
 
-// Splits of d_h's sum over the vocabulary: none longer than the work of a workgroup's
-// place, so that a long sum for few rows does not outlast all else.
-int vocab_splits(const VocabGemm& h, const VocabGemm& w, int terms) {
+// Parts of the sums: none much longer than the work of a workgroup's place, so that a
+// long sum for few tiles (d_h of few rows, d_w of a small vocabulary) does not outlast all
+// else.
+VocabParts vocab_grads_parts(const VocabGemm& h, const VocabGemm& w, int terms) {
     const bool big = big_grads(h, w, terms);
     const int tile = big ? 256 : 128;
-    const int64_t th = tiles(h.m, h.n, tile), tw = tiles(w.m, w.n, tile), steps = (h.k + 63) / 64;
-    int64_t share = (th * steps + tw * ((h.rows + 63) / 64)) / (big ? 256 : 512);
+    const int64_t th = tiles(h.m, h.n, tile), tw = tiles(w.m, w.n, tile);
+    const int64_t steps_h = (h.k + 63) / 64, steps_w = (h.rows + 63) / 64;
+    int64_t share = (th * steps_h + tw * steps_w) / (big ? 256 : 512);
     if (share < 8) share = 8;
-    const int64_t n = (steps + share - 1) / share;
-    return (int)(n < 1 ? 1 : n > kVocabSplits ? kVocabSplits : n);
+    auto parts = [&](int64_t n) { return (int)(n < 1 ? 1 : n > kVocabSplits ? kVocabSplits : n); };
+    // d_h's are joined by its last kernel in any case; d_w's take a kernel more
+    return {parts((steps_h + share - 1) / share), parts(steps_w / share)};
 }
 
 int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream) {

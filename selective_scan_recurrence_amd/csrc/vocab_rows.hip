@@ -424,27 +424,26 @@ __global__ __launch_bounds__(256) void patch_ids(VocabPatch p, int groups) {
         p.g[n * p.plane + (int64_t)c * p.ld_g + v] = p.gt[n * p.plane + (int64_t)v * p.r.Np + c] = t[n];
 }
 
-// Rows of d_h, four columns a lane; with many parts (few rows) LANES lanes share out a
-// column's, else a workgroup takes four rows.
+// Rows of a gradient, four columns a lane; with many parts (few rows) LANES lanes share
+// out a column's, else a workgroup takes four rows.
 template <int LANES>
-__global__ __launch_bounds__(LANES > 1 ? 64 * LANES : 256) void dh_rows(VocabDh d) {
+__global__ __launch_bounds__(LANES > 1 ? 64 * LANES : 256) void sum_rows(VocabSum d) {
     constexpr int kRows = LANES > 1 ? 1 : 4;
     const int x = threadIdx.x / 64, lane = LANES > 1 ? x : 0;
     const int64_t i = (int64_t)blockIdx.x * kRows + (LANES > 1 ? 0 : x);
     const int col = 4 * (64 * (int)blockIdx.y + (threadIdx.x & 63));
-    const bool mine = i < d.r.N && col < d.r.D;
+    const bool mine = i < d.n && col < d.D;
     if (LANES == 1 && !mine) return;
-    const int c = mine ? d.r.pos[i] : kRowOut;
+    const int64_t c = !mine ? kRowOut : d.pos ? d.pos[i] : i;
     const float fill = c == kRowBad ? __builtin_nanf("") : 0.0f;
     float v[4] = {fill, fill, fill, fill};
     if (c >= 0) {
         const float* from = d.acc + (int64_t)c * d.Dp + col;
-        const int64_t part = (int64_t)d.r.Np * d.Dp;
         for (int s = lane; s < d.parts; s += 8 * LANES) {
             float4 a[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-                a[y] = *reinterpret_cast<const float4*>(from + min(s + y * LANES, d.parts - 1) * part);
+                a[y] = *reinterpret_cast<const float4*>(from + min(s + y * LANES, d.parts - 1) * d.part);
 #pragma unroll
             for (int y = 0; y < 8; ++y)
                 if (s + y * LANES < d.parts) {
@@ -464,25 +463,9 @@ __global__ __launch_bounds__(LANES > 1 ? 64 * LANES : 256) void dh_rows(VocabDh 
         }
     }
     const int64_t at = i * d.ld + col;
-    const int left = d.r.D - col;
-    if (d.io == SSM_F32) {
-        float* to = static_cast<float*>(d.d_h) + at;
-        if (left >= 4) __builtin_memcpy(to, v, 16);
-        else
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < left) to[e] = v[e];
-    } else {
-        uint16_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = bf16_rne(v[e]);
-        uint16_t* to = static_cast<uint16_t*>(d.d_h) + at;
-        if (left >= 4) __builtin_memcpy(to, w, 8);
-        else
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < left) to[e] = w[e];
-    }
+    const int left = d.D - col;
+    if (d.dtype == SSM_F32) store_dw(static_cast<float*>(d.out) + at, v, left, d.accumulate);
+    else store_dw(static_cast<bf16_t*>(d.out) + at, v, left, d.accumulate);
 }
 
 unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
@@ -546,9 +529,9 @@ int launch_vocab_patch(const VocabPatch& p, hipStream_t stream) {
     return launched();
 }
 
-int launch_vocab_dh(const VocabDh& d, hipStream_t stream) {
-    if (d.parts > 16) dh_rows<16><<<dim3(d.r.N, blocks(d.r.D, 256)), 1024, 0, stream>>>(d);
-    else dh_rows<1><<<dim3(blocks(d.r.N, 4), blocks(d.r.D, 256)), 256, 0, stream>>>(d);
+int launch_vocab_sum(const VocabSum& d, hipStream_t stream) {
+    if (d.parts > 16) sum_rows<16><<<dim3(d.n, blocks(d.D, 256)), 1024, 0, stream>>>(d);
+    else sum_rows<1><<<dim3(blocks(d.n, 4), blocks(d.D, 256)), 256, 0, stream>>>(d);
     return launched();
 }
 

@@ -195,6 +195,29 @@ def test_big_tiles(io, top):
     compare(on_gpu, io, run(t, io, dw=io), dw=io)
 
 
+@pytest.mark.parametrize("spread,top", [(64, 40), (5, 12), (100, 70)])
+@pytest.mark.parametrize("n", [3, 70, 300])
+def test_ids_close_together(n, spread, top):
+    """Many ids of a row within a few neighbours of the vocabulary."""
+    t = R.problem(44, n, 64, 700, "bf16", top=top)
+    t["top_id"] = torch.where(t["top_id"] < 0, -1, 130 + t["top_id"] % spread).int()
+    if spread < top:  # entries with the same id hold the same logit's two shares
+        t["top_id"][:, spread:] = t["top_id"][:, :1]
+    compare(t, "bf16", run(t, "bf16"))
+
+
+@pytest.mark.parametrize("n,d,v,io,dw", [(3000, 70, 256, "bf16", "f32"), (3000, 130, 300, "bf16", "bf16"),
+                                         (1100, 65, 129, "f32", "f32"), (70, 65, 9000, "f32", "f32")])
+@pytest.mark.parametrize("add", [False, True])
+def test_long_sums_for_few_tiles(n, d, v, io, dw, add):
+    """Sums over many rows or a long vocabulary for small gradients, formed in parts."""
+    t = R.problem(45, n, d, v, io, out=0.1)
+    d_w0 = None
+    if add:
+        d_w0 = (0.01 * torch.randn(v, d, generator=torch.Generator().manual_seed(5))).to(R.DTYPES[dw])
+    compare(t, io, run(t, io, dw=dw, d_w0=d_w0, pad_w=3), dw=dw, d_w0=d_w0)
+
+
 @pytest.mark.parametrize("n", [3, 130])
 def test_weights_past_4_gigabytes(n):
     """W of 36000 x 65536: rows whose offset passes 32 bits.  All zero but for a value on
