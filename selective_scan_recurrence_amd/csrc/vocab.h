@@ -88,11 +88,23 @@ struct VocabPatch {
 };
 int launch_vocab_patch(const VocabPatch& p, hipStream_t stream);
 
+// The parts of d_h's sum over the vocabulary: `parts` for n rows, and as many more (up to
+// `most`) as the workgroups form that rows which are left out would have taken.
+struct VocabSplit {
+    const int32_t* count;
+    int n, tile, parts, most;
+    __device__ __forceinline__ int rows() const { return (min(n, *count) + tile - 1) / tile; }  // of tiles
+    __device__ __forceinline__ int of(int rows) const {
+        return max(min(parts * ((n + tile - 1) / tile) / max(rows, 1), most), 1);
+    }
+};
+
 // The sum over parts [parts][part / Dp][Dp], in the caller's tensor.
 struct VocabSum {
     const float* acc;
     int64_t part;
     int parts, Dp;
+    VocabSplit split;    // with a count: it says the parts, of whole tiles of rows
     const int32_t* pos;  // d_h: where row i's sum is, kRowOut (zero) or kRowBad (NaN); NULL: at i
     int n, D;            // of out
     int dtype;
@@ -119,21 +131,25 @@ struct VocabGemm {
     float* slog;
     const float *lse2, *coef;  // backward
     uint16_t *g, *gt;
-    // gradients: [splits] parts of k (d_h: f32 always), out_part values apart
+    // gradients: parts of k, each of whole tiles of rows (d_h, f32 always: how many is
+    // split's to say) or out_part values apart
     void* out;
     int64_t ld_out, out_part;
+    VocabSplit split;
     int splits, out_dtype;
     bool accumulate;
 };
 int vocab_parts(const VocabGemm& g, int terms);  // partials of a forward's logits, at most m / 64 + 4
-struct VocabParts {
+struct VocabParts {  // of the gradients' sums
     int d_h, d_w;
+    int most;  // d_h: at most, with rows left out
+    bool big;  // tiles
 };
 VocabParts vocab_grads_parts(const VocabGemm& d_h, const VocabGemm& d_w, int terms);
 int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream);
 int launch_vocab_logits_bwd(const VocabGemm& g, int terms, hipStream_t stream);
 // both products of the gradient (n = 0: not that one)
-int launch_vocab_grads(const VocabGemm& d_h, const VocabGemm& d_w, int terms, hipStream_t stream);
+int launch_vocab_grads(const VocabGemm& d_h, const VocabGemm& d_w, int terms, bool big, hipStream_t stream);
 
 // Up to 64 rows (Np = 64), h and W read where they lie.  Rows keep their places; one
 // that is left out has pos < 0.

@@ -59,25 +59,22 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
 struct Plan {
     int64_t Np, Kd, piece, ld;  // ld: row stride of what has the piece as columns
     int pieces;
-    VocabParts parts;  // of the gradients' sums
+    VocabParts parts;  // backward: set by the call
     bool few, packed;  // W goes through the workspace
     size_t count, rows, pos, kid, h, part, state, slog, w, ht, wt, g, gt, lse2, coef, at, acc, acc_w, bytes;
 };
 
 constexpr int64_t kPieceBytes = (int64_t)5 << 28;
 
-// for both products, d_h's also for d_h alone, whichever has more
-VocabParts parts_of(const VocabShape& s, const Plan& p) {
-    if (p.few) return {vocab_few_splits(p.piece, s.D), 1};
+VocabParts parts_of(const VocabShape& s, const Plan& p, bool d_h, bool d_w) {
+    if (p.few) return {vocab_few_splits(p.piece, s.D), 1, 1, false};
     VocabGemm h = {}, w = {};
     h.m = w.m = s.D;
-    h.n = h.rows = s.N;
+    h.n = d_h ? s.N : 0;
+    h.rows = s.N;
     h.k = (int)p.piece;
-    const int alone = vocab_grads_parts(h, w, s.terms).d_h;
-    w.n = (int)p.piece;
-    VocabParts n = vocab_grads_parts(h, w, s.terms);
-    n.d_h = n.d_h > alone ? n.d_h : alone;
-    return n;
+    w.n = d_w ? (int)p.piece : 0;
+    return vocab_grads_parts(h, w, s.terms);
 }
 
 Plan plan_of(const VocabShape& s, bool backward, bool packed) {
@@ -118,9 +115,15 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
         p.lse2 = take(p.Np * 4);
         p.coef = take(p.Np * 4);
         p.at = take(p.Np * s.K * 4);
-        p.parts = parts_of(s, p);
-        p.acc = take(p.parts.d_h * p.Np * p.Kd * 4);
-        p.acc_w = p.parts.d_w > 1 ? take(p.parts.d_w * p.piece * p.Kd * 4) : 0;
+        // of the three calls (both gradients, either alone) the one that takes the most
+        int64_t acc = 0, acc_w = 0;
+        for (int x = 1; x < 4; ++x) {
+            const VocabParts n = parts_of(s, p, x & 1, x & 2);
+            if (n.d_h > acc) acc = n.d_h;
+            if (n.d_w > acc_w) acc_w = n.d_w;
+        }
+        p.acc = take(acc * p.Np * p.Kd * 4);
+        p.acc_w = acc_w > 1 ? take(acc_w * p.piece * p.Kd * 4) : 0;
     } else {
         p.part = take(p.piece / (p.few ? 16 : 64) * p.Np * 8);
         p.state = take(p.Np * 8);
@@ -297,15 +300,21 @@ VocabGemm product_w(const Call& c, int64_t v0, int n, void* d_w) {
 
 int join_d_w(const Call& c, int64_t v0, int n, void* d_w) {
     const Plan& p = c.p;
-    return launch_vocab_sum({c.at<float>(p.acc_w), p.piece * p.Kd, p.parts.d_w, (int)p.Kd, nullptr, n, c.s.D, c.s.dw,
-                             static_cast<char*>(d_w) + v0 * c.s.ld_w * (int64_t)size_of(c.s.dw), c.s.ld_w,
+    return launch_vocab_sum({c.at<float>(p.acc_w), p.piece * p.Kd, p.parts.d_w, (int)p.Kd, {}, nullptr, n, c.s.D,
+                             c.s.dw, static_cast<char*>(d_w) + v0 * c.s.ld_w * (int64_t)size_of(c.s.dw), c.s.ld_w,
                              c.s.accumulate}, c.stream);
+}
+
+VocabSplit split_of(const Call& c) {
+    return {c.r.count, c.s.N, c.p.parts.big ? 256 : 128, c.p.parts.d_h, c.p.parts.most};
 }
 
 int join_d_h(const Call& c, void* d_h) {
     const Plan& p = c.p;
-    return launch_vocab_sum({c.at<float>(p.acc), p.Np * p.Kd, p.parts.d_h, (int)p.Kd, c.r.pos, c.s.N, c.s.D, c.s.io,
-                             d_h, c.s.ld_h, false}, c.stream);
+    VocabSum d = {c.at<float>(p.acc), p.Np * p.Kd, p.parts.d_h, (int)p.Kd, {}, c.r.pos, c.s.N, c.s.D, c.s.io,
+                  d_h, c.s.ld_h, false};
+    if (!p.few) d.split = split_of(c);
+    return launch_vocab_sum(d, c.stream);
 }
 
 VocabCoef factors(const Call& c, const float* logq, const float* loss, const float* lse, const float* d_loss,
@@ -367,9 +376,9 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
         gh.b = g; gh.b_plane = p.Np * p.ld; gh.ldb = p.ld;
         gh.m = s.D; gh.n = d_h ? s.N : 0; gh.rows = s.N; gh.k = (int)round_up(n, kVocabStep);
         gh.count = c.r.count; gh.Np = p.Np;
-        gh.out = c.at<float>(p.acc); gh.ld_out = p.Kd; gh.out_part = p.Np * p.Kd; gh.splits = p.parts.d_h;
+        gh.out = c.at<float>(p.acc); gh.ld_out = p.Kd; gh.split = split_of(c);
         gh.accumulate = x > 0;
-        RUN(launch_vocab_grads(gh, product_w(c, v0, n, d_w), s.terms, c.stream));
+        RUN(launch_vocab_grads(gh, product_w(c, v0, n, d_w), s.terms, p.parts.big, c.stream));
         if (d_w && p.parts.d_w > 1) RUN(join_d_w(c, v0, n, d_w));
     }
     return d_h ? join_d_h(c, d_h) : SSM_OK;
@@ -425,7 +434,8 @@ int ssm_vocab_ce_bwd(const ssm_vocab_desc* desc, const void* h, const void* w, c
     if (s.N > 0 && (!loss || !lse || !d_loss)) return SSM_ERR_NULL;
     if (!all_aligned(4, {loss, lse, d_loss, d_lse}) || !aligned(d_h, size_of(s.io)) || !aligned(d_w, size_of(s.dw)))
         return SSM_ERR_ALIGN;
-    const Call c = make_call(s, true, h, w, target, nullptr, nullptr, workspace, static_cast<hipStream_t>(stream));
+    Call c = make_call(s, true, h, w, target, nullptr, nullptr, workspace, static_cast<hipStream_t>(stream));
+    c.p.parts = parts_of(s, c.p, d_h, d_w);
     return backward(c, nullptr, loss, lse, d_loss, d_lse, d_h, d_w);
 }
 
@@ -455,7 +465,8 @@ int ssm_vocab_kd_bwd(const ssm_vocab_desc* desc, const void* h, const void* w, c
     if (!all_aligned(4, {top_logit, top_lse, logq, lse, d_loss, d_lse}) || !aligned(d_h, size_of(s.io)) ||
         !aligned(d_w, size_of(s.dw)))
         return SSM_ERR_ALIGN;
-    const Call c = make_call(s, true, h, w, top_id, top_logit, top_lse, workspace, static_cast<hipStream_t>(stream));
+    Call c = make_call(s, true, h, w, top_id, top_logit, top_lse, workspace, static_cast<hipStream_t>(stream));
+    c.p.parts = parts_of(s, c.p, d_h, d_w);
     return backward(c, logq, nullptr, lse, d_loss, d_lse, d_h, d_w);
 }
 

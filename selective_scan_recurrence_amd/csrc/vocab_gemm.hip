@@ -463,16 +463,17 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void logits_bwd(VocabGemm p
 }
 
 template <class T, int RUNS>
-__device__ __forceinline__ void tile_d_h(const VocabGemm& p, int n_rows, const Place& place, int id, uint8_t* lds) {
+__device__ __forceinline__ void tile_d_h(const VocabGemm& p, int n_rows, const Place& place, int parts, int id,
+                                         uint8_t* lds) {
     constexpr int TM = T::TM, TN = T::TN;
     int m0, n0;
     const int tiles = place.mt * place.nt, split = id / tiles, all = p.k / kVocabStep;
     place.of(id - split * tiles, &m0, &n0);
     f32x4 acc[TM][TN];
-    product<T, RUNS, 1>(p, m0 *= T::BM, n0 *= T::BN, n_rows, (int)((int64_t)all * split / p.splits),
-                        (int)((int64_t)all * (split + 1) / p.splits), lds, acc);
+    product<T, RUNS, 1>(p, m0 *= T::BM, n0 *= T::BN, n_rows, (int)((int64_t)all * split / parts),
+                        (int)((int64_t)all * (split + 1) / parts), lds, acc);
     const Lane<T, 1> l(m0, n0);
-    float* out = static_cast<float*>(p.out) + split * p.out_part;
+    float* out = static_cast<float*>(p.out) + (int64_t)split * place.nt * T::BN * p.ld_out;
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -523,10 +524,11 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void grads(VocabGemm h, Voc
     const Place ph = {(h.m + T::BM - 1) / T::BM, (n_h + T::BN - 1) / T::BN};
     const Place pw = {(w.m + T::BM - 1) / T::BM, (w.n + T::BN - 1) / T::BN};
     // every XCD takes its part of d_h, whose sums are longer as a rule, then of d_w
-    const int tiles_h = ph.mt * ph.nt * h.splits, pid = blockIdx.x, first = (int)on_xcds(tiles_h);
+    const int parts = h.split.of(ph.nt);
+    const int tiles_h = ph.mt * ph.nt * parts, pid = blockIdx.x, first = (int)on_xcds(tiles_h);
     if (pid < first) {
         const int id = tile_of(pid, tiles_h);
-        if (id >= 0) tile_d_h<T, RUNS>(h, n_h, ph, id, lds);
+        if (id >= 0) tile_d_h<T, RUNS>(h, n_h, ph, parts, id, lds);
     } else {
         const int id = tile_of(pid - first, pw.mt * pw.nt * w.splits);
         if (id >= 0) tile_d_w<T, RUNS>(w, count, pw, id, lds);
@@ -554,12 +556,27 @@ bool big_logits(const VocabGemm& g, int terms, Results r) {
     return big_tiles(tiles(g.m, g.n, 256), tiles(g.m, g.n, 128), steps, {r.big * terms, r.small * terms});
 }
 
-bool big_grads(const VocabGemm& h, const VocabGemm& w, int terms) {
-    const int64_t bh = tiles(h.m, h.n, 256), bw = tiles(w.m, w.n, 256);
-    // the mean of both sums' lengths
-    const double steps_h = h.k / kVocabStep, steps_w = (double)((h.rows + kVocabStep - 1) / kVocabStep);
-    const double steps = (terms == 3 ? 6 : 1) * (bh * steps_h + bw * steps_w) / (bh + bw);
-    return big_tiles(bh + bw, tiles(h.m, h.n, 128) + tiles(w.m, w.n, 128), steps, kSums);
+// Time until the last of nh workgroups of `a` us, and nw of `b` us after them in line,
+// leave `places`.
+double line_up(int64_t places, int64_t nh, double a, int64_t nw, double b) {
+    const int64_t rounds = nh / places, late = nh % places, early = places - late;
+    const double t0 = rounds * a, t1 = late ? t0 + a : t0;
+    double t = t1;
+    if (nw > 0) {
+        // from the time that a perfect fit would take to the first with room for all
+        const double least = (nw * b + early * t0 + late * t1) / places;
+        int64_t j = (int64_t)((least - t0) / b);
+        for (;; ++j) {
+            const double e = t0 + j * b + 1e-6;
+            const int64_t then = e > t1 ? (int64_t)((e - t1) / b) : 0;
+            t = e;
+            if (early * j + late * then >= nw) break;
+            // the late places' next end, when it comes before the early ones'
+            t = t1 + (then + 1) * b;
+            if (t < e + b && early * j + late * (then + 1) >= nw) break;
+        }
+    }
+    return t > t1 ? t : t1;
 }
 
 int launched() { return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
@@ -582,7 +599,7 @@ int launch_bwd(const VocabGemm& g, int terms, hipStream_t stream) {
 
 template <class T>
 unsigned grads_grid(const VocabGemm& h, const VocabGemm& w) {
-    return (unsigned)on_xcds(tiles(h.m, h.n, T::BM) * h.splits) + (unsigned)on_xcds(tiles(w.m, w.n, T::BM) * w.splits);
+    return (unsigned)on_xcds(tiles(h.m, h.n, T::BM) * h.split.parts) + (unsigned)on_xcds(tiles(w.m, w.n, T::BM) * w.splits);
 }
 
 template <class T>
@@ -598,19 +615,47 @@ int vocab_parts(const VocabGemm& g, int terms) {
     return big_logits(g, terms, kStatistics) ? (g.m + 255) / 256 * 2 : (g.m + 127) / 128 * 2;
 }
 
-// Parts of the sums: none much longer than the work of a workgroup's place, so that a
-// long sum for few tiles (d_h of few rows, d_w of a small vocabulary) does not outlast all
-// else.
+// A launch of both sums: tiles, and parts of either sum, so that a long sum for few tiles
+// (d_h of few rows, d_w of a small vocabulary) does not outlast all else, nor a last round
+// of tiles leave most compute units idle.  f32, 1023 rows, width 771, vocabulary 10007: 204
+// us, with a share of d_h for every compute unit 277.
 VocabParts vocab_grads_parts(const VocabGemm& h, const VocabGemm& w, int terms) {
-    const bool big = big_grads(h, w, terms);
-    const int tile = big ? 256 : 128;
-    const int64_t th = tiles(h.m, h.n, tile), tw = tiles(w.m, w.n, tile);
-    const int64_t steps_h = (h.k + 63) / 64, steps_w = (h.rows + 63) / 64;
-    int64_t share = (th * steps_h + tw * steps_w) / (big ? 256 : 512);
-    if (share < 8) share = 8;
-    auto parts = [&](int64_t n) { return (int)(n < 1 ? 1 : n > kVocabSplits ? kVocabSplits : n); };
-    // d_h's are joined by its last kernel in any case; d_w's take a kernel more
-    return {parts((steps_h + share - 1) / share), parts(steps_w / share)};
+    VocabParts best = {1, 1, 1, true};
+    double least = 1e30;
+    const int64_t steps_h = (h.k + 63) / 64, steps_w = (h.rows + 63) / 64, runs = terms == 3 ? 6 : 1;
+    const int64_t most = steps_h / 4 < 1 ? 1 : steps_h / 4 < kVocabSplits ? steps_h / 4 : kVocabSplits;
+    for (const bool big : {true, false}) {
+        const int tile = big ? 256 : 128;
+        const int64_t th = tiles(h.m, h.n, tile), tw = tiles(w.m, w.n, tile), places = big ? 256 : 512;
+        // a workgroup's fair share of steps
+        double share = (double)(th * steps_h + tw * steps_w) / places;
+        if (share < 8) share = 8;
+        const double even = th > 0 ? steps_h / share : 1;
+        for (int x = 0; x < 8; ++x) {
+            VocabParts p = {(int)(even * (0.5 + 0.25 * x) + 0.5), 1, (int)most, big};
+            if (p.d_h < 1) p.d_h = 1;
+            if (p.d_h > most) break;
+            for (int y = 0; y < 2; ++y) {
+                if (y == 1) {
+                    p.d_w = tw > 0 ? (int)(steps_w / share) : 1;
+                    if (p.d_w <= 1) break;
+                    if (p.d_w > kVocabSplits) p.d_w = kVocabSplits;
+                }
+                const int64_t nh = th * p.d_h, nw = tw * p.d_w;
+                // alone on its compute unit a small tile's step takes 0.54 us
+                const double step = big ? 1.48 : nh + nw <= 256 ? 0.54 : 0.88, rest = big ? kSums.big : kSums.small;
+                const double a = (step * runs * steps_h) / p.d_h + rest, b = (step * runs * steps_w) / p.d_w + rest;
+                // parts of d_w take a kernel more; a part's read and write, at 4.5 TB/s
+                const double kept = (p.d_h - 1) * (double)h.m * h.n + (p.d_w > 1 ? p.d_w * (double)w.m * w.n : 0.0);
+                const double t = line_up(places, nh, a, nw, b) + (p.d_w > 1 ? 4 : 0) + 8e-6 / 4.5 * kept;
+                if (t < least) {
+                    least = t;
+                    best = p;
+                }
+            }
+        }
+    }
+    return best;
 }
 
 int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream) {
@@ -621,8 +666,8 @@ int launch_vocab_logits_bwd(const VocabGemm& g, int terms, hipStream_t stream) {
     return big_logits(g, terms, kBothOrders) ? launch_bwd<Big>(g, terms, stream) : launch_bwd<Small>(g, terms, stream);
 }
 
-int launch_vocab_grads(const VocabGemm& h, const VocabGemm& w, int terms, hipStream_t stream) {
-    return big_grads(h, w, terms) ? launch_grads<Big>(h, w, terms, stream) : launch_grads<Small>(h, w, terms, stream);
+int launch_vocab_grads(const VocabGemm& h, const VocabGemm& w, int terms, bool big, hipStream_t stream) {
+    return big ? launch_grads<Big>(h, w, terms, stream) : launch_grads<Small>(h, w, terms, stream);
 }
 
 }  // namespace ssm

@@ -429,7 +429,7 @@ __global__ __launch_bounds__(256) void patch_ids(VocabPatch p, int groups) {
 template <int LANES>
 __global__ __launch_bounds__(LANES > 1 ? 64 * LANES : 256) void sum_rows(VocabSum d) {
     constexpr int kRows = LANES > 1 ? 1 : 4;
-    const int x = threadIdx.x / 64, lane = LANES > 1 ? x : 0;
+    const int x = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = LANES > 1 ? x : 0;
     const int64_t i = (int64_t)blockIdx.x * kRows + (LANES > 1 ? 0 : x);
     const int col = 4 * (64 * (int)blockIdx.y + (threadIdx.x & 63));
     const bool mine = i < d.n && col < d.D;
@@ -439,14 +439,21 @@ __global__ __launch_bounds__(LANES > 1 ? 64 * LANES : 256) void sum_rows(VocabSu
     float v[4] = {fill, fill, fill, fill};
     if (c >= 0) {
         const float* from = d.acc + (int64_t)c * d.Dp + col;
-        for (int s = lane; s < d.parts; s += 8 * LANES) {
+        int parts = d.parts;
+        int64_t part = d.part;
+        if (d.split.count) {
+            const int rows = d.split.rows();
+            parts = d.split.of(rows);
+            part = (int64_t)rows * d.split.tile * d.Dp;
+        }
+        for (int s = lane; s < parts; s += 8 * LANES) {
             float4 a[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-                a[y] = *reinterpret_cast<const float4*>(from + min(s + y * LANES, d.parts - 1) * d.part);
+                if (s + y * LANES < parts) a[y] = *reinterpret_cast<const float4*>(from + (s + y * LANES) * part);
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-                if (s + y * LANES < d.parts) {
+                if (s + y * LANES < parts) {
                     v[0] += a[y].x; v[1] += a[y].y; v[2] += a[y].z; v[3] += a[y].w;
                 }
         }

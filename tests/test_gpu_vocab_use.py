@@ -208,10 +208,11 @@ def test_ids_close_together(n, spread, top):
 
 @pytest.mark.parametrize("n,d,v,io,dw", [(3000, 70, 256, "bf16", "f32"), (3000, 130, 300, "bf16", "bf16"),
                                          (1100, 65, 129, "f32", "f32"), (70, 65, 9000, "f32", "f32")])
-@pytest.mark.parametrize("add", [False, True])
-def test_long_sums_for_few_tiles(n, d, v, io, dw, add):
-    """Sums over many rows or a long vocabulary for small gradients, formed in parts."""
-    t = R.problem(45, n, d, v, io, out=0.1)
+@pytest.mark.parametrize("add,out", [(False, 0.1), (True, 0.1), (False, 0.9)])
+def test_long_sums_for_few_tiles(n, d, v, io, dw, add, out):
+    """Sums over many rows or a long vocabulary for small gradients, formed in parts: the
+    more of them the more rows are left out."""
+    t = R.problem(45, n, d, v, io, out=out)
     d_w0 = None
     if add:
         d_w0 = (0.01 * torch.randn(v, d, generator=torch.Generator().manual_seed(5))).to(R.DTYPES[dw])
