@@ -213,6 +213,14 @@ __device__ __forceinline__ void store_dw(E* to, float (&v)[V], int left, bool ac
             if (r < left) to[r] = w[r];
 }
 
+// Joins two partials of a softmax: a maximum, and the sum of exp2 of what is over it.
+__device__ __forceinline__ void merge(float& m, float& s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    // an infinite sum stays one whatever it is scaled by
+    s = (s < __builtin_inff() ? s * fast_exp2(m - top) : s) + (s2 < __builtin_inff() ? s2 * fast_exp2(m2 - top) : s2);
+    m = top;
+}
+
 // v's next bf16 term, of TERMS in all; v keeps the rest.  One: v rounded.  Two: that,
 // and the rest rounded (2^-17 of v is left).  Three: v itself, each term what the ones
 // before leave with the low half cut off, so that no rounding passes the largest

@@ -87,7 +87,7 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
     const int64_t T = s.terms, V = round_up(s.V, kVocabTile);
     // bytes a vocabulary entry of a piece
     int64_t each = packed ? T * p.Kd * 2 : 0;
-    each += backward ? 4 * s.g_terms * p.Np + (p.few ? 0 : 2 * T * p.Kd) : p.Np / (p.few ? 2 : 8);
+    each += backward ? 4 * s.g_terms * p.Np + (p.few ? 0 : 2 * T * p.Kd) : p.Np / (p.few ? 4 : 8);
     int64_t most = kPieceBytes / each / kVocabTile * kVocabTile;
     if (most < kVocabTile) most = kVocabTile;
     p.pieces = (int)((V + most - 1) / most);
@@ -125,7 +125,7 @@ Plan plan_of(const VocabShape& s, bool backward, bool packed) {
         p.acc = take(acc * p.Np * p.Kd * 4);
         p.acc_w = acc_w > 1 ? take(acc_w * p.piece * p.Kd * 4) : 0;
     } else {
-        p.part = take(p.piece / (p.few ? 16 : 64) * p.Np * 8);
+        p.part = take(p.piece / (p.few ? 32 : 64) * p.Np * 8);
         p.state = take(p.Np * 8);
         p.slog = take(p.Np * s.K * 4);
     }

@@ -94,70 +94,17 @@ __device__ __forceinline__ void load_h(const VocabFew& p, int n, int k, u32x4 (&
 }
 
 // ---- the logits -----------------------------------------------------------------
-// A workgroup of 8 waves owns 8 / KW groups of M = 16 MT of the vocabulary and all rows
-// (16 NT of them).  The KW waves of a group share out the width in chunks of 64, a lane
-// reading 16 neighbouring values of a row, so that four lanes take a 128-byte line
-// (bf16), and add up through LDS.  Eight waves a group read h least often; two are for
-// widths of a few chunks, where the adding up would take longer than the reading.
-template <typename E, int MT, int NT, int KW, bool BWD>
-__global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
-    constexpr int T = kTerms<E>, M = 16 * MT, N = 16 * NT, kLanes = 64 * KW / N, LPT = kLanes < M ? kLanes : M;
-    constexpr int VPT = M / LPT, kRow = M + 4;
-    __shared__ __attribute__((aligned(16))) float sums[8 / KW][KW][N][kRow];
+// A group of KW waves has the sums of its 16 of the vocabulary from m0 of the piece in
+// `red`, in KW parts.  Forward: a partial for the workgroup, and the logits at the rows'
+// ids; backward: g in both orders.
+constexpr int kM = 16, kRow = kM + 4;
+template <int T, int NT, int KW, bool BWD>
+__device__ __forceinline__ void finish(const VocabFew& p, float (&red)[KW][16 * NT][kRow], int m0) {
+    constexpr int M = kM, N = 16 * NT, kLanes = 64 * KW / N, LPT = kLanes < M ? kLanes : M, VPT = M / LPT;
+    constexpr int kGroups = 8 / KW;
     const VocabRows& r = p.r;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, i16 = lane & 15;
-    const int group = wave / KW, part = wave % KW, tid = threadIdx.x % (64 * KW);  // in the group
-    float (&red)[KW][N][kRow] = sums[group];
-    const int block = blockIdx.x * (8 / KW) + group, m0 = block * M;  // in the piece
-    const E* w[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        w[t] = static_cast<const E*>(p.w) + (int64_t)min(p.v0 + m0 + 16 * t + i16, r.V - 1) * p.ld_w;
-    f32x4 acc[MT][NT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
-    Raw<E> next[MT];
-    int k = 64 * part + 16 * q;
-    if (64 * part < r.D)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) next[t].load(w[t], k, r.D);
-    for (; k - 16 * q < r.D; k += 64 * KW) {
-        Raw<E> cur[MT];
-        // in f32 half of h at a time, for its registers
-        constexpr int H = T == 3 ? 1 : 2;
-        u32x4 x[H][NT][T];
-        auto load_x = [&](int half) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) load_h<E>(p, min(16 * j + i16, r.N - 1), k + 8 * half, x[half % H][j]);
-        };
-        load_x(0);
-        if constexpr (H == 2) load_x(1);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            cur[t] = next[t];
-            if (k - 16 * q + 64 * KW < r.D) next[t].load(w[t], k + 64 * KW, r.D);
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (half >= H) load_x(half);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                u32x4 a[T];
-                cur[t].operand(half, a);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc[t][j] = products<T, T>(a, x[half % H][j], acc[t][j]);
-            }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<f32x4*>(&red[part][16 * j + i16][16 * t + 4 * q]) = acc[t][j];
-    __syncthreads();
-
+    const int group = threadIdx.x / (64 * KW), tid = threadIdx.x % (64 * KW);
+    __shared__ float2 joined[kGroups][N];  // forward
     // LPT lanes of a wave share a row, with every LPT-th of its logits each
     const int n = tid / LPT, l = tid % LPT;
     const int there = min(M, r.V - p.v0 - m0);  // of the vocabulary: none or less past its end
@@ -188,7 +135,12 @@ __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
             for (int x = 0; x < VPT; ++x) s += fast_exp2(s2[x] - m);
 #pragma unroll
             for (int d = 1; d < LPT; d *= 2) s += __shfl_xor(s, d);
-            if (l == 0) p.part[(int64_t)block * r.Np + n] = make_float2(none ? -0x1p127f : m, s);
+            const float2 own = make_float2(none ? -0x1p127f : m, s);
+            if constexpr (kGroups > 1) {
+                if (l == 0) joined[group][n] = own;
+            } else if (l == 0) {
+                p.part[(int64_t)blockIdx.x * r.Np + n] = own;
+            }
         } else {
             const bool out = n >= r.N || r.pos[n] < 0;
             const float a = out ? 0.0f : p.coef[n], lse2 = out ? 0.0f : p.lse2[n];
@@ -208,6 +160,16 @@ __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
                 if constexpr (!BWD) p.slog[(int64_t)y * r.Np + n] = red[0][n][at];
                 else if (r.pos[n] >= 0) red[0][n][at] = p.at[(int64_t)y * r.Np + n];
             }
+    }
+    if constexpr (!BWD && kGroups > 1) {
+        __syncthreads();
+        if (threadIdx.x < N) {
+            float2 all = joined[0][threadIdx.x];
+#pragma unroll
+            for (int g = 1; g < kGroups; ++g)  // of those that lie in the piece
+                if (m0 - M * group + M * g < p.P) merge(all.x, all.y, joined[g][threadIdx.x].x, joined[g][threadIdx.x].y);
+            p.part[(int64_t)blockIdx.x * r.Np + threadIdx.x] = all;
+        }
     }
     if constexpr (BWD) {
         __syncthreads();
@@ -240,6 +202,97 @@ __global__ __launch_bounds__(512, 2) void few_logits(VocabFew p) {
             }
         }
     }
+}
+
+// A workgroup of 8 waves owns 8 / KW groups of 16 of the vocabulary and all rows (16 NT of
+// them).  The KW waves of a group share out the width in chunks of 64, a lane reading 16
+// neighbouring values of a row of W, so that four lanes take a 128-byte line (bf16), and
+// add up through LDS.  Waves with the same part of the width share h's chunk through LDS,
+// in pieces of 16 bytes swizzled by their row: 64 rows, width 2560, vocabulary 32000: 67
+// us with h read by every wave, 35 so.  W's chunks and h's are read two steps ahead: more
+// take the registers that two workgroups a compute unit have.
+template <typename E, int NT, int KW, bool BWD>
+__global__ __launch_bounds__(512, kTerms<E> == 1 ? 4 : 2) void few_logits(VocabFew p) {
+    constexpr int T = kTerms<E>, N = 16 * NT, kStage = KW * T * N * 128, kRed = 8 * N * kRow * 4;
+    constexpr int kPieces = KW * T * N * 8, X = (kPieces + 511) / 512, kAhead = 2;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage > kRed ? 2 * kStage : kRed];
+    const VocabRows& r = p.r;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
+    const int i16 = lane & 15, group = wave / KW, part = wave % KW;
+    const int m0 = (blockIdx.x * (8 / KW) + group) * 16;  // in the piece
+    const E* w = static_cast<const E*>(p.w) + (int64_t)min(p.v0 + m0 + i16, r.V - 1) * p.ld_w;
+    const int steps = (r.D + 64 * KW - 1) / (64 * KW);
+    Raw<E> ring[kAhead];
+    u32x4 hold[kAhead][X];
+    auto fetch = [&](int s, Raw<E>& a, u32x4 (&h)[X]) {
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+            const int at = threadIdx.x + 512 * x, n = min(at / 8 % N, r.N - 1), t = at / (8 * N) % T;
+            const int k = 64 * (s * KW + at / (8 * N * T)) + 8 * (at % 8);
+            if (kPieces % 512 && at >= kPieces) continue;
+            if constexpr (T == 1) {
+                u32x4 v[1];
+                load_h<E>(p, n, k, v);
+                h[x] = v[0];
+            } else {
+                const int64_t Kd = (r.D + 63) / 64 * 64;
+                h[x] = k < Kd ? *reinterpret_cast<const u32x4*>(p.hp + (t * r.Np + n) * Kd + k) : u32x4{0, 0, 0, 0};
+            }
+        }
+        a.load(w, 64 * (s * KW + part) + 16 * q, r.D);
+    };
+    auto put = [&](const u32x4 (&h)[X], uint8_t* to) {
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+            const int at = threadIdx.x + 512 * x, row = at / 8;
+            if (kPieces % 512 && at >= kPieces) continue;
+            *reinterpret_cast<u32x4*>(to + row * 128 + 16 * ((at ^ row) & 7)) = h[x];
+        }
+    };
+    f32x4 acc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        if (u < steps) fetch(u, ring[u], hold[u]);
+    put(hold[0], lds);
+    __syncthreads();
+    for (int s0 = 0; s0 < steps; s0 += kAhead)
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int s = s0 + u;
+            if (s < steps) {
+                if (s + 1 < steps) put(hold[(u + 1) % kAhead], lds + (u + 1) % 2 * kStage);
+                const Raw<E> cur = ring[u];
+                if (s + kAhead < steps) fetch(s + kAhead, ring[u], hold[u]);
+                const uint8_t* from = lds + u % 2 * kStage + part * (T * N * 128);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    u32x4 a[T], x[T][NT];
+                    cur.operand(half, a);
+#pragma unroll
+                    for (int t = 0; t < T; ++t)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+                            x[t][j] = *reinterpret_cast<const u32x4*>(from + (t * N + 16 * j + i16) * 128 +
+                                                                      16 * ((2 * q + half) ^ (i16 & 7)));
+                    // products' order, rows by turns: no product waits for the one before it
+#pragma unroll
+                    for (int y = T == 1 ? 5 : 0; y < 6; ++y)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const int ta = (0x001102 >> (4 * y)) & 15, tb = (0x010120 >> (4 * y)) & 15;
+                            acc[j] = mfma(a[ta], x[tb][j], acc[j]);
+                        }
+                }
+                __syncthreads();
+            }
+        }
+    float (&red)[KW][N][kRow] = reinterpret_cast<float (*)[KW][N][kRow]>(lds)[group];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4*>(&red[part][16 * j + i16][4 * q]) = acc[j];
+    __syncthreads();
+    finish<T, NT, KW, BWD>(p, red, m0);
 }
 
 // ---- d_h ------------------------------------------------------------------------
@@ -275,7 +328,7 @@ __global__ __launch_bounds__(256, 2) void few_d_h(VocabFew p) {
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int t = 0; t < GT; ++t) {
-                // written to the end of a workgroup's 16 MT of the vocabulary
+                // written to the end of a group's 16 of the vocabulary
                 const u32x4 x = *reinterpret_cast<const u32x4*>(p.g + t * plane + (int64_t)(16 * j + i16) * p.P + v);
                 s.g[j][t] = v < rows ? x : u32x4{0, 0, 0, 0};
             }
@@ -408,45 +461,35 @@ __global__ __launch_bounds__(256, 2) void few_d_w(VocabFew p) {
     }
 }
 
-// How the logits are shared out: 16 mt of the vocabulary a group, the more the fewer
-// times h is read, as long as there are enough workgroups; and kw waves a group.
+// How the logits are shared out: 16 nt rows, and the least kw waves a group that leave
+// every compute unit a workgroup.  (64 rows, width 2560, vocabulary 32000: 60 us with 1, 41
+// with 2, 50 with 4; vocabulary 131072: 153, 173 and 219.)
 struct FewTile {
-    int mt, nt, kw;
+    int nt, kw;
 };
 FewTile few_tile(const VocabRows& r) {
-    FewTile f;
-    f.nt = r.N <= 16 ? 1 : r.N <= 32 ? 2 : 4;
-    const int most = r.terms == 3 || f.nt > 2 ? 2 : 4;
-    f.kw = r.D <= 1024 && r.V >= 64 * 256 ? 2 : 8;
-    f.mt = 1;
-    while (f.mt < most && r.V / (32 * f.mt * (8 / f.kw)) >= 400) f.mt *= 2;
+    FewTile f = {r.N <= 16 ? 1 : r.N <= 32 ? 2 : 4, 1};
+    // four take 192 KB of LDS for 64 rows in f32
+    const int most = r.terms == 3 && f.nt == 4 ? 2 : 4;
+    while (f.kw < most && 64 * f.kw < r.D && (int64_t)r.V * f.kw < 128 * 300) f.kw *= 2;
     return f;
 }
 
-template <typename E, int MT, int NT, bool BWD>
-void start(const VocabFew& p, int kw, int v, hipStream_t stream) {
-    constexpr int M = 16 * MT;
-    if (kw == 8) few_logits<E, MT, NT, 8, BWD><<<(v + M - 1) / M, 512, 0, stream>>>(p);
-    else few_logits<E, MT, NT, 2, BWD><<<(v + 4 * M - 1) / (4 * M), 512, 0, stream>>>(p);
-}
-
 template <typename E, int NT, bool BWD>
-void start(const VocabFew& p, const FewTile& f, int v, hipStream_t stream) {
-    if (f.mt == 1) start<E, 1, NT, BWD>(p, f.kw, v, stream);
-    else if (f.mt == 4) {
-        if constexpr (sizeof(E) == 2 && NT <= 2) start<E, 4, NT, BWD>(p, f.kw, v, stream);
-    } else {
-        start<E, 2, NT, BWD>(p, f.kw, v, stream);
-    }
+void start(const VocabFew& p, int kw, int v, hipStream_t stream) {
+    const unsigned grid = (v + 128 / kw - 1) / (128 / kw);
+    if (kw == 1) few_logits<E, NT, 1, BWD><<<grid, 512, 0, stream>>>(p);
+    else if (kw == 2) few_logits<E, NT, 2, BWD><<<grid, 512, 0, stream>>>(p);
+    else if constexpr (sizeof(E) == 2 || NT < 4) few_logits<E, NT, 4, BWD><<<grid, 512, 0, stream>>>(p);
 }
 
 template <typename E, bool BWD>
 int launch_logits(const VocabFew& p, hipStream_t stream) {
     const FewTile f = few_tile(p.r);
     const int v = p.r.V - p.v0 < p.P ? p.r.V - p.v0 : p.P;
-    if (f.nt == 1) start<E, 1, BWD>(p, f, v, stream);
-    else if (f.nt == 2) start<E, 2, BWD>(p, f, v, stream);
-    else start<E, 4, BWD>(p, f, v, stream);
+    if (f.nt == 1) start<E, 1, BWD>(p, f.kw, v, stream);
+    else if (f.nt == 2) start<E, 2, BWD>(p, f.kw, v, stream);
+    else start<E, 4, BWD>(p, f.kw, v, stream);
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
@@ -476,7 +519,7 @@ int launch_d_w(const VocabFew& p, hipStream_t stream) {
 
 }  // namespace
 
-int vocab_few_part(const VocabRows& r) { return 16 * few_tile(r).mt; }
+int vocab_few_part(const VocabRows& r) { return 128 / few_tile(r).kw; }
 
 // Parts of d_h's sum over the vocabulary, of 4 steps at least: four workgroups a compute
 // unit, and not many more, since every part is written and read again.

@@ -226,13 +226,6 @@ __device__ __forceinline__ float top_offset(const VocabRows& r, int64_t i, int l
 
 // ---- softmax statistics ----------------------------------------------------------
 
-__device__ __forceinline__ void merge(float& m, float& s, float m2, float s2) {
-    const float top = fmaxf(m, m2);
-    // an infinite sum stays one whatever it is scaled by
-    s = (s < __builtin_inff() ? s * fast_exp2(m - top) : s) + (s2 < __builtin_inff() ? s2 * fast_exp2(m2 - top) : s2);
-    m = top;
-}
-
 // sums over the LANES lanes of a row, 8, 64 or a whole workgroup
 template <int LANES, typename Combine>
 __device__ __forceinline__ void combine_lanes(float& m, float& s, Combine combine) {
