@@ -530,7 +530,7 @@ int ssm_norm_residual_bwd(const ssm_norm_desc *desc, const void *dh, const void 
  *
  * Rows without a target (target < 0; no entry with an id >= 0 and a logit above
  * -inf) are left out: loss, lse and logq are 0, d_h is 0, and their rows of h,
- * d_loss and d_lse are not read, so they may hold anything.  A row with a target
+ * d_loss and d_lse may hold anything.  A row with a target
  * or an id of n_vocab or more has loss, lse, logq and d_h NaN, adds nothing to
  * d_W, and sets SSM_DEVERR_TARGET in *err (a device word, NULL: dropped).  Entries
  * with the same id add up; an absent entry's logq is 0.
@@ -538,12 +538,12 @@ int ssm_norm_residual_bwd(const ssm_norm_desc *desc, const void *dh, const void 
  * Products of bf16 values are exact and summed in f32; in f32 they are formed of
  * three bf16 terms a value and are off by at most 2^-21 of the product (an
  * infinity may come out as NaN; parts below 2^-126 may count as zero).  g enters
- * its two products in the io type's terms: with bf16 io it is rounded to bf16, as
- * the outputs are, also when d_W is f32.  Sums have a fixed order: results repeat
- * bitwise. */
+ * its two products in such terms: three in f32; with bf16 io one, g rounded to bf16
+ * as the outputs are, also when d_W is f32, or, up to 64 rows, two (2^-17 of g is
+ * left).  Sums have a fixed order: results repeat bitwise. */
 typedef struct ssm_vocab_desc {
     int64_t n_rows;     /* 0..2^21                                               */
-    int64_t width;      /* 1..2^16                                               */
+    int64_t width;      /* 1..2^16; n_rows * width at most 2^34                  */
     int64_t n_vocab;    /* 1..2^24                                               */
     int64_t n_top;      /* teacher's entries a row, 1..1024; cross entropy: 0    */
     int64_t ld_h;       /* row strides of h and d_h, and of w and d_w, in        */

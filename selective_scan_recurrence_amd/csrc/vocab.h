@@ -11,10 +11,8 @@
 
 namespace ssm {
 
-// The products' tiles: 64 of the summed axis a step, waves of 64 columns (n)
-// by 64 or 128 rows (m).
-constexpr int kVocabStep = 64;
-constexpr int kVocabTile = 256;  // what tensors in the workspace are padded to
+constexpr int kVocabStep = 64;    // of the summed axis, a step of the products' tiles
+constexpr int kVocabTile = 256;   // what tensors in the workspace are padded to
 constexpr int kVocabSplits = 64;  // parts of a gradient's sum, at most
 
 // What the small kernels need of a call.  `rows` are the rows that count, in

@@ -22,7 +22,7 @@ int64_t off_channels(int64_t v) { return v % 2048 ? v : v + 256; }
 
 struct VocabShape {
     int N, D, V, K, top;
-    int g_terms;  // bf16 terms of g: see few rows
+    int g_terms;  // bf16 terms of g
     int64_t ld_h, ld_w;
     int io, dw, terms;
     float scale, top_scale;
@@ -36,6 +36,8 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
     if (d->n_rows < 0 || d->n_rows > 1 << 21 || d->width < 1 || d->width > 1 << 16 || d->n_vocab < 1 ||
         d->n_vocab > 1 << 24 || d->n_top < 0 || d->n_top > 1024)
         return SSM_ERR_SHAPE;
+    // a launch has under 2^32 lanes, and h is packed 8 values a lane
+    if (d->n_rows * d->width > (int64_t)1 << 34) return SSM_ERR_SHAPE;
     VocabShape s;
     s.N = (int)d->n_rows; s.D = (int)d->width; s.V = (int)d->n_vocab;
     s.top = (int)d->n_top; s.K = s.top ? s.top : 1;
@@ -55,7 +57,7 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
 // Where a call keeps what in its workspace, and the vocabulary's pieces.  A
 // piece's tensors take up to 1.25 GiB: with 16384 rows in bf16 that is 16384
 // of the vocabulary, long enough a sum that adding to d_h once a piece costs
-// little (a piece's d_h product takes over a millisecond, the addition 0.07).
+// little (a piece's two gradients take 2 ms, the addition 0.07).
 struct Plan {
     int64_t Np, Kd, piece, ld;  // ld: row stride of what has the piece as columns
     int pieces;

@@ -18,8 +18,9 @@
 // % 16) ends with 4 S neighbouring m from 4 S q.  S = 2 where they leave in bf16, 1
 // in f32: the 4 lanes of a row of out then store 64 neighbouring bytes (with 16 m a
 // lane, which leave in two stores of every second 16 bytes, the backward's logits of
-// 16384 x 16384 rows, width 2560, took 1340 us instead of 1130).  Tile j of a wave's TN
-// tiles of B takes the rows TN i + j: TN neighbouring n a lane for g's other order.
+// 16384 x 16384 rows, width 2560, took 1340 us, so 1220, and past the caches 1095).
+// Tile j of a wave's TN tiles of B takes the rows TN i + j: TN neighbouring n a lane
+// for g's other order.
 //
 // The big tile has one wave a SIMD with 64 accumulators of 4 registers each, a
 // quarter fewer bytes from LDS than eight waves of 128 x 64.  That counts because

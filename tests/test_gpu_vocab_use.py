@@ -195,6 +195,46 @@ def test_big_tiles(io, top):
     compare(on_gpu, io, run(t, io, dw=io), dw=io)
 
 
+@pytest.mark.parametrize("n,d,v,io,top", [
+    (1, 64, 40, "bf16", 0), (17, 130, 5000, "bf16", 3), (64, 65, 300, "f32", 0), (65, 65, 129, "bf16", 0),
+    (300, 70, 5000, "f32", 5), (130, 200, 30000, "bf16", 0), (5000, 33, 300, "bf16", 2), (2048, 96, 2100, "f32", 0),
+])
+@pytest.mark.parametrize("only", ["d_h", "d_w", None])
+def test_nothing_behind_the_workspace_is_written(n, d, v, io, top, only):
+    t = _on_gpu(n, d, v, io, top)
+    desc = ops.vocab_desc(n_rows=n, width=d, n_vocab=v, n_top=top, io=io)
+    for backward in (False, True):
+        size = ops.vocab_workspace(desc, backward).numel()
+        whole = torch.full((size + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+        ws = whole[:size]
+        if top:
+            f = ops.vocab_kd_fwd(desc, t["h"], t["w"], t["top_id"], t["top_logit"], ws=ws)
+        else:
+            f = ops.vocab_ce_fwd(desc, t["h"], t["w"], t["target"], ws=ws)
+        if backward:
+            kw = dict(ws=ws, want_h=only != "d_w", want_w=only != "d_h")
+            if top:
+                ops.vocab_kd_bwd(desc, t["h"], t["w"], t["top_id"], t["top_logit"], f.logq, f.lse, t["d_loss"], **kw)
+            else:
+                ops.vocab_ce_bwd(desc, t["h"], t["w"], t["target"], f.loss, f.lse, t["d_loss"], **kw)
+        assert bool((whole[size:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("n,d,v,io", [(40, 70, 3000, "bf16"), (3000, 70, 300, "bf16"), (300, 70, 5000, "f32")])
+def test_either_gradient_alone(n, d, v, io):
+    """Its parts may be others than with both: the same values within the bounds."""
+    t = R.problem(46, n, d, v, io, out=0.2)
+    desc = ops.vocab_desc(n_rows=n, width=d, n_vocab=v, io=io)
+    g = {k: x.cuda() for k, x in t.items()}
+    f = ops.vocab_ce_fwd(desc, g["h"], g["w"], g["target"])
+    a = (desc, g["h"], g["w"], g["target"], f.loss, f.lse, g["d_loss"])
+    one, other = ops.vocab_ce_bwd(*a, want_w=False), ops.vocab_ce_bwd(*a, want_h=False)
+    assert one.d_w is None and other.d_h is None
+    want = R.Reference(t["h"], t["w"], io, target=t["target"]).backward(t["d_loss"])
+    R.check("d_h", one.d_h, *want["d_h"])
+    R.check("d_w", other.d_w, *want["d_w"])
+
+
 @pytest.mark.parametrize("spread,top", [(64, 40), (5, 12), (100, 70)])
 @pytest.mark.parametrize("n", [3, 70, 300])
 def test_ids_close_together(n, spread, top):

@@ -65,6 +65,15 @@ def test_bad_descriptor(call, top, field, value):
 
 
 @pytest.mark.parametrize("call,top", CALLS)
+def test_most_values(call, top):
+    """h's values are packed eight a lane, and a launch has under 2^32 lanes."""
+    assert _status(call, _desc(n_rows=(1 << 18) + 1, width=1 << 16, n_top=top)) == ssm.SSM_ERR_SHAPE
+    for d in (_desc(n_rows=(1 << 18) + 1, width=1 << 16), _desc(n_rows=1 << 21, width=(1 << 13) + 1)):
+        assert ssm.ssm_vocab_workspace_bytes(d, 0) == 0 and ssm.ssm_vocab_workspace_bytes(d, 1) == 0
+    assert ssm.ssm_vocab_workspace_bytes(_desc(n_rows=1 << 18, width=1 << 16), 0) > 0
+
+
+@pytest.mark.parametrize("call,top", CALLS)
 def test_bad_dtype(call, top):
     for field in ("io_dtype", "dw_dtype"):
         d = _desc(n_top=top)
