@@ -461,17 +461,30 @@ __global__ __launch_bounds__(256, 2) void few_d_w(VocabFew p) {
     }
 }
 
-// How the logits are shared out: 16 nt rows, and the least kw waves a group that leave
-// every compute unit a workgroup.  (64 rows, width 2560, vocabulary 32000: 60 us with 1, 41
-// with 2, 50 with 4; vocabulary 131072: 153, 173 and 219.)
+// How the logits are shared out: 16 nt rows, and kw waves a group, more of them where the
+// last round of workgroups then leaves fewer compute units idle.  (W from memory, bf16: 64
+// rows, width 2560, vocabulary 32000: 72 us with 1, 54 with 2, 65 with 4; vocabulary 131072:
+// 152, 172 and 220; 2 rows, width 1314, vocabulary 86475: 83, 66 and 70.)
 struct FewTile {
     int nt, kw;
 };
 FewTile few_tile(const VocabRows& r) {
     FewTile f = {r.N <= 16 ? 1 : r.N <= 32 ? 2 : 4, 1};
-    // four take 192 KB of LDS for 64 rows in f32
-    const int most = r.terms == 3 && f.nt == 4 ? 2 : 4;
-    while (f.kw < most && 64 * f.kw < r.D && (int64_t)r.V * f.kw < 128 * 300) f.kw *= 2;
+    // 64 rows in f32: one workgroup a compute unit, and four waves a group take 192 KB of LDS
+    const bool large = r.terms == 3 && f.nt == 4;
+    const int64_t places = large ? 256 : 512;
+    double best = 0.0;
+    for (int kw = 1; kw <= (large ? 2 : 4); kw *= 2) {
+        // a wave takes four steps at least unless most places are empty (15 rows, width 144,
+        // vocabulary 77982: 22 us with 2, 15 with 1)
+        if (kw > 1 && (best < 0.5 ? 32 : 256) * kw > r.D) break;
+        const int64_t groups = ((int64_t)r.V * kw + 127) / 128, rounds = (groups + places - 1) / places;
+        const double used = (double)groups / (rounds * places);
+        if (used > 1.1 * best) {
+            best = used;
+            f.kw = kw;
+        }
+    }
     return f;
 }
 
