@@ -5,8 +5,9 @@ Tolerances, before any run: STEP = 2^-23 is a whole step of f32, since the
 matrix unit may cut off where it does not round.  A sum of n products is off by
 at most a step of its magnitude for each of the additions that it makes one
 after the other: one for every 8 products (the fewest that the matrix unit takes
-at once), six runs over them in f32, and a few to join parts; in f32 its products
-are also off by 2^-21 each.  From the logits' error follow those of the
+at once), six runs over them in f32, and a few to join parts (a sum's p parts have
+128 products or more each: a part's additions and p joins, n/8p + p with p <= n/128
+are no more than n/8 for p >= 2); in f32 its products are also off by 2^-21 each.  From the logits' error follow those of the
 statistics, of g (an exponential is off by as much, relative to itself, as its
 argument is), and of the products with g, which is rounded to its type first.
 Below TINY = 2^-126 f32 values may count as zero: an exponential and then g, so
