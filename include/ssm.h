@@ -533,7 +533,9 @@ int ssm_norm_residual_bwd(const ssm_norm_desc *desc, const void *dh, const void 
  * d_loss and d_lse may hold anything.  A row with a target
  * or an id of n_vocab or more has loss, lse, logq and d_h NaN, adds nothing to
  * d_W, and sets SSM_DEVERR_TARGET in *err (a device word, NULL: dropped).  Entries
- * with the same id add up; an absent entry's logq is 0.
+ * with the same id add up; an absent entry's logq is 0.  Teacher's logits may have any
+ * finite value: the lowest, as masked ones hold, has no mass beside higher ones, and
+ * where p is 0 p log p is 0.
  *
  * Products of bf16 values are exact and summed in f32; in f32 they are formed of
  * three bf16 terms a value and are off by at most 2^-21 of the product (an

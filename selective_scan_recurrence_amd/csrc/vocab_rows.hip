@@ -207,21 +207,34 @@ bool is_wide(const VocabPack& p) {
 
 // ---- the teacher's probabilities -----------------------------------------------
 
-// log2 p_k = t2_k - off, t2 = top_scale log2 e * logit: off from the row's
-// entries (their largest, and the sum of the rest against it) or from top_lse.
-__device__ __forceinline__ float top2(const VocabRows& r, int64_t e) {
-    return present(r, e) ? r.logit[e] * (r.top_scale * kLog2e) : -__builtin_inff();
+// Logits are taken off each other before anything multiplies them: masked ones hold the
+// lowest finite value, whose products with top_scale and log2 e are infinite.
+struct Teacher {
+    float base;  // top_lse, or half of the logit with the most mass: of halves every difference is finite
+    float off;   // log2 of the sum of the entries' masses against that one's
+};
+
+// log2 p of an entry
+__device__ __forceinline__ float top2(const VocabRows& r, int64_t e, const Teacher& t) {
+    if (!present(r, e)) return -__builtin_inff();
+    const float x = r.logit[e];
+    if (r.top_lse) return fmaf(r.top_scale, x, -t.base) * kLog2e;
+    return (0.5f * x - t.base) * r.top_scale * (2.0f * kLog2e) - t.off;
 }
 
 // by the 2^x lanes of a group with the same row
-__device__ __forceinline__ float top_offset(const VocabRows& r, int64_t i, int lane, int lanes) {
-    if (r.top_lse) return r.top_lse[i] * kLog2e;
+__device__ __forceinline__ Teacher teacher_of(const VocabRows& r, int64_t i, int lane, int lanes) {
+    if (r.top_lse) return {r.top_lse[i], 0.0f};
+    const float sign = r.top_scale < 0.0f ? -1.0f : 1.0f;
     float m = -__builtin_inff(), s = 0.0f;
-    for (int k = lane; k < r.K; k += lanes) m = fmaxf(m, top2(r, i * r.K + k));
+    for (int k = lane; k < r.K; k += lanes)
+        if (present(r, i * r.K + k)) m = fmaxf(m, sign * r.logit[i * r.K + k]);
     for (int d = 1; d < lanes; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-    for (int k = lane; k < r.K; k += lanes) s += fast_exp2(top2(r, i * r.K + k) - m);
+    Teacher t = {0.5f * sign * m, 0.0f};
+    for (int k = lane; k < r.K; k += lanes) s += fast_exp2(top2(r, i * r.K + k, t));
     for (int d = 1; d < lanes; d *= 2) s += __shfl_xor(s, d);
-    return m + fast_log2(s);
+    t.off = fast_log2(s);
+    return t;
 }
 
 // ---- softmax statistics ----------------------------------------------------------
@@ -293,14 +306,16 @@ __global__ __launch_bounds__(256) void join_rows(VocabJoin j) {
         if (lane == 0 && j.loss) j.loss[i] = ((m - j.slog[c]) + l) * kLn2;
         return;
     }
-    const float off = top_offset(r, i, lane & 63, LANES < 64 ? LANES : 64);
+    const Teacher t = teacher_of(r, i, lane & 63, LANES < 64 ? LANES : 64);
     float loss = 0.0f, none = 0.0f;
     for (int k = lane; k < r.K; k += LANES) {
         const int64_t e = i * r.K + k;
         const bool there = present(r, e);
-        const float q = there ? (j.slog[(int64_t)k * r.Np + c] - m) - l : 0.0f, p = top2(r, e) - off;
+        const float q = there ? (j.slog[(int64_t)k * r.Np + c] - m) - l : 0.0f, log_p = top2(r, e, t);
         if (j.logq) j.logq[e] = q * kLn2;
-        if (there) loss += fast_exp2(p) * (p - q);
+        // p log p is 0 at 0, where its logarithm may be infinite
+        const float p = fast_exp2(log_p);
+        if (p != 0.0f) loss += p * (log_p - q);
     }
     combine_lanes<LANES>(none, loss, [](float&, float& a, float, float b) { a += b; });
     if (lane == 0 && j.loss) j.loss[i] = loss * kLn2;
@@ -319,11 +334,12 @@ __device__ __forceinline__ void target_factors(const VocabCoef& f, int i, int c)
 // by a wave
 __device__ __forceinline__ void top_factors(const VocabCoef& f, int64_t i, int c, int lane) {
     const VocabRows& r = f.r;
-    const float d = f.scale * f.d_loss[i], off = top_offset(r, i, lane, 64);
+    const float d = f.scale * f.d_loss[i];
+    const Teacher t = teacher_of(r, i, lane, 64);
     float mass = 1.0f;
     if (r.top_lse) {
         mass = 0.0f;
-        for (int k = lane; k < r.K; k += 64) mass += fast_exp2(top2(r, i * r.K + k) - off);
+        for (int k = lane; k < r.K; k += 64) mass += fast_exp2(top2(r, i * r.K + k, t));
         for (int x = 1; x < 64; x *= 2) mass += __shfl_xor(mass, x);
     }
     const float a = d * mass + (f.d_lse ? f.scale * f.d_lse[i] : 0.0f);
@@ -336,7 +352,7 @@ __device__ __forceinline__ void top_factors(const VocabCoef& f, int64_t i, int c
         if (!present(r, i * r.K + k)) continue;
         float p = 0.0f;  // of every entry with this id
         for (int x = 0; x < r.K; ++x)
-            if (ids[x] == ids[k]) p += fast_exp2(top2(r, i * r.K + x) - off);
+            if (ids[x] == ids[k]) p += fast_exp2(top2(r, i * r.K + x, t));
         f.at[(int64_t)k * r.Np + c] = a * fast_exp2(f.logq[i * r.K + k] * kLog2e) - d * p;
     }
 }
