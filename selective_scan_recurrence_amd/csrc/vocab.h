@@ -8,12 +8,12 @@
 
 #include "device_common.h"
 #include "ssm.h"
+#include "vocab_plan.h"
 
 namespace ssm {
 
 constexpr int kVocabStep = 64;    // of the summed axis, a step of the products' tiles
 constexpr int kVocabTile = 256;   // what tensors in the workspace are padded to
-constexpr int kVocabSplits = 64;  // parts of a gradient's sum, at most
 
 // What the small kernels need of a call.  `rows` are the rows that count, in
 // order: row c of them is row rows[c] of h.
@@ -117,7 +117,6 @@ struct VocabGemm {
     const uint16_t *a, *b;
     int64_t a_plane, b_plane, lda, ldb;
     int m, n, k;           // rows of A and of B, and length of the sum (d_w: count's)
-    int rows;              // d_h: all rows, for a plan of both sums
     const int32_t* count;  // device: bounds n (d_w: k, in whole steps)
     int64_t Np;
     // logits
@@ -138,12 +137,6 @@ struct VocabGemm {
     bool accumulate;
 };
 int vocab_parts(const VocabGemm& g, int terms);  // partials of a forward's logits, at most m / 64 + 4
-struct VocabParts {  // of the gradients' sums
-    int d_h, d_w;
-    int most;  // d_h: at most, with rows left out
-    bool big;  // tiles
-};
-VocabParts vocab_grads_parts(const VocabGemm& d_h, const VocabGemm& d_w, int terms);
 int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream);
 int launch_vocab_logits_bwd(const VocabGemm& g, int terms, hipStream_t stream);
 // both products of the gradient (n = 0: not that one)

@@ -70,13 +70,7 @@ constexpr int64_t kPieceBytes = (int64_t)5 << 28;
 
 VocabParts parts_of(const VocabShape& s, const Plan& p, bool d_h, bool d_w) {
     if (p.few) return {vocab_few_splits(p.piece, s.D), 1, 1, false};
-    VocabGemm h = {}, w = {};
-    h.m = w.m = s.D;
-    h.n = d_h ? s.N : 0;
-    h.rows = s.N;
-    h.k = (int)p.piece;
-    w.n = d_w ? (int)p.piece : 0;
-    return vocab_grads_parts(h, w, s.terms);
+    return vocab_grads_parts(s.D, s.N, p.piece, d_h, d_w, s.terms);
 }
 
 Plan plan_of(const VocabShape& s, bool backward, bool packed) {
@@ -376,7 +370,7 @@ int backward(const Call& c, const float* logq, const float* loss, const float* l
         VocabGemm gh = {};
         gh.a = c.at<uint16_t>(p.wt); gh.a_plane = s.D * p.ld; gh.lda = p.ld;
         gh.b = g; gh.b_plane = p.Np * p.ld; gh.ldb = p.ld;
-        gh.m = s.D; gh.n = d_h ? s.N : 0; gh.rows = s.N; gh.k = (int)round_up(n, kVocabStep);
+        gh.m = s.D; gh.n = d_h ? s.N : 0; gh.k = (int)round_up(n, kVocabStep);
         gh.count = c.r.count; gh.Np = p.Np;
         gh.out = c.at<float>(p.acc); gh.ld_out = p.Kd; gh.split = split_of(c);
         gh.accumulate = x > 0;

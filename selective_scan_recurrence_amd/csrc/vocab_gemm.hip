@@ -536,8 +536,6 @@ __global__ __launch_bounds__(256, T::TM > 4 ? 1 : 2) void grads(VocabGemm h, Voc
     }
 }
 
-int64_t tiles(int64_t m, int64_t n, int tile) { return (m + tile - 1) / tile * ((n + tile - 1) / tile); }
-
 // Whether 256 x 256 tiles, one a compute unit, take less time than 128 x 128 tiles, two a
 // compute unit.  A round of tiles takes `steps` steps of k, 1.48 us each (a big tile's)
 // or 0.88, and its results: `big` or `small` us, measured with sums of 5 and of 40
@@ -546,7 +544,7 @@ int64_t tiles(int64_t m, int64_t n, int tile) { return (m + tile - 1) / tile * (
 struct Results {
     double big, small;
 };
-constexpr Results kStatistics = {5.0, 2.0}, kBothOrders = {13.0, 8.0}, kSums = {10.0, 6.0};
+constexpr Results kStatistics = {5.0, 2.0}, kBothOrders = {13.0, 8.0};
 
 bool big_tiles(int64_t big, int64_t small, double steps, Results r) {
     return ((big + 255) / 256) * (1.48 * steps + r.big) <= ((small + 511) / 512) * (0.88 * steps + r.small);
@@ -554,37 +552,14 @@ bool big_tiles(int64_t big, int64_t small, double steps, Results r) {
 
 bool big_logits(const VocabGemm& g, int terms, Results r) {
     const double steps = (terms == 3 ? 6 : 1) * (g.k / kVocabStep);
-    return big_tiles(tiles(g.m, g.n, 256), tiles(g.m, g.n, 128), steps, {r.big * terms, r.small * terms});
-}
-
-// Time until the last of nh workgroups of `a` us, and nw of `b` us after them in line,
-// leave `places`.
-double line_up(int64_t places, int64_t nh, double a, int64_t nw, double b) {
-    const int64_t rounds = nh / places, late = nh % places, early = places - late;
-    const double t0 = rounds * a, t1 = late ? t0 + a : t0;
-    double t = t1;
-    if (nw > 0) {
-        // from the time that a perfect fit would take to the first with room for all
-        const double least = (nw * b + early * t0 + late * t1) / places;
-        int64_t j = (int64_t)((least - t0) / b);
-        for (;; ++j) {
-            const double e = t0 + j * b + 1e-6;
-            const int64_t then = e > t1 ? (int64_t)((e - t1) / b) : 0;
-            t = e;
-            if (early * j + late * then >= nw) break;
-            // the late places' next end, when it comes before the early ones'
-            t = t1 + (then + 1) * b;
-            if (t < e + b && early * j + late * (then + 1) >= nw) break;
-        }
-    }
-    return t > t1 ? t : t1;
+    return big_tiles(vocab_tiles(g.m, g.n, 256), vocab_tiles(g.m, g.n, 128), steps, {r.big * terms, r.small * terms});
 }
 
 int launched() { return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 
 template <class T>
 int launch_fwd(const VocabGemm& g, int terms, hipStream_t stream) {
-    const unsigned grid = (unsigned)on_xcds(tiles(g.m, g.n, T::BM));
+    const unsigned grid = (unsigned)on_xcds(vocab_tiles(g.m, g.n, T::BM));
     if (terms == 1) logits_fwd<T, 1><<<grid, 256, 0, stream>>>(g);
     else logits_fwd<T, 6><<<grid, 256, 0, stream>>>(g);
     return launched();
@@ -592,7 +567,7 @@ int launch_fwd(const VocabGemm& g, int terms, hipStream_t stream) {
 
 template <class T>
 int launch_bwd(const VocabGemm& g, int terms, hipStream_t stream) {
-    const unsigned grid = (unsigned)on_xcds(tiles(g.m, g.n, T::BM));
+    const unsigned grid = (unsigned)on_xcds(vocab_tiles(g.m, g.n, T::BM));
     if (terms == 3) logits_bwd<T, 6, 3><<<grid, 256, 0, stream>>>(g);
     else logits_bwd<T, 1, 1><<<grid, 256, 0, stream>>>(g);
     return launched();
@@ -600,7 +575,7 @@ int launch_bwd(const VocabGemm& g, int terms, hipStream_t stream) {
 
 template <class T>
 unsigned grads_grid(const VocabGemm& h, const VocabGemm& w) {
-    return (unsigned)on_xcds(tiles(h.m, h.n, T::BM) * h.split.parts) + (unsigned)on_xcds(tiles(w.m, w.n, T::BM) * w.splits);
+    return (unsigned)on_xcds(vocab_tiles(h.m, h.n, T::BM) * h.split.parts) + (unsigned)on_xcds(vocab_tiles(w.m, w.n, T::BM) * w.splits);
 }
 
 template <class T>
@@ -614,49 +589,6 @@ int launch_grads(const VocabGemm& h, const VocabGemm& w, int terms, hipStream_t 
 
 int vocab_parts(const VocabGemm& g, int terms) {
     return big_logits(g, terms, kStatistics) ? (g.m + 255) / 256 * 2 : (g.m + 127) / 128 * 2;
-}
-
-// A launch of both sums: tiles, and parts of either sum, so that a long sum for few tiles
-// (d_h of few rows, d_w of a small vocabulary) does not outlast all else, nor a last round
-// of tiles leave most compute units idle.  f32, 1023 rows, width 771, vocabulary 10007: 204
-// us, with a share of d_h for every compute unit 277.
-VocabParts vocab_grads_parts(const VocabGemm& h, const VocabGemm& w, int terms) {
-    VocabParts best = {1, 1, 1, true};
-    double least = 1e30;
-    const int64_t steps_h = (h.k + 63) / 64, steps_w = (h.rows + 63) / 64, runs = terms == 3 ? 6 : 1;
-    const int64_t most = steps_h / 4 < 1 ? 1 : steps_h / 4 < kVocabSplits ? steps_h / 4 : kVocabSplits;
-    for (const bool big : {true, false}) {
-        const int tile = big ? 256 : 128;
-        const int64_t th = tiles(h.m, h.n, tile), tw = tiles(w.m, w.n, tile), places = big ? 256 : 512;
-        // a workgroup's fair share of steps
-        double share = (double)(th * steps_h + tw * steps_w) / places;
-        if (share < 8) share = 8;
-        const double even = th > 0 ? steps_h / share : 1;
-        for (int x = 0; x < 8; ++x) {
-            VocabParts p = {(int)(even * (0.5 + 0.25 * x) + 0.5), 1, (int)most, big};
-            if (p.d_h < 1) p.d_h = 1;
-            if (p.d_h > most) break;
-            for (int y = 0; y < 2; ++y) {
-                if (y == 1) {
-                    p.d_w = tw > 0 ? (int)(steps_w / share) : 1;
-                    if (p.d_w <= 1) break;
-                    if (p.d_w > kVocabSplits) p.d_w = kVocabSplits;
-                }
-                const int64_t nh = th * p.d_h, nw = tw * p.d_w;
-                // alone on its compute unit a small tile's step takes 0.54 us
-                const double step = big ? 1.48 : nh + nw <= 256 ? 0.54 : 0.88, rest = big ? kSums.big : kSums.small;
-                const double a = (step * runs * steps_h) / p.d_h + rest, b = (step * runs * steps_w) / p.d_w + rest;
-                // parts of d_w take a kernel more; a part's read and write, at 4.5 TB/s
-                const double kept = (p.d_h - 1) * (double)h.m * h.n + (p.d_w > 1 ? p.d_w * (double)w.m * w.n : 0.0);
-                const double t = line_up(places, nh, a, nw, b) + (p.d_w > 1 ? 4 : 0) + 8e-6 / 4.5 * kept;
-                if (t < least) {
-                    least = t;
-                    best = p;
-                }
-            }
-        }
-    }
-    return best;
 }
 
 int launch_vocab_logits_fwd(const VocabGemm& g, int terms, hipStream_t stream) {
