@@ -139,9 +139,7 @@ def load():
         lib.ssm_norm_residual_fwd.argtypes = [N] + [P] * 13
         lib.ssm_norm_residual_bwd.argtypes = [N] + [P] * 17 + [SZ, P]
         for fn in ("ssm_ckpt8_pack", "ssm_ckpt8_unpack", "ssm_ckpt8_wgrad", "ssm_norm_gated_fwd",
-                   "ssm_norm_gated_bwd", "ssm_norm_residual_fwd", "ssm_norm_residual_bwd",
-           "ssm_vocab_workspace_bytes", "ssm_vocab_ce_fwd", "ssm_vocab_ce_bwd", "ssm_vocab_kd_fwd",
-           "ssm_vocab_kd_bwd"):
+                   "ssm_norm_gated_bwd", "ssm_norm_residual_fwd", "ssm_norm_residual_bwd"):
             getattr(lib, fn).restype = ctypes.c_int
         V = ctypes.POINTER(SsmVocabDesc)
         lib.ssm_vocab_workspace_bytes.argtypes = [V, ctypes.c_int]

@@ -20,6 +20,8 @@ int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 // rows, width 2560: 2070 us, without 2140).
 int64_t off_channels(int64_t v) { return v % 2048 ? v : v + 256; }
 
+constexpr int kMostVocab = 1 << 24;
+
 struct VocabShape {
     int N, D, V, K, top;
     int g_terms;  // bf16 terms of g
@@ -34,7 +36,7 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
     if (!known(d->io_dtype) || !known(d->dw_dtype)) return SSM_ERR_DTYPE;
     if (d->reserved != 0 || (d->flags & ~(uint32_t)SSM_VOCAB_ACCUMULATE)) return SSM_ERR_SHAPE;
     if (d->n_rows < 0 || d->n_rows > 1 << 21 || d->width < 1 || d->width > 1 << 16 || d->n_vocab < 1 ||
-        d->n_vocab > 1 << 24 || d->n_top < 0 || d->n_top > 1024)
+        d->n_vocab > kMostVocab || d->n_top < 0 || d->n_top > 1024)
         return SSM_ERR_SHAPE;
     // a launch has under 2^32 lanes, and h is packed 8 values a lane
     if (d->n_rows * d->width > (int64_t)1 << 34) return SSM_ERR_SHAPE;
@@ -253,6 +255,8 @@ VocabPack placed_h(const Call& c, size_t to, int64_t plane) {
     return p;
 }
 
+// a piece takes the whole vocabulary
+static_assert(((int64_t)kMostVocab * kVocabFew / 4) <= kPieceBytes, "");
 int forward_few(const Call& c, float* loss, float* lse, float* logq, uint32_t* err) {
     const Plan& p = c.p;
     VocabFew f = few_of(c);
@@ -266,14 +270,9 @@ int forward_few(const Call& c, float* loss, float* lse, float* logq, uint32_t* e
         b.pack_h = &packed;
         RUN(launch_vocab_begin(b, c.s.io, c.stream));
     }
-    for (int x = 0; x < p.pieces; ++x) {
-        f.v0 = (int)(x * p.piece);
-        const int n = c.s.V - f.v0 < f.P ? c.s.V - f.v0 : f.P;
-        RUN(launch_vocab_few_logits(f, false, c.stream));
-        RUN(launch_vocab_join({f.r, f.part, (n + tile - 1) / tile, c.at<float2>(p.state), x == 0, x == p.pieces - 1,
-                               f.slog, loss, lse, logq, err}, c.stream));
-    }
-    return SSM_OK;
+    RUN(launch_vocab_few_logits(f, false, c.stream));
+    return launch_vocab_join({f.r, f.part, (c.s.V + tile - 1) / tile, nullptr, true, true, f.slog, loss, lse, logq, err},
+                             c.stream);
 }
 
 // the product for d_w of a piece [v0, v0 + n), or of its sum's parts

@@ -72,25 +72,20 @@ struct Raw {
     }
 };
 
-// Eight of the same values of h: as they lie, or (f32) of its terms in the workspace,
-// which every workgroup would have to form again.
-template <typename E>
-__device__ __forceinline__ void load_h(const VocabFew& p, int n, int k, u32x4 (&f)[kTerms<E>]) {
-    if constexpr (kTerms<E> == 1) {
-        const bf16_t* row = static_cast<const bf16_t*>(p.h) + (int64_t)n * p.ld_h;
-        if (k + 8 <= p.r.D) {
-            __builtin_memcpy(&f[0], row + k, 16);
-        } else {
-            bf16_t v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = k + e < p.r.D ? row[k + e] : 0;
-            __builtin_memcpy(&f[0], v, 16);
-        }
+// Eight of the same values of h as they lie (f32 reads its terms from the workspace, which
+// every workgroup would have to form again).
+__device__ __forceinline__ u32x4 load_h(const VocabFew& p, int n, int k) {
+    const bf16_t* row = static_cast<const bf16_t*>(p.h) + (int64_t)n * p.ld_h;
+    u32x4 f;
+    if (k + 8 <= p.r.D) {
+        __builtin_memcpy(&f, row + k, 16);
     } else {
-        const int64_t Kd = (p.r.D + 63) / 64 * 64;
+        bf16_t v[8];
 #pragma unroll
-        for (int t = 0; t < 3; ++t) f[t] = *reinterpret_cast<const u32x4*>(p.hp + (t * p.r.Np + n) * Kd + k);
+        for (int e = 0; e < 8; ++e) v[e] = k + e < p.r.D ? row[k + e] : 0;
+        __builtin_memcpy(&f, v, 16);
     }
+    return f;
 }
 
 // ---- the logits -----------------------------------------------------------------
@@ -135,12 +130,7 @@ __device__ __forceinline__ void finish(const VocabFew& p, float (&red)[KW][16 * 
             for (int x = 0; x < VPT; ++x) s += fast_exp2(s2[x] - m);
 #pragma unroll
             for (int d = 1; d < LPT; d *= 2) s += __shfl_xor(s, d);
-            const float2 own = make_float2(none ? -0x1p127f : m, s);
-            if constexpr (kGroups > 1) {
-                if (l == 0) joined[group][n] = own;
-            } else if (l == 0) {
-                p.part[(int64_t)blockIdx.x * r.Np + n] = own;
-            }
+            if (l == 0) joined[group][n] = make_float2(none ? -0x1p127f : m, s);
         } else {
             const bool out = n >= r.N || r.pos[n] < 0;
             const float a = out ? 0.0f : p.coef[n], lse2 = out ? 0.0f : p.lse2[n];
@@ -161,7 +151,7 @@ __device__ __forceinline__ void finish(const VocabFew& p, float (&red)[KW][16 * 
                 else if (r.pos[n] >= 0) red[0][n][at] = p.at[(int64_t)y * r.Np + n];
             }
     }
-    if constexpr (!BWD && kGroups > 1) {
+    if constexpr (!BWD) {
         __syncthreads();
         if (threadIdx.x < N) {
             float2 all = joined[0][threadIdx.x];
@@ -231,9 +221,7 @@ __global__ __launch_bounds__(512, kTerms<E> == 1 ? 4 : 2) void few_logits(VocabF
             const int k = 64 * (s * KW + at / (8 * N * T)) + 8 * (at % 8);
             if (kPieces % 512 && at >= kPieces) continue;
             if constexpr (T == 1) {
-                u32x4 v[1];
-                load_h<E>(p, n, k, v);
-                h[x] = v[0];
+                h[x] = load_h(p, n, k);
             } else {
                 const int64_t Kd = (r.D + 63) / 64 * 64;
                 h[x] = k < Kd ? *reinterpret_cast<const u32x4*>(p.hp + (t * r.Np + n) * Kd + k) : u32x4{0, 0, 0, 0};

@@ -269,7 +269,7 @@ __global__ __launch_bounds__(256) void join_rows(VocabJoin j) {
     } else {
         const int state = row_state_by<(LANES < 64 ? LANES : 64)>(r, (int)i, lane & 63);
         c = state < 0 ? state : (int)i;
-        if (state == kRowBad && j.err && j.last && lane == 0) atomicOr(j.err, (uint32_t)SSM_DEVERR_TARGET);
+        if (state == kRowBad && j.err && lane == 0) atomicOr(j.err, (uint32_t)SSM_DEVERR_TARGET);
     }
     if (c < 0) {
         if (!j.last) return;
