@@ -539,7 +539,8 @@ int ssm_norm_residual_bwd(const ssm_norm_desc *desc, const void *dh, const void 
  *
  * Products of bf16 values are exact and summed in f32; in f32 they are formed of
  * three bf16 terms a value and are off by at most 2^-21 of the product (an
- * infinity may come out as NaN; parts below 2^-126 may count as zero).  g enters
+ * infinity may come out as NaN; parts below 2^-126 may count as zero); a logit of
+ * 2^127 or more may count as infinite.  g enters
  * its two products in such terms: three in f32; with bf16 io one, g rounded to bf16
  * as the outputs are, also when d_W is f32, or, up to 64 rows, two (2^-17 of g is
  * left).  Sums have a fixed order: results repeat bitwise. */
@@ -552,7 +553,7 @@ typedef struct ssm_vocab_desc {
     int64_t ld_w;       /* elements (0: width), at most 2^22                     */
     int32_t io_dtype;   /* ssm_dtype of h, w and d_h                             */
     int32_t dw_dtype;   /* ssm_dtype of d_w: io's, or f32                        */
-    float scale;        /* of the logits (1 / temperature); finite               */
+    float scale;        /* of the logits (1 / temperature); |scale| below 2^127  */
     float top_scale;    /* of the teacher's logits; finite                       */
     uint32_t flags;     /* SSM_VOCAB_ACCUMULATE                                  */
     uint32_t reserved;  /* must be 0                                             */

@@ -46,7 +46,8 @@ int check(const ssm_vocab_desc* d, VocabShape* out) {
     s.ld_h = d->ld_h ? d->ld_h : s.D;
     s.ld_w = d->ld_w ? d->ld_w : s.D;
     if (s.ld_h < s.D || s.ld_w < s.D || s.ld_h > 1 << 22 || s.ld_w > 1 << 22) return SSM_ERR_SHAPE;
-    if (!isfinite(d->scale) || !isfinite(d->top_scale)) return SSM_ERR_SHAPE;
+    // the logits carry scale log2 e
+    if (!isfinite(d->scale * kLog2e) || !isfinite(d->top_scale)) return SSM_ERR_SHAPE;
     s.io = d->io_dtype; s.dw = d->dw_dtype; s.terms = s.io == SSM_BF16 ? 1 : 3;
     s.g_terms = s.terms == 3 ? 3 : s.N <= kVocabFew ? 2 : 1;
     if (s.io == SSM_F32 && s.dw == SSM_BF16) return SSM_ERR_UNSUPPORTED;

@@ -145,6 +145,15 @@ def test_nothing_to_do():
     _kd_bwd(_desc(n_top=2), d_h=None, d_w=None)
 
 
+@pytest.mark.parametrize("call,top", CALLS)
+@pytest.mark.parametrize("scale", [2.4e38, -3.0e38])
+def test_scale_times_log2_e_is_finite(call, top, scale):
+    """The kernels' logits are times log2 e; a teacher's scale is not."""
+    assert _status(call, _desc(n_top=top, scale=scale)) == ssm.SSM_ERR_SHAPE
+    assert ssm.ssm_vocab_workspace_bytes(_desc(n_top=top, scale=scale), 1) == 0
+    assert ssm.ssm_vocab_workspace_bytes(_desc(n_top=top, scale=1.7e38, top_scale=scale), 1) > 0
+
+
 def test_strides_default_to_dense():
     d = ssm.SsmVocabDesc(4, 96, 300, 0, 0, 0, ssm.SSM_BF16, ssm.SSM_F32, 1.0, 1.0, 0, 0)
     assert ssm.ssm_vocab_workspace_bytes(d, 1) == ssm.ssm_vocab_workspace_bytes(_desc(), 1)
