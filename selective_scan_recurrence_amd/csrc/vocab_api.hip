@@ -24,7 +24,10 @@ constexpr int kMostVocab = 1 << 24;
 
 struct VocabShape {
     int N, D, V, K, top;
-    int g_terms;  // bf16 terms of g
+    // Bf16 terms of g.  One with bf16 tensors, as their results are rounded: a second would
+    // double the 4.2 ms that both products take in a step's 8.9 (16384 rows, width 2560,
+    // vocabulary 32768).  Up to 64 rows, where W's bytes bound the products, two.
+    int g_terms;
     int64_t ld_h, ld_w;
     int io, dw, terms;
     float scale, top_scale;

@@ -2,8 +2,8 @@
 // bound by W's bytes, so W goes from memory to registers as it lies, once for the
 // logits and once for d_h, in its own type and alignment, and nothing of it is
 // laid out again.  With so few rows a gradient may hang on a single rounded value of
-// g, and the products wait for W's bytes: g has a second bf16 term, which takes its
-// rounding (2^-9 of a value) out of the result.
+// g, and the products wait for W's bytes: g has a second bf16 term, which takes the
+// first's rounding (up to 2^-8 of a value) out of the result but for 2^-17.
 #include <type_traits>
 
 #include "vocab.h"

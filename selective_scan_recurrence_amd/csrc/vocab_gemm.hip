@@ -6,8 +6,9 @@
 //            orders, since one product sums over the vocabulary and one over rows
 //   d_h:     A = W turned (m: width),  B = g (n: rows)
 //   d_w:     A = h turned (m: width),  B = g turned (n: vocabulary)
-// An f32 value is three bf16 terms, and a product the six of its nine partial
-// products that reach 2^-24 of it, the small ones first: six runs over k.
+// An f32 value is three bf16 terms, and a product the six largest of its nine partial
+// products (the other three reach 2^-21 of it together), the small ones first: six runs
+// over k.
 //
 // A workgroup of 2 x 2 waves owns 256 x 256 (or 128 x 128) of out and walks k in
 // steps of 64: 128-byte rows go from memory to LDS past the registers, into one of
